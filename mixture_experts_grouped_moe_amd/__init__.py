@@ -33,6 +33,7 @@ MOE_BF16, MOE_FP32, MOE_E4M3, MOE_E2M1X2, MOE_E8M0, MOE_I32 = 1, 2, 3, 4, 5, 6
 MOE_LAYOUT_ROWS, MOE_LAYOUT_KBLOCK = 0, 1
 _W_DTYPES = {"bf16": MOE_BF16, "e4m3": MOE_E4M3, "e2m1x2": MOE_E2M1X2}
 _EPILOGUES = {"none": 0, "swiglu": 1, "relu2": 2}
+_ACTS = {"swiglu": 1, "relu2": 2}
 
 
 class MoeError(RuntimeError):
@@ -652,3 +653,10 @@ def moe_relu2_layer(x, topk_ids, topk_w, w1, w2, b1=None, b2=None, num_tokens=No
     h = moe_grouped_gemm(x, w1, "bf16", routing, T, k, E, a_row_div=k, bias=b1, epilogue="relu2", stream=stream)
     c2 = moe_grouped_gemm(h, w2, "bf16", routing, T, k, E, a_row_div=1, bias=b2, stream=stream)
     return moe_combine(c2, topk_w, k, num_tokens=T, stream=stream)
+
+
+# the training entry points (moe_train.h) bind to the library loaded above
+from . import training  # noqa: E402
+from .training import *  # noqa: E402,F401,F403
+
+__all__ += training.__all__

@@ -12,16 +12,16 @@
 #include "moe.h"
 
 #include "decode_layer.h"
+#include "host.h"
 #include "params.h"
 
 namespace {
-
 constexpr int64_t kDecodeMaxTokens = 32;
-constexpr int32_t kAlignMaxExperts = 1024;
-
 thread_local std::string g_last_error;
+}  // namespace
 
-moe_status fail(moe_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace moe {
+
 moe_status fail(moe_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -58,6 +58,16 @@ moe_status hip_status(hipError_t err, const char* what) {
   if (err != hipSuccess) return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(err));
   return ok();
 }
+
+}  // namespace moe
+
+namespace {
+
+using moe::check_device;
+using moe::fail;
+using moe::hip_status;
+using moe::kAlignMaxExperts;
+using moe::ok;
 
 int64_t bucket(int64_t m) {
   if (m < 0) return -1;

@@ -61,6 +61,54 @@ struct WgradParams {
   uint32_t topk_magic;  // slot s's token row s / top_k = (s * topk_magic) >> topk_shift
   int32_t topk_shift;
   float* dw;
+  // x as MXFP8 (wgrad_kernel<true>): codes through x / x_ld (bytes), scales here
+  const uint8_t* xs;
+  int64_t xs_ld;
+};
+
+// The router (route.hip): forward and backward.
+struct RouteParams {
+  const void* logits;  // fp32 or bf16 rows
+  int64_t ld;
+  const uint8_t* mask; // or null
+  int64_t T;
+  int32_t E, k;
+  int32_t sigmoid, renorm, stats;
+  float scale;
+  int32_t* ids;
+  float* w;
+  int32_t* counts;
+  int32_t* num_routed;
+  float* prob_sum;
+  float* losses;
+  // partial statistics in the workspace, one row per workgroup
+  float* part_p;
+  int32_t* part_c;
+  float* part_z;
+  int32_t* part_n;
+  // backward
+  const float* dw;
+  const float* dlosses;  // or null
+  void* dlogits;
+  int64_t dld;
+};
+
+// The activation with an MXFP8 checkpoint (act.hip): forward and backward.
+struct ActParams {
+  const uint16_t* pre;
+  int64_t pre_ld;
+  int64_t rows;
+  int32_t n;
+  uint16_t* h;  // backward: or null
+  int64_t h_ld;
+  uint8_t* q;
+  int64_t q_ld;
+  uint8_t* s;
+  int64_t s_ld;
+  const uint16_t* dh;
+  int64_t dh_ld;
+  uint16_t* dpre;
+  int64_t dpre_ld;
 };
 
 hipError_t launch_align(const int32_t* ids, int32_t S, int32_t E, int32_t B, int32_t* sorted_ids,
@@ -76,7 +124,19 @@ hipError_t launch_gemm_f8(const GemmParams& p, bool swiglu, bool bias, hipStream
 hipError_t launch_gemm_per_token(const GemmParams& p, bool bias, hipStream_t stream);
 hipError_t launch_combine(const uint16_t* c, int64_t c_ld, const float* w, int64_t T, int32_t top_k,
                           int64_t N, uint16_t* y, int64_t y_ld, hipStream_t stream);
+// the same over the slots whose id lies in [0, E)
+hipError_t launch_combine_routed(const uint16_t* c, int64_t c_ld, const float* w, const int32_t* ids, int64_t T,
+                                 int32_t top_k, int32_t E, int64_t N, uint16_t* y, int64_t y_ld, hipStream_t stream);
+hipError_t launch_combine_backward(const uint16_t* dy, int64_t dy_ld, const uint16_t* c, int64_t c_ld, const float* w,
+                                   const int32_t* ids, int64_t T, int32_t top_k, int32_t E, int64_t N, uint16_t* dc,
+                                   int64_t dc_ld, float* dw, hipStream_t stream);
+int64_t route_workspace_bytes(int64_t T, int32_t E);
+hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t stream);
+hipError_t launch_route_backward(const RouteParams& p, bool bf16, hipStream_t stream);
+hipError_t launch_act(const ActParams& p, bool swiglu, hipStream_t stream);
+hipError_t launch_act_backward(const ActParams& p, bool swiglu, hipStream_t stream);
 hipError_t launch_wgrad(const WgradParams& p, hipStream_t stream);
+hipError_t launch_wgrad_mxfp8(const WgradParams& p, hipStream_t stream);
 // Copy one block of rows-layout codes/scales into the K-block layout.
 hipError_t launch_pack(const uint8_t* w, int64_t w_stride_e, int64_t w_ld, const uint8_t* ws,
                        int64_t ws_stride_e, int64_t ws_ld, int32_t E, int32_t N, int32_t K, int32_t row_bytes,

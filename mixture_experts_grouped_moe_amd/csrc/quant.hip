@@ -25,25 +25,11 @@
 // its single rounding, which is the definition's.
 #include "common.h"
 #include "params.h"
+#include "quant_util.h"
 
 namespace moe {
 
 constexpr int kQuantThreads = 256;
-
-typedef short q_v2s __attribute__((ext_vector_type(2)));
-typedef __bf16 q_v2bf __attribute__((ext_vector_type(2)));
-typedef unsigned short q_v2u16 __attribute__((ext_vector_type(2)));
-
-// Two bf16 elements (bits of one dword) -> the dword with their magnitudes
-// clamped to `lim2` (448 * 2^X in both halves) and the sign of a zero
-// element cleared. Each half's magnitude plus 0x7FFF has bit 15 set exactly
-// when the magnitude is non-zero, and never carries into the other half.
-__device__ __forceinline__ uint32_t clamp_pair(uint32_t d, uint32_t lim2) {
-  const uint32_t mag = d & 0x7FFF7FFFu;
-  const uint32_t sgn = d & 0x80008000u & (mag + 0x7FFF7FFFu);
-  const q_v2u16 m = __builtin_elementwise_min(__builtin_bit_cast(q_v2u16, mag), __builtin_bit_cast(q_v2u16, lim2));
-  return __builtin_bit_cast(uint32_t, m) | sgn;
-}
 
 __global__ __launch_bounds__(kQuantThreads) void quant_mxfp8_kernel(
     const uint16_t* __restrict__ x, int64_t x_ld, int64_t rows, int32_t kb, uint8_t* __restrict__ q,
@@ -57,48 +43,12 @@ __global__ __launch_bounds__(kQuantThreads) void quant_mxfp8_kernel(
     u32x4_t v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = src[j];
-    // block maximum of |v| on the bf16 bits (order of magnitudes = order of bits)
-    uint32_t amax = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        amax = max(amax, v[j][w] & 0x7FFFu);
-        amax = max(amax, (v[j][w] >> 16) & 0x7FFFu);
-      }
+    u32x4_t out[2];
+    const uint32_t byte = mx_quantize_block(v, out);
     u32x4_t* dst = reinterpret_cast<u32x4_t*>(q + row * q_ld + (int64_t)b * 32);
-    if (amax >= 0x7F80u) {  // exponent field all ones: a NaN or an infinity in the block
-      const uint32_t nan4 = 0x7F7F7F7Fu;
-      dst[0] = u32x4_t{nan4, nan4, nan4, nan4};
-      dst[1] = u32x4_t{nan4, nan4, nan4, nan4};
-      s[row * s_ld + b] = (uint8_t)0xFF;
-      continue;
-    }
-    // floor(log2(max)) from the exponent field; a zero or subnormal maximum
-    // (below 2^-126) gives X below -127, so the clamp decides
-    const int e = (int)(amax >> 7);
-    const int X = e == 0 ? -127 : min(max(e - 127 - 8, -127), 127);
-    // the conversion's scale operand: E8M0 byte X + 127 in the exponent
-    // field (byte 0 is 2^-127); X <= 119 for finite inputs, so 448 * 2^X
-    // (bf16 exponent 135 + X, mantissa 0x60) is a finite bf16
-    const float scale = __uint_as_float((uint32_t)(X + 127) << 23);
-    const uint32_t lim = ((uint32_t)(135 + X) << 7) | 0x60u;
-    const uint32_t lim2 = lim | (lim << 16);
-    uint32_t out[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int w = 0; w < 4; w += 2) {
-        // elements 8j + 2w .. 8j + 2w + 3 -> the four bytes of dword 2j + w/2
-        const uint32_t lo = clamp_pair(v[j][w], lim2), hi = clamp_pair(v[j][w + 1], lim2);
-        q_v2s r = {0, 0};
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(q_v2bf, lo), scale, false);
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(q_v2bf, hi), scale, true);
-        out[2 * j + w / 2] = __builtin_bit_cast(uint32_t, r);
-      }
-    dst[0] = u32x4_t{out[0], out[1], out[2], out[3]};
-    dst[1] = u32x4_t{out[4], out[5], out[6], out[7]};
-    s[row * s_ld + b] = (uint8_t)(X + 127);
+    dst[0] = out[0];
+    dst[1] = out[1];
+    s[row * s_ld + b] = (uint8_t)byte;
   }
 }
 

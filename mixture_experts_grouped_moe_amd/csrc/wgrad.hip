@@ -77,6 +77,8 @@ constexpr int kWgXLoads = kWgXUnitB / 1024 / kWgWaves;  //   + 2 x (2 rows each)
 constexpr int kWgStores = 8 * 4;             // 16-byte stores per lane per tile
 constexpr int kWgPerCU = 1;                  // resident workgroups per CU
 constexpr int kWgMaxExperts = 1024;
+constexpr int kWgRawUnitB = kWgUM * kWgTK;   // 8 KB: a unit of x as E4M3 codes
+constexpr int kWgRawPairB = 2 * (kWgRawUnitB + kWgThreads * 4);  // a pair of units: codes, one scale dword per lane
 constexpr int kWgGroupN = 8;                 // N tiles per group of the tile order
 constexpr uint32_t kWgOOB = 0x80000000u;     // buffer offset past x, grad and one expert's dW (each below 2 GB)
 constexpr int kWgStoreNT = 2;                // cache-policy bits of the dW stores: non-temporal
@@ -145,9 +147,25 @@ struct WgTile {
   int e, n0, k0, b0, b1;
 };
 
+// One byte per lane from `rsrc` at `voff` into LDS, zero-extended to the dword
+// at lds_base + 4 * lane.
+__device__ __forceinline__ void wg_dma_byte(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_ubyte %0, %2, 0 offen lds"
+               :: "v"(voff), "s"(__builtin_amdgcn_readfirstlane(lds_base)), "s"(rsrc) : "m0");
+}
+
+// MX: x comes as E4M3 codes with E8M0 scales. Its pieces (half the bytes) go
+// one pair of units further ahead into an LDS area of their own by the same
+// DMA; before a pair's products, each wave decodes the pieces of the next
+// pair that it loaded itself (so no barrier is needed between) to bf16, which
+// is exact, into the stage where the products will read them. Every element
+// is decoded once per tile; decoding at the operand reads would repeat it in
+// the four waves that share a column.
+template <bool MX>
 __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams p) {
   // four stages of [grad unit | x unit], slot-major
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kWgStages][kWgStageB];
+  __shared__ __attribute__((aligned(1024))) uint8_t raw[MX ? kWgRawPairB : 16];
   __shared__ int32_t s_start[kWgMaxExperts + 1];  // first block of expert e (s_start[E] = end)
 
   const int tid = threadIdx.x;
@@ -199,14 +217,23 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
     return t;
   };
 
-  const __amdgpu_buffer_rsrc_t g_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)p.grad, 0, (int)(uint32_t)((int64_t)p.S * p.grad_ld * 2), 0x00020000);
-  const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)p.x, 0, (int)(uint32_t)((int64_t)(p.S / p.top_k) * p.x_ld * 2), 0x00020000);
+  // (the buffers end with their last row's last element: a view's last row
+  // may end with its allocation)
+  const int64_t T = p.S / p.top_k;
+  constexpr int XB = MX ? 1 : 2;  // bytes of an element of x
+  auto span = [](int64_t rows, int64_t ld, int64_t width, int bytes) {
+    return (int)(uint32_t)(rows > 0 ? ((rows - 1) * ld + width) * bytes : 0);
+  };
+  const __amdgpu_buffer_rsrc_t g_rsrc =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.grad, 0, span(p.S, p.grad_ld, p.N, 2), 0x00020000);
+  const __amdgpu_buffer_rsrc_t x_rsrc =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, span(T, p.x_ld, p.K, XB), 0x00020000);
+  const __amdgpu_buffer_rsrc_t xs_rsrc =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.xs, 0, MX ? span(T, p.xs_ld, p.K / 32, 1) : 0, 0x00020000);
   const __amdgpu_buffer_rsrc_t sorted_rsrc = __builtin_amdgcn_make_buffer_rsrc(
       (void*)p.sorted, 0, (int)(uint32_t)((int64_t)p.max_blocks * kWgBM * 4), 0x00020000);
   const uint32_t lds_base = (uint32_t)(uintptr_t)(wg_lds_u8_t*)&lds[0][0];
-  const uint32_t g_row = (uint32_t)(p.grad_ld * 2), x_row = (uint32_t)(p.x_ld * 2);
+  const uint32_t g_row = (uint32_t)(p.grad_ld * 2), x_row = (uint32_t)(p.x_ld * XB);
 
   // ---- loader: walks the same tiles' units one pair ahead of the
   //      computation. Unit u of a tile is slots [32u, 32u + 32) of its block
@@ -253,40 +280,112 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
   ld_ids_pair(ids, ids_b);
   wg_wait_barrier<0>(ids, ids_b);
 
-  auto issue_unit = [&](int stage, const wg_i32x4_t& uid) {
-    // scalar row offsets of the wave's 8 slots within the tile's column
-    // range (a PAD slot s = S lands at or past the end of both buffers)
-    // (past the last tile the ids are 0 and the bases put every lane past
-    // the buffers: s * row + kWgOOB stays below 2^32)
-    const uint32_t g_base = ld_live ? (uint32_t)ld.n0 * 2 : kWgOOB;
-    const uint32_t x_base = ld_live ? (uint32_t)ld.k0 * 2 : kWgOOB;
-    uint32_t go[4], xo[4];
+  // token row of slot s
+  auto token_row = [&](uint32_t sl) {
+    const uint64_t prod = ((uint64_t)__umulhi(sl, p.topk_magic) << 32) | (sl * p.topk_magic);
+    return (uint32_t)(prod >> p.topk_shift);
+  };
+  // scalar row offsets of the wave's 4 slots of a unit within the tile's
+  // column range (a PAD slot s = S lands at or past the end of the buffers;
+  // past the last tile the ids are 0 and the bases put every lane past
+  // the buffers: s * row + kWgOOB stays below 2^32)
+  auto issue_grad = [&](int stage, const wg_i32x4_t& uid, uint32_t g_base) {
+    uint32_t go[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint32_t s = (uint32_t)uid[r];
-      const uint64_t prod = ((uint64_t)__umulhi(s, p.topk_magic) << 32) | (s * p.topk_magic);
-      const uint32_t xrow = (uint32_t)(prod >> p.topk_shift);
-      go[r] = s * g_row + g_base;
-      xo[r] = xrow * x_row + x_base;
-    }
+    for (int r = 0; r < 4; ++r) go[r] = (uint32_t)uid[r] * g_row + g_base;
     const uint32_t dst = lds_base + (uint32_t)(stage * kWgStageB);
 #pragma unroll
     for (int i = 0; i < kWgGLoads; ++i)
       wg_dma16(g_rsrc, pick(xm1, go[2 * i + 1], go[2 * i]) + (i % 2 ? x_col1 : x_col0),
                dst + (uint32_t)((wave * kWgGLoads + i) * 1024));
+  };
+  auto issue_x = [&](int stage, const wg_i32x4_t& uid, uint32_t x_base) {
+    uint32_t xo[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) xo[r] = token_row((uint32_t)uid[r]) * x_row + x_base;
+    const uint32_t dst = lds_base + (uint32_t)(stage * kWgStageB);
 #pragma unroll
     for (int i = 0; i < kWgXLoads; ++i)
       wg_dma16(x_rsrc, pick(xm1, xo[2 * i + 1], xo[2 * i]) + (i % 2 ? x_col1 : x_col0),
                dst + (uint32_t)(kWgGUnitB + (wave * kWgXLoads + i) * 1024));
   };
-  auto issue_pair = [&](int stage) {  // stages stage, stage + 1
-    issue_unit(stage, ids);
-    issue_unit(stage + 1, ids_b);
+  // MX: the wave's 4 rows of 256 code bytes in one load (16 lanes a row), and
+  // for every lane the scale byte of its 16 columns
+  const uint32_t raw_base = (uint32_t)(uintptr_t)(wg_lds_u8_t*)&raw[0];
+  const uint32_t ym1 = lane & 16 ? ~0u : 0u;
+  auto issue_raw = [&](int unit, const wg_i32x4_t& uid, uint32_t x_base, uint32_t s_base) {
+    uint32_t xo[4], so[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t row = token_row((uint32_t)uid[r]);
+      xo[r] = row * x_row + x_base;
+      so[r] = row * (uint32_t)p.xs_ld + s_base;
+    }
+    wg_dma16(x_rsrc, pick(xm1, pick(ym1, xo[3], xo[2]), pick(ym1, xo[1], xo[0])) + (uint32_t)(lane % 16) * 16,
+             raw_base + (uint32_t)(unit * kWgRawUnitB + wave * 1024));
+    wg_dma_byte(xs_rsrc, pick(xm1, pick(ym1, so[3], so[2]), pick(ym1, so[1], so[0])) + (uint32_t)(lane % 16) / 2,
+                raw_base + (uint32_t)(2 * kWgRawUnitB + unit * kWgThreads * 4 + wave * 256));
+  };
+  // MX: this wave's pieces of the pair in `raw`, decoded into the x parts of
+  // stages stage, stage + 1
+  auto decode_raw = [&](int stage) {
+    const wg_lds_u8_t* src = (const wg_lds_u8_t*)&raw[0];
+#pragma unroll
+    for (int unit = 0; unit < 2; ++unit) {
+      const u32x4_t c = *(const __attribute__((address_space(3))) u32x4_t*)(src + unit * kWgRawUnitB + wave * 1024 +
+                                                                            lane * 16);
+      const uint32_t b = *(const __attribute__((address_space(3))) uint32_t*)(src + 2 * kWgRawUnitB +
+                                                                              (unit * kWgThreads + wave * 64 + lane) * 4);
+      const float scale = e8m0_as_scale(b);
+      const bf16x8_t v0 = dequant_e4m3x8(c[0], c[1], scale), v1 = dequant_e4m3x8(c[2], c[3], scale);
+      const int m = wave * 4 + lane / 16, u = 2 * (lane % 16);
+      wg_lds_u8_t* dst = (wg_lds_u8_t*)&lds[stage + unit][kWgGUnitB + m * kWgXRowB];
+      *(__attribute__((address_space(3))) bf16x8_t*)(dst + wg_swz(m, u) * 16) = v0;
+      *(__attribute__((address_space(3))) bf16x8_t*)(dst + wg_swz(m, u + 1) * 16) = v1;
+    }
+    // the reads are done before the next pair's codes may overwrite `raw`
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+  // moves the loader to the next pair and starts its ids' loads, complete by
+  // the next wait
+  auto ld_next = [&]() {
     if (ld_live) {
       ld_u += 2;
       ld_skip_empty();
-      ld_ids_pair(ids, ids_b);  // complete by the next wait
+      ld_ids_pair(ids, ids_b);
     }
+  };
+  // !MX: the pair the loader points at, into stages stage, stage + 1
+  auto issue_pair = [&](int stage) {
+    const uint32_t g_base = ld_live ? (uint32_t)ld.n0 * 2 : kWgOOB;
+    const uint32_t x_base = ld_live ? (uint32_t)ld.k0 * 2 : kWgOOB;
+    issue_grad(stage, ids, g_base);
+    issue_x(stage, ids, x_base);
+    issue_grad(stage + 1, ids_b, g_base);
+    issue_x(stage + 1, ids_b, x_base);
+    ld_next();
+  };
+  // MX: the codes of the pair the loader points at, whose ids and grad base
+  // are kept for its gradient loads one pair later
+  wg_i32x4_t g_ids, g_ids_b;
+  uint32_t g_base_kept = 0;
+  auto issue_raw_pair = [&]() {
+    const uint32_t x_base = ld_live ? (uint32_t)ld.k0 : kWgOOB;
+    const uint32_t s_base = ld_live ? (uint32_t)ld.k0 / 32 : kWgOOB;
+    issue_raw(0, ids, x_base, s_base);
+    issue_raw(1, ids_b, x_base, s_base);
+    g_ids = ids;
+    g_ids_b = ids_b;
+    g_base_kept = ld_live ? (uint32_t)ld.n0 * 2 : kWgOOB;
+    ld_next();
+  };
+  // MX: the next pair's gradients and decoded x into stages stage, stage + 1,
+  // then the codes of the pair after it
+  auto advance_mx = [&](int stage) {
+    issue_grad(stage, g_ids, g_base_kept);
+    issue_grad(stage + 1, g_ids_b, g_base_kept);
+    decode_raw(stage);
+    issue_raw_pair();
   };
 
   // waves 4 x 2: wave (wn, wk) computes dW rows n0 + wn*64 .. + 63 and
@@ -321,7 +420,13 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
   //      before them); the barrier makes every wave's DMA visible and
   //      guarantees all waves finished the previous pair, whose two stages
   //      the loads issued next overwrite.
-  issue_pair(0);
+  if constexpr (MX) {
+    issue_raw_pair();
+    wg_wait_barrier<0>(ids, ids_b);
+    advance_mx(0);
+  } else {
+    issue_pair(0);
+  }
   int st = 0;  // first stage of the next pair computed
   bool stored = false;
   for (int it = 0; tile_index(it) < total; ++it) {
@@ -340,7 +445,10 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
       } else {
         wg_wait_barrier<0>(ids, ids_b);
       }
-      issue_pair(st ^ 2);  // the pair computed last, now free
+      if constexpr (MX)  // the stages of the pair computed last, now free
+        advance_mx(st ^ 2);
+      else
+        issue_pair(st ^ 2);
       contract(st);
       contract(st + 1);
       st ^= 2;
@@ -388,7 +496,8 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
 
 int wgrad_block_m() { return kWgBM; }
 
-hipError_t launch_wgrad(const WgradParams& p_in, hipStream_t stream) {
+template <bool MX>
+static hipError_t wg_launch(const WgradParams& p_in, hipStream_t stream) {
   WgradParams p = p_in;
   p.tiles_n = (p.N + kWgTN - 1) / kWgTN;
   p.tiles_k = (p.K + kWgTK - 1) / kWgTK;
@@ -410,8 +519,11 @@ hipError_t launch_wgrad(const WgradParams& p_in, hipStream_t stream) {
   // stretch of tiles per XCD per round)
   int64_t grid = (int64_t)cus * kWgPerCU;
   grid = (grid + 7) / 8 * 8;
-  hipLaunchKernelGGL(wgrad_kernel, dim3((uint32_t)grid), dim3(kWgThreads), 0, stream, p);
+  hipLaunchKernelGGL(wgrad_kernel<MX>, dim3((uint32_t)grid), dim3(kWgThreads), 0, stream, p);
   return hipGetLastError();
 }
+
+hipError_t launch_wgrad(const WgradParams& p, hipStream_t stream) { return wg_launch<false>(p, stream); }
+hipError_t launch_wgrad_mxfp8(const WgradParams& p, hipStream_t stream) { return wg_launch<true>(p, stream); }
 
 }  // namespace moe

@@ -36,8 +36,13 @@ other than itself:
     quant.mx_quantize_e4m3  pinned  (every code round-trips at a known shared exponent;
                                      scale rule, ties, saturation, zero and clamped
                                      blocks; torch's float8_e4m3fn cast in range)
+    train.route             pinned  (uniform and collapsed routers, scalar loop, masked experts and rows)
+    train.route_backward    pinned  (central differences of the forward definition)
+    train.combine_routed / combine_backward  pinned (gemm.combine, linearity)
+    train.act_mxfp8 / act_backward  pinned  (quant and gemm's parts, central differences, closed forms)
+    train.wgrad_mxfp8_expert pinned (wgrad.wgrad_expert on the decoded rows)
 """
 
-from . import formats, bucket, align, gemm, wgrad, layer, layout, quant  # noqa: F401
+from . import formats, bucket, align, gemm, wgrad, layer, layout, quant, train  # noqa: F401
 
-__all__ = ["formats", "bucket", "align", "gemm", "wgrad", "layer", "layout", "quant"]
+__all__ = ["formats", "bucket", "align", "gemm", "wgrad", "layer", "layout", "quant", "train"]

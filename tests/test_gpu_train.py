@@ -1,0 +1,607 @@
+"""GPU tests of the training entry points (moe_train.h) against the float64
+oracle (oracle.train): the router with its losses and gradient, the combine
+over partly routed tokens and its backward pass, the activation with an MXFP8
+checkpoint, the weight gradient over MXFP8 rows, and a whole training step.
+
+Tolerances (u = 2^-24, half a step of fp32):
+* router: exp(a - m) in fp32 carries the roundings of a, of a - m and of the
+  exponential's argument reduction, each up to 2u times a magnitude of at most
+  D = max|a| + max(m - a) over the finite log scores a above m - 100 (below, a
+  probability is under 2^-144 and only has to be tiny), plus the function's
+  own error (a few u) and the sums' (one u per addition of positive terms):
+  relative error below (4 D + 64 + additions) u. The gradient's terms are
+  measured against the size of what is added up, with E and top_k additions.
+* bf16 outputs: half a step, 2^-8 of the value, plus the fp32 error before it
+  (2^-20 of the terms' size).
+* dot products of N terms in fp32: N u of the sum of magnitudes.
+* weight gradient: one u per slot added (twice, for the order inside an MFMA).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from helpers import bf16_to_f64, need_gpu
+from oracle import quant as oquant
+from oracle import train as otrain
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _moe():
+    import mixture_experts_grouped_moe_amd as moe
+    return moe
+
+
+def f64(t):
+    return t.detach().float().cpu().double().numpy()
+
+
+def close(got, ref, tol, what=""):
+    """|got - ref| <= tol elementwise, with equal NaN and infinity masks."""
+    got, ref, tol = (np.asarray(v, dtype=np.float64) for v in (got, ref, tol))
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    # what lies past the largest float32 (and bfloat16) rounds to infinity
+    ref = np.where(np.abs(ref) > 2.0 ** 128, np.copysign(np.inf, ref), ref)
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), f"{what}: NaN positions differ"
+    inf = np.isinf(ref)
+    assert np.array_equal(got[inf], ref[inf]), f"{what}: infinities differ"
+    ok = ~np.isnan(ref) & ~inf
+    err = np.abs(got - ref)[ok]
+    bound = np.broadcast_to(tol, ref.shape)[ok]
+    assert (err <= bound).all(), f"{what}: worst {np.max(err / np.maximum(bound, 1e-300)):.3g} of the tolerance"
+
+
+# ------------------------------------------------------------------- router
+
+def logits(T, E, seed, dtype="fp32", std=1.5):
+    z = torch.randn((T, E), generator=synth.gen(seed, "logits"), dtype=torch.float32) * std
+    return (z.to(torch.bfloat16) if dtype == "bf16" else z).cuda()
+
+
+def spread(z, score):
+    """D of the module's tolerance."""
+    a = otrain.log_scores(z, score)
+    a = np.where(np.isfinite(a), a, np.nan)
+    if np.isnan(a).all():
+        return 0.0
+    with np.errstate(all="ignore"):
+        m = np.nanmax(np.where(np.isnan(a), -np.inf, a), axis=1, keepdims=True)
+        near = a > m - 100
+    return float(np.max(np.where(near, np.abs(a) + (m - a), 0.0), initial=0.0))
+
+
+def check_route(z, k, score="softmax", renorm=True, scale=1.0, mask=None, **kw):
+    moe = _moe()
+    got = moe.moe_route(z, k, score=score, renormalize=renorm, scale=scale, mask=mask, balance=True, **kw)
+    torch.cuda.synchronize()
+    zz, mm = f64(z), None if mask is None else mask.cpu().numpy()
+    ids, w, counts, n, p, loss = otrain.route(zz, k, score, renorm, scale, mm)
+    T, E = zz.shape
+    assert np.array_equal(got[0].cpu().numpy(), ids)
+    assert np.array_equal(got[2].cpu().numpy(), counts)
+    assert int(got[3]) == n
+    tol = (4 * spread(zz, score) + 64 + E) * U
+    close(f64(got[1]), w, tol * np.abs(w) + 2.0 ** -120, "weights")
+    with np.errstate(invalid="ignore"):
+        close(f64(got[4]), p, (tol + T * U) * np.abs(p) + 2.0 ** -120, "prob_sum")
+        close(f64(got[5]), loss, (2 * tol + T * U) * np.abs(loss) + 2.0 ** -120, "losses")
+    # without the statistics: the same ids and weights
+    ids2, w2 = moe.moe_route(z, k, score=score, renormalize=renorm, scale=scale, mask=mask)
+    assert torch.equal(ids2, got[0])
+    assert np.array_equal(w2.cpu().numpy(), got[1].cpu().numpy(), equal_nan=True)
+    return got
+
+
+def check_route_backward(z, k, fwd, score="softmax", renorm=True, scale=1.0, losses=True, seed=1, dw=None, **kw):
+    moe = _moe()
+    ids, _, counts, n = fwd[:4]
+    T, E = z.shape
+    if dw is None:
+        dw = torch.randn((T, k), generator=synth.gen(seed, "dw")).cuda()
+    dl = torch.tensor([0.5, -0.25], device="cuda") if losses else None
+    got = moe.moe_route_backward(z, ids, dw, score=score, renormalize=renorm, scale=scale,
+                                 counts=counts if losses else None, num_routed=n if losses else None, dlosses=dl, **kw)
+    torch.cuda.synchronize()
+    zz = f64(z)
+    ref, size = otrain.route_backward(zz, ids.cpu().numpy(), dw.cpu().double().numpy(), score, renorm, scale,
+                                      counts.cpu().numpy(), int(n), None if dl is None else dl.cpu().double().numpy())
+    tol = (4 * spread(zz, score) + 64 + E + 2 * k) * U
+    half = 2.0 ** -8 if z.dtype == torch.bfloat16 else U
+    close(f64(got), ref, 2 * tol * size + half * np.abs(ref) + 2.0 ** -120, "dlogits")
+    return got
+
+
+SHAPES = [(1, 1, 1), (1, 8, 2), (5, 7, 7), (7, 64, 6), (33, 97, 5), (130, 128, 4), (257, 256, 8), (64, 300, 10),
+          (40, 512, 8), (17, 1024, 64), (9, 1000, 1)]
+
+
+@pytest.mark.parametrize("T,E,k", SHAPES)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True),
+                                          ("sigmoid", False)])
+def test_route_and_gradient(T, E, k, dtype, score, renorm):
+    z = logits(T, E, T * 7 + E, dtype)
+    mask = (torch.rand(T, generator=synth.gen(T + E, "mask")) < 0.8).to(torch.uint8).cuda() if T > 5 else None
+    fwd = check_route(z, k, score, renorm, 2.5, mask)
+    check_route_backward(z, k, fwd, score, renorm, 2.5)
+    check_route_backward(z, k, fwd, score, renorm, 2.5, losses=False)
+
+
+@pytest.mark.parametrize("T", [0, 6001])
+def test_route_no_tokens_and_many_rows_per_wave(T):
+    z = logits(T, 40, 3)
+    fwd = check_route(z, 3)
+    check_route_backward(z, 3, fwd)
+
+
+def test_route_ties_take_the_lowest_expert():
+    # logits of few distinct values, both zeros among them
+    g = synth.gen(5, "ties")
+    v = torch.tensor([-1.0, -0.0, 0.0, 0.5])
+    z = v[torch.randint(0, 4, (200, 130), generator=g)].cuda()
+    for zz in (z, z.to(torch.bfloat16)):
+        fwd = check_route(zz, 9)
+        check_route_backward(zz, 9, fwd)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True),
+                                          ("sigmoid", False)])
+def test_route_masked_experts_and_rows(dtype, score, renorm):
+    z = torch.randn((12, 70), generator=synth.gen(6, "z"))
+    low = torch.finfo(dtype).min
+    z[0, 5:] = -float("inf")           # five experts left for six places
+    z[1] = -float("inf")               # none
+    z[2, 1:] = -float("inf")           # one
+    z[3, 3:] = low                     # masked by the type's lowest value: chosen last, weight 0
+    z[4] = low                         # all of them: uniform
+    z[5, :] = 80.0                     # far from 0
+    z[6, :] = -80.0
+    z[7, 40] = 300.0
+    z = z.to(dtype).cuda()
+    mask = torch.ones(12, dtype=torch.bool, device="cuda")
+    mask[8] = False
+    z[8, 10] = float("nan")            # padding may hold anything
+    z[8, 11] = float("inf")
+    zz = z[:8] if score == "softmax" else z[[0, 1, 2, 5, 6, 7]]  # sigmoid of the lowest value: tested below
+    got = check_route(zz, 6, score, renorm)
+    check_route_backward(zz, 6, got, score, renorm, losses=False)
+    m = check_route(z[8:].contiguous(), 6, score, renorm, mask=mask[8:])
+    assert (m[0][0] == -1).all() and (m[1][0] == 0).all()
+    d = check_route_backward(torch.where(torch.isfinite(z[8:]), z[8:], 0), 6, m, score, renorm)
+    assert (d[0] == 0).all()
+    moe = _moe()
+    ids, w = moe.moe_route(z, 6, score=score, renormalize=renorm, mask=mask)
+    dirty = moe.moe_route_backward(z, ids, torch.full_like(w, float("nan")), score=score, renormalize=renorm)
+    assert (dirty[[1, 8]] == 0).all()  # nothing of a padded row's logits or weight gradients comes through
+
+
+def test_route_sigmoid_of_the_lowest_value():
+    # sigmoid underflows: unnormalised weights 0; renormalised, those left decide
+    z = torch.full((2, 20), torch.finfo(torch.float32).min)
+    z[0, :2] = torch.tensor([1.0, 2.0])
+    got = check_route(z.cuda(), 4, "sigmoid", False)
+    assert (got[1][0, 2:] == 0).all() and (got[1][1] == 0).all()
+    got = check_route(z.cuda(), 4, "sigmoid", True)
+    assert (got[1][1] == 0.25).all()
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True),
+                                          ("sigmoid", False)])
+def test_route_non_finite_logits_show(score, renorm):
+    z = logits(6, 50, 8)
+    z[2, 3] = float("nan")
+    z[3] = float("nan")
+    got = check_route(z, 5, score, renorm)
+    assert torch.isnan(got[5][0]) and int(got[3]) == 6 and (got[0][2] >= 0).all() and (got[0][3] == -1).all()
+    z = logits(6, 50, 9)
+    z[1, 7] = float("inf")
+    moe = _moe()
+    ids, w, _, n, p, loss = moe.moe_route(z, 5, score=score, renormalize=renorm, balance=True)
+    assert int(ids[1, 0]) == 7 and int(n) == 6
+    assert torch.isnan(loss[0]) == (score == "softmax")
+    if score == "sigmoid":
+        assert torch.isfinite(w).all()
+
+
+def test_route_strided_rows_and_given_outputs():
+    moe = _moe()
+    base = logits(30, 100, 10)
+    z = base[:, 3:99]
+    poison = (torch.full((30, 5), -7, dtype=torch.int32, device="cuda"),
+              torch.full((30, 5), float("nan"), device="cuda"),
+              torch.full((96,), -7, dtype=torch.int32, device="cuda"),
+              torch.full((1,), -7, dtype=torch.int32, device="cuda"),
+              torch.full((96,), float("nan"), device="cuda"), torch.full((2,), float("nan"), device="cuda"))
+    ws = torch.full((moe.moe_route_workspace_bytes(30, 96),), 0xAB, dtype=torch.uint8, device="cuda")
+    fwd = check_route(z, 5, out=poison, workspace=ws)
+    assert fwd[0] is poison[0]
+    wide = torch.full((33, 101), 9.0, device="cuda")
+    check_route_backward(z, 5, fwd, out=wide[:30, 2:98])
+    wide[:30, 2:98] = 9.0
+    assert (wide == 9.0).all()
+    b = base.to(torch.bfloat16)[:, 3:99]                    # rows on odd 2-byte addresses
+    check_route_backward(b, 5, check_route(b, 5), out=wide.to(torch.bfloat16)[:30, 1:97])
+
+
+def test_route_backward_skips_ids_out_of_range():
+    z = logits(4, 20, 11)
+    fwd = list(check_route(z, 3))
+    ids = fwd[0].clone()
+    ids[1, 2] = 20
+    ids[2, 1] = -5
+    ids[3, 0] = -1
+    fwd[0] = ids
+    check_route_backward(z, 3, fwd, renorm=False)
+    check_route_backward(z, 3, fwd)
+
+
+def test_route_repeats_bit_for_bit_on_any_stream():
+    moe = _moe()
+    z = logits(3000, 256, 12)
+    ref = moe.moe_route(z, 8, balance=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        a = moe.moe_route(z, 8, balance=True)
+        b = moe.moe_route(z, 8, balance=True, stream=side)      # both at once
+        torch.cuda.synchronize()
+        for x, y, r in zip(a, b, ref):
+            assert torch.equal(x, r) and torch.equal(y, r)
+
+
+# ------------------------------------------------------------------ combine
+
+def _combine_case(T, k, N, E, seed, unrouted=True):
+    g = synth.gen(seed, "combine")
+    dy = torch.randn((T, N), generator=g).to(torch.bfloat16)
+    c = torch.randn((T * k, N), generator=g).to(torch.bfloat16)
+    w = torch.rand((T, k), generator=g)
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    if unrouted and T > 2:
+        ids[1] = -1
+        ids[2, 0] = E
+        c[k:2 * k] = float("nan")
+        c[2 * k] = float("inf")
+        w[1] = float("nan")
+    return dy.cuda(), c.cuda(), w.cuda(), ids.cuda()
+
+
+@pytest.mark.parametrize("T,k,N", [(1, 1, 8), (3, 2, 64), (7, 6, 1856), (50, 4, 2880), (21, 8, 7168), (5, 13, 264),
+                                   (9, 10, 4104), (300, 1, 136)])
+def test_combine_routed_and_backward(T, k, N):
+    moe, E = _moe(), 9
+    dy, c, w, ids = _combine_case(T, k, N, E, T + N)
+    y = moe.moe_combine_routed(c, w, ids, E)
+    dc, dw = moe.moe_combine_backward(dy, c, w, ids, E)
+    torch.cuda.synchronize()
+    n = ids.cpu().numpy()
+    cc, ww = f64(c), w.cpu().double().numpy()
+    ref = otrain.combine_routed(cc, ww, n, E)
+    on = (n >= 0) & (n < E)
+    size = otrain.combine_routed(np.abs(cc), np.abs(ww), n, E)
+    close(f64(y), ref, 2.0 ** -8 * np.abs(ref) + k * U * size, "y")
+    rc, rw, rs = otrain.combine_backward(f64(dy), cc, ww, n, E)
+    close(f64(dc), rc, 2.0 ** -8 * (1 + 2.0 ** -15) * np.abs(rc), "dC")
+    close(f64(dw), rw, N * U * rs, "dw")
+    assert (f64(dc)[~on.reshape(-1)] == 0).all() and (f64(dw)[~on] == 0).all()
+    # every slot routed: the plain combine's bits, and the same gradient without ids
+    dy, c, w, ids = _combine_case(T, k, N, E, T + N, unrouted=False)
+    assert torch.equal(moe.moe_combine_routed(c, w, ids, E), moe.moe_combine(c, w, k))
+    a, b = moe.moe_combine_backward(dy, c, w, ids, E), moe.moe_combine_backward(dy, c, w)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_combine_backward_strides_and_rows_behind():
+    moe, T, k, N = _moe(), 11, 3, 96
+    dy, c, w, ids = _combine_case(T, k, N, 5, 77)
+    wide = torch.full((T * k + 2, N + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    cw = torch.full((T * k, N + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    cw[:, :N] = c
+    dyw = torch.cat([dy, dy], 1)[:, N:]
+    dw = torch.empty((T, k), device="cuda")
+    moe.moe_combine_backward(dyw, cw[:, :N], w, ids, 5, out=(wide[:, 8:N + 8], dw))
+    ref = moe.moe_combine_backward(dy, c, w, ids, 5)
+    torch.cuda.synchronize()
+    assert torch.equal(wide[:T * k, 8:N + 8], ref[0]) and torch.equal(dw, ref[1])
+    wide[:T * k, 8:N + 8] = 7.0
+    assert (wide == 7.0).all()
+
+
+def test_combine_no_tokens():
+    moe = _moe()
+    e = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
+    w, ids = torch.zeros((0, 2), device="cuda"), torch.zeros((0, 2), dtype=torch.int32, device="cuda")
+    assert moe.moe_combine_routed(e, w, ids, 4).shape == (0, 64)
+    assert moe.moe_combine_backward(e, e, w, ids, 4)[0].shape == (0, 64)
+
+
+# --------------------------------------------------------------- activation
+
+def _check_act(pre, dh, activation, **kw):
+    moe = _moe()
+    h, q, s = moe.moe_act_mxfp8(pre, activation, **kw)
+    torch.cuda.synchronize()
+    p = f64(pre)
+    rh, rq, rs = otrain.act_mxfp8(p, activation)
+    assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
+    close(f64(h), rh, 2.0 ** -8 * (1 + 2.0 ** -10) * np.abs(rh) + 2.0 ** -126, "h")
+    q0, s0 = moe.moe_quantize_mxfp8(pre)
+    assert torch.equal(q, q0) and torch.equal(s, s0)
+    d, h2 = moe.moe_act_mxfp8_backward(q, s, dh, activation)
+    torch.cuda.synchronize()
+    rd, rh2, size = otrain.act_backward(rq, rs, f64(dh), activation)
+    close(f64(d), rd, 2.0 ** -8 * np.abs(rd) + 2.0 ** -20 * size + 2.0 ** -126, "dpre")
+    close(f64(h2), rh2, 2.0 ** -8 * (1 + 2.0 ** -10) * np.abs(rh2) + 2.0 ** -126, "h again")
+    d1, none = moe.moe_act_mxfp8_backward(q, s, dh, activation, recompute=False)
+    assert none is None and torch.equal(d1, d)
+    return h, q, s
+
+
+@pytest.mark.parametrize("R,N,activation", [(1, 64, "swiglu"), (1, 32, "relu2"), (42, 1856, "relu2"),
+                                            (77, 5760, "swiglu"), (300, 192, "swiglu"), (129, 96, "relu2"),
+                                            (1000, 448, "swiglu"), (0, 128, "swiglu"), (0, 96, "relu2")])
+def test_act_checkpoint_and_backward(R, N, activation):
+    g = synth.gen(R + N, "act")
+    # blocks of very different magnitudes
+    mag = torch.pow(2.0, torch.randint(-12, 5, (R, N // 32, 1), generator=g).float())
+    pre = (torch.randn((R, N // 32, 32), generator=g) * mag).reshape(R, N).to(torch.bfloat16).cuda()
+    dh = torch.randn((R, N // 2 if activation == "swiglu" else N), generator=g).to(torch.bfloat16).cuda()
+    _check_act(pre, dh, activation)
+
+
+def test_act_edges():
+    # zeros, saturated gates on both sides, and blocks that hold a NaN or an infinity
+    moe = _moe()
+    pre = torch.zeros((6, 128))
+    pre[1, :32] = 60.0
+    pre[1, 32:64] = -60.0
+    pre[1, 64:] = 3.0
+    pre[2] = torch.linspace(-20, 20, 128)
+    pre[3] = -1.278
+    dh = torch.ones((6, 64), dtype=torch.bfloat16, device="cuda")
+    _check_act(pre.to(torch.bfloat16).cuda(), dh, "swiglu")
+    _check_act(pre.to(torch.bfloat16).cuda(), torch.ones((6, 128), dtype=torch.bfloat16, device="cuda"), "relu2")
+    pre[4, 70] = float("inf")
+    pre[5, 3] = float("nan")
+    p = pre.to(torch.bfloat16).cuda()
+    h, q, s = moe.moe_act_mxfp8(p, "swiglu")
+    d, h2 = moe.moe_act_mxfp8_backward(q, s, dh, "swiglu")
+    torch.cuda.synchronize()
+    assert int(s[4, 2]) == 0xFF and int(s[5, 0]) == 0xFF and (s[:4] != 0xFF).all()
+    assert torch.isnan(h[5, 3]) and torch.isfinite(h[5, 4:]).all()
+    # the NaN block is 32 elements of one half; its partner half's gradient is NaN with it
+    for row in (4, 5):
+        assert torch.isnan(h2[row, :32]).all() and torch.isfinite(h2[row, 32:]).all()
+        assert torch.isfinite(d[row, 32:64]).all() and torch.isfinite(d[row, 96:]).all()
+    assert torch.isnan(d[4, :32]).all() and torch.isnan(d[5, :32]).all() and torch.isnan(d[5, 64:96]).all()
+
+
+def test_act_strides_and_rows_behind():
+    moe, R, N = _moe(), 13, 128
+    g = synth.gen(4, "act")
+    base = torch.randn((R, N + 24), generator=g).to(torch.bfloat16).cuda()
+    pre = base[:, 8:8 + N]
+    ref = moe.moe_act_mxfp8(pre.contiguous(), "swiglu")
+    h = torch.full((R + 1, 80), 5.0, dtype=torch.bfloat16, device="cuda")
+    q = torch.full((R + 1, N + 16), 0xAB, dtype=torch.uint8, device="cuda")
+    s = torch.full((R + 1, 7), 0xCD, dtype=torch.uint8, device="cuda")
+    moe.moe_act_mxfp8(pre, "swiglu", out=(h[:, 8:72], q[:, 16:], s[:, 3:]))
+    torch.cuda.synchronize()
+    assert torch.equal(h[:R, 8:72], ref[0]) and torch.equal(q[:R, 16:], ref[1]) and torch.equal(s[:R, 3:], ref[2])
+    dh = torch.randn((R, 72), generator=g).to(torch.bfloat16).cuda()[:, 8:]
+    want = moe.moe_act_mxfp8_backward(ref[1], ref[2], dh.contiguous(), "swiglu")
+    d = torch.full((R + 1, N + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    h2 = torch.full((R + 1, 72), 5.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_act_mxfp8_backward(q[:R, 16:], s[:R, 3:], dh, "swiglu", out=(d[:, 8:], h2[:, :64]))
+    torch.cuda.synchronize()
+    assert torch.equal(d[:R, 8:], want[0]) and torch.equal(h2[:R, :64], want[1])
+    h[:R, 8:72], q[:R, 16:], s[:R, 3:], d[:R, 8:], h2[:R, :64] = 5.0, 0xAB, 0xCD, 5.0, 5.0
+    assert (h == 5).all() and (q == 0xAB).all() and (s == 0xCD).all() and (d == 5).all() and (h2 == 5).all()
+
+
+# ---------------------------------------------------------- weight gradient
+
+def _wgrad_case(T, k, E, N, K, seed):
+    d = synth.config5(seed=seed, T=T, E=E, N=N, K=K, k=k, device="cuda")
+    moe = _moe()
+    xq, xs = moe.moe_quantize_mxfp8(d["x"])
+    return xq, xs, d["grad"], d["ids"]
+
+
+def _check_wgrad(xq, xs, grad, ids, E, out=None, experts=None):
+    moe = _moe()
+    T, k = ids.shape
+    routing = moe.moe_align(ids, E, moe.moe_wgrad_block_m())
+    dw = moe.moe_wgrad_mxfp8(xq, xs, grad, routing, T, k, E, out=out)
+    torch.cuda.synchronize()
+    n, hq, hs, hg = ids.cpu().numpy(), xq.cpu().numpy(), xs.cpu().numpy(), f64(grad)
+    for e in range(E) if experts is None else experts:
+        ref, size = otrain.wgrad_mxfp8_expert(hq, hs, hg, n, k, e)
+        close(dw[e].cpu().double().numpy(), ref, (2 * int((n == e).sum()) + 2) * U * size, f"expert {e}")
+    return dw
+
+
+@pytest.mark.parametrize("T,k,E,N,K", [(300, 4, 8, 256, 384), (97, 2, 5, 160, 96), (1000, 8, 32, 64, 128),
+                                       (130, 3, 7, 96, 160), (64, 6, 12, 64, 64), (1, 1, 1, 32, 32),
+                                       (64, 2, 8, 512, 256), (700, 1, 2, 288, 544)])
+def test_wgrad_mxfp8(T, k, E, N, K):
+    case = _wgrad_case(T, k, E, N, K, T)
+    dw = _check_wgrad(*case, E, out=torch.full((E, N, K), float("nan"), device="cuda"))
+    # the bits of moe_wgrad on the decoded rows (exact in bf16)
+    moe = _moe()
+    xq, xs, grad, ids = case
+    x = torch.from_numpy(oquant.mx_dequantize_e4m3(xq.cpu().numpy(), xs.cpu().numpy())).to(torch.bfloat16).cuda()
+    routing = moe.moe_align(ids, E, moe.moe_wgrad_block_m())
+    assert torch.equal(dw, moe.moe_wgrad(x, grad, routing, T, k, E))
+
+
+def test_wgrad_mxfp8_unrouted_slots_and_empty_experts():
+    xq, xs, grad, ids = _wgrad_case(200, 3, 10, 96, 128, 5)
+    ids = torch.where(ids >= 7, -1, ids).contiguous()          # experts 7..9 empty, their slots routed nowhere
+    ids[10:20] = -1                                            # padded tokens: rows that may hold anything
+    xq[10:20], xs[10:20] = 0x7F, 0xFF
+    grad[30:60] = float("nan")
+    dw = _check_wgrad(xq, xs, grad, ids, 10)
+    assert (dw[7:] == 0).all()
+
+
+def test_wgrad_mxfp8_strides_at_the_end_of_an_allocation():
+    T, k, E, N, K = 50, 2, 3, 64, 96
+    xq, xs, grad, ids = _wgrad_case(T, k, E, N, K, 6)
+    xw = torch.zeros((T, K + 32), dtype=torch.uint8, device="cuda")
+    sw = torch.zeros((T, 8), dtype=torch.uint8, device="cuda")
+    gw = torch.zeros((T * k, N + 8), dtype=torch.bfloat16, device="cuda")
+    xw[:, 32:], sw[:, 5:], gw[:, 8:] = xq, xs, grad            # the last row ends with the buffer
+    _check_wgrad(xw[:, 32:], sw[:, 5:], gw[:, 8:], ids, E)
+
+
+def test_wgrad_mxfp8_scale_edges():
+    T, k, E, N, K = 40, 1, 2, 32, 64
+    xq, xs, grad, ids = _wgrad_case(T, k, E, N, K, 7)
+    xs[:, 0] = 100 + torch.arange(T, device="cuda", dtype=torch.uint8)
+    xq[:, 32:] = 0
+    xs[:, 1] = 0
+    _check_wgrad(xq, xs, grad, ids, E)
+    xs[3, 1] = 0xFF                                            # a NaN block reaches its 32 columns of one expert
+    moe = _moe()
+    routing = moe.moe_align(ids, E, moe.moe_wgrad_block_m())
+    dw = moe.moe_wgrad_mxfp8(xq, xs, grad, routing, T, k, E)
+    e = int(ids[3, 0])
+    assert torch.isnan(dw[e, :, 32:]).all() and torch.isfinite(dw[e, :, :32]).all() and torch.isfinite(dw[1 - e]).all()
+
+
+def test_wgrad_mxfp8_no_tokens():
+    moe, E, N, K = _moe(), 4, 64, 96
+    ids = torch.zeros((0, 2), dtype=torch.int32, device="cuda")
+    routing = moe.moe_align(ids, E, moe.moe_wgrad_block_m())
+    dw = torch.full((E, N, K), float("nan"), device="cuda")
+    moe.moe_wgrad_mxfp8(torch.zeros((0, K), dtype=torch.uint8, device="cuda"),
+                        torch.zeros((0, K // 32), dtype=torch.uint8, device="cuda"),
+                        torch.zeros((0, N), dtype=torch.bfloat16, device="cuda"), routing, 0, 2, E, out=dw)
+    torch.cuda.synchronize()
+    assert (dw == 0).all()
+
+
+def test_wgrad_mxfp8_large_sampled():
+    # ragged tiles, hundreds of blocks, many tiles per workgroup
+    T, k, E, N, K = 4096, 4, 48, 1056, 2880
+    case = _wgrad_case(T, k, E, N, K, 8)
+    a = _check_wgrad(*case, E, experts=[0, 17, 47]).clone()
+    moe = _moe()
+    routing = moe.moe_align(case[3], E, moe.moe_wgrad_block_m())
+    assert torch.equal(a, moe.moe_wgrad_mxfp8(*case[:3], routing, T, k, E))
+
+
+# --------------------------------------------------------- the whole step
+
+def _step(moe, d, bufs=None):
+    """One forward and backward pass of a SwiGLU layer; returns its tensors."""
+    T, H = d["x"].shape
+    E, k, I = d["w1"].shape[0], d["k"], d["w2"].shape[2]
+    xq, xs = moe.moe_quantize_mxfp8(d["x"])
+    ids, w, counts, n, _, losses = moe.moe_route(d["logits"], k, mask=d["mask"], balance=True)
+    routing = moe.moe_align(ids, E, moe.moe_gemm_block_m("bf16", T))
+    pre = moe.moe_grouped_gemm(d["x"], d["w1"], "bf16", routing, T, k, E, k)
+    h, q, s = moe.moe_act_mxfp8(pre, "swiglu")
+    c = moe.moe_grouped_gemm(h, d["w2"], "bf16", routing, T, k, E, 1)
+    y = moe.moe_combine_routed(c, w, ids, E)
+    dc, dw = moe.moe_combine_backward(d["dy"], c, w, ids, E)
+    dh = moe.moe_grouped_gemm(dc, d["w2t"], "bf16", routing, T, k, E, 1)
+    dpre, h = moe.moe_act_mxfp8_backward(q, s, dh, "swiglu")
+    wr = moe.moe_align(ids, E, moe.moe_wgrad_block_m())
+    dw2 = moe.moe_wgrad(h, dc, wr, T * k, 1, E)
+    dw1 = moe.moe_wgrad_mxfp8(xq, xs, dpre, wr, T, k, E)
+    dxs = moe.moe_grouped_gemm(dpre, d["w1t"], "bf16", routing, T, k, E, 1)
+    dx = moe.moe_combine_routed(dxs, d["ones"], ids, E)
+    dz = moe.moe_route_backward(d["logits"], ids, dw, counts=counts, num_routed=n, dlosses=d["dlosses"])
+    return {"y": y, "losses": losses, "dw1": dw1, "dw2": dw2, "dx": dx, "dz": dz, "ids": ids}
+
+
+def _step_case(T=70, H=128, I=96, E=6, k=2):
+    g = synth.gen(31, "step")
+
+    def normal(*shape, std=1.0):
+        return torch.randn(shape, generator=g) * std
+    d = {"k": k, "x": normal(T, H).to(torch.bfloat16).cuda(), "logits": normal(T, E).cuda(),
+         "w1": normal(E, 2 * I, H, std=H ** -0.5).to(torch.bfloat16).cuda(),
+         "w2": normal(E, H, I, std=I ** -0.5).to(torch.bfloat16).cuda(),
+         "dy": normal(T, H).to(torch.bfloat16).cuda(), "mask": torch.ones(T, dtype=torch.uint8).cuda(),
+         "ones": torch.ones((T, k)).cuda(), "dlosses": torch.tensor([0.3, 0.1]).cuda()}
+    d["mask"][5:9] = 0
+    d["x"][6] = float("nan")                        # padding may hold anything
+    d["w1t"], d["w2t"] = (t.transpose(1, 2).contiguous() for t in (d["w1"], d["w2"]))
+    return d
+
+
+def test_training_step_against_autograd():
+    moe, d = _moe(), _step_case()
+    T, H = d["x"].shape
+    E, k, I = 6, 2, 96
+    # NaN in freed memory, so that an unwritten row that is read would show
+    torch.cuda.empty_cache()
+    torch.full((1 << 24,), float("nan"), device="cuda")
+    got = _step(moe, d)
+    torch.cuda.synchronize()
+    # the same step in float64 by autograd, without any rounding
+    live = torch.ones(T, dtype=torch.bool)
+    live[5:9] = False
+    x = torch.where(live[:, None], d["x"].double().cpu(), 0).requires_grad_()
+    z = d["logits"].double().cpu().requires_grad_()
+    w1, w2 = (d[n].double().cpu().requires_grad_() for n in ("w1", "w2"))
+    ids = got["ids"].cpu().long()
+    ix = ids.clamp(min=0)
+    p = torch.softmax(z, 1)
+    v = p.gather(1, ix)
+    w = (v / v.sum(1, keepdim=True)) * live[:, None]
+    pre = torch.einsum("th,tknh->tkn", x, w1[ix])
+    h = torch.nn.functional.silu(pre[..., :I]) * pre[..., I:]
+    y = (torch.einsum("tki,tkni->tkn", h, w2[ix]) * w[:, :, None]).sum(1)
+    n = int(live.sum())
+    f = torch.bincount(ix[live].reshape(-1), minlength=E).double() / (n * k)
+    loss = torch.stack([E * (f * p[live].mean(0)).sum(), (torch.logsumexp(z[live], 1) ** 2).mean()])
+    ((y * d["dy"].double().cpu()).sum() + (loss * d["dlosses"].double().cpu()).sum()).backward()
+    np.testing.assert_allclose(got["losses"].cpu().numpy(), loss.detach().numpy(), rtol=1e-5)
+
+    # relative to the largest entry. Forward: four bf16 roundings (pre, h, C,
+    # y), 4 * 2^-8. Backward: those and the MXFP8 roundings of x and pre, each
+    # 2^-4 of an element (2^-3 where a block's maximum saturates) whose effects
+    # add up like random signs over at least 8 terms: 2 * 2^-3 / sqrt(8) + 8 * 2^-8
+    for name, ref, tol in (("y", y, 2.0 ** -6), ("dz", z.grad, 0.12), ("dw1", w1.grad, 0.12), ("dw2", w2.grad, 0.12),
+                           ("dx", x.grad, 0.12)):
+        r, g = ref.detach().numpy(), f64(got[name])
+        assert np.isfinite(g).all(), name
+        err = np.abs(g - r).max() / np.abs(r).max()
+        assert err <= tol, (name, err)
+    assert (got["y"][5:9] == 0).all() and (got["dz"][5:9] == 0).all() and (got["dx"][5:9] == 0).all()
+
+
+def test_training_step_captured_and_replayed():
+    moe, d = _moe(), _step_case()
+    ref = {n: t.clone() for n, t in _step(moe, d).items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(moe, d)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = _step(moe, d)
+    for i in range(3):
+        for t in out.values():
+            t.fill_(-3)
+        eager = _step(moe, d)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in ref:
+            assert torch.equal(out[n], ref[n]) and torch.equal(eager[n], ref[n]), (i, n)
