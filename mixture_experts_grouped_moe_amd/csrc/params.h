@@ -81,7 +81,10 @@ struct RouteParams {
   int32_t* num_routed;
   float* prob_sum;
   float* losses;
-  // partial statistics in the workspace, one row per workgroup
+  // partial statistics in the workspace, one row per workgroup; the finishing
+  // kernel's partial products and its ticket
+  double* part_b;
+  int32_t* ticket;
   float* part_p;
   int32_t* part_c;
   float* part_z;

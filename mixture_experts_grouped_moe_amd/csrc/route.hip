@@ -2,96 +2,202 @@
 // its per-expert counts and probability sums, the balance and z losses, and
 // their gradient.
 //
-// One wave per token row: lane l holds the VPL consecutive experts
-// [VPL l, VPL l + VPL). The row's maximum, sum of exponentials and top-k are
-// wave reductions over registers, so the logits are read once and nothing of
-// size T x E is written by the forward pass. The probabilities are not kept:
-// the backward pass recomputes them from the logits, which it would have to
-// read in their place.
+// Forward (top_k <= 16). LPR lanes hold a row (8 up to 256 experts, so a wave
+// takes 8 rows at once and its cross-lane steps serve all of them), VPL
+// logits each, read once in whole cache lines. The top-k is a merge, not k
+// rounds of a maximum: every lane sorts its logits in groups of L >= top_k
+// with a fixed network, merges the groups keeping L, and log2(LPR) exchanges
+// merge the lanes' lists, after which every lane has the row's list. Keys
+// carry the expert's index below the logit (route_util.h), so ties need no
+// extra step and ordering a pair takes two instructions. Taking the maximum k
+// times over one row per wave cost 335 us on 65536 x 256 fp32 logits with
+// top 8 and statistics; the logits' bytes take 14 us at the copy rate.
+// Wider top_k (up to 64): k rounds of a wave's maximum, one row per wave.
 //
-// Statistics: each wave adds its rows' probabilities into registers, a
-// workgroup adds its waves' in order and writes one partial row per
-// workgroup; a second launch adds those in order (in double) and forms the
-// losses. No floating-point atomics, so repeated calls give equal bits.
+// Backward: the same layout. The probabilities are not kept by the forward
+// pass but recomputed from the logits, which the gradient would otherwise
+// replace by a read of the same size. The chosen experts' terms go through a
+// row of LDS that is zero otherwise, so adding them costs one scattered write
+// and one read however many there are.
+//
+// Statistics: each lane adds its rows' probabilities into registers, a
+// workgroup adds its lanes' and writes one partial row, and a second launch
+// adds those in order (in double) and forms the losses. No floating-point
+// atomics, so repeated calls give equal bits. Scores and sums are fp32, the
+// token counts integers.
 #include <type_traits>
 
 #include "common.h"
 #include "params.h"
+#include "route_util.h"
 
 namespace moe {
 
-constexpr int kRtWaves = 4;
+constexpr int kRtWaves = 8;
 constexpr int kRtThreads = kRtWaves * 64;
-constexpr int kRtMaxGrid = 512;      // workgroups of the row kernels, the partial rows of the statistics
-constexpr int kRtFinThreads = 1024;
+constexpr int kRtMaxGrid = 512;   // workgroups of the row kernels: partial rows of the statistics
+constexpr int kRtListMax = 16;    // widest top_k of the merging kernel
+constexpr int kRtFinThreads = 512;
+constexpr int kRtFinExperts = 16; // experts per workgroup of the finishing kernel
 
-__device__ __forceinline__ float rt_neg_inf() { return -__builtin_huge_valf(); }
-
-__device__ __forceinline__ float rt_load(const float* p) { return *p; }
-__device__ __forceinline__ float rt_load(const uint16_t* p) { return bf16_bits_to_f32(*p); }
-__device__ __forceinline__ void rt_store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void rt_store(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
-
-template <class F>
-__device__ __forceinline__ float rt_reduce(float v, F f) {
+// One partial row of a workgroup: its LDS sums s_p[waves][width], its counts,
+// routed tokens and squared log sums.
+template <int WIDTH>
+__device__ __forceinline__ void rt_write_partial(const RouteParams& p, const float (&s_p)[kRtWaves][WIDTH],
+                                                 const int32_t* s_c, const int32_t* s_n, const float* s_z) {
+  for (int e = threadIdx.x; e < p.E; e += kRtThreads) {
+    float v = 0.0f;
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = f(v, __shfl_xor(v, d, 64));
-  return v;
-}
-__device__ __forceinline__ float rt_sum(float v) {
-  return rt_reduce(v, [](float a, float b) { return a + b; });
-}
-__device__ __forceinline__ float rt_max(float v) {
-  return rt_reduce(v, [](float a, float b) { return fmaxf(a, b); });
-}
-
-// log of the unnormalised score: z itself, or log sigmoid(z) without
-// cancellation on either side (NaN stays NaN)
-__device__ __forceinline__ float rt_log_score(float z, bool sigmoid) {
-  if (!sigmoid) return z;
-  return (z > 0.0f ? 0.0f : z) - log1pf(expf(-fabsf(z)));
-}
-
-// A row's logits and log scores in registers with its maximum and sum.
-template <int VPL>
-struct RtRow {
-  float z[VPL], a[VPL];
-  float m, s;  // maximum of a, sum of exp(a - m)
-
-  template <class T>
-  __device__ __forceinline__ void load(const T* row, int E, int lane, bool sigmoid) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
-      z[i] = e < E ? rt_load(row + e) : rt_neg_inf();
-    }
-    m = rt_neg_inf();
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      a[i] = rt_log_score(z[i], sigmoid);
-      m = fmaxf(m, a[i]);
-    }
-    m = rt_max(m);
-    const float m0 = m == rt_neg_inf() ? 0.0f : m;
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      a[i] -= m0;
-      s += expf(a[i]);
-    }
-    s = rt_sum(s);
+    for (int i = 0; i < kRtWaves; ++i) v += s_p[i][e];
+    p.part_p[(int64_t)blockIdx.x * p.E + e] = v;
+    p.part_c[(int64_t)blockIdx.x * p.E + e] = s_c[e];
   }
-};
+  if (threadIdx.x == 0) {
+    int n = 0;
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRtWaves; ++i) {
+      n += s_n[i];
+      z += s_z[i];
+    }
+    p.part_n[blockIdx.x] = n;
+    p.part_z[blockIdx.x] = z;
+    if (blockIdx.x == 0) *p.ticket = 0;
+  }
+}
 
-template <class T, int VPL>
-__global__ __launch_bounds__(kRtThreads) void route_kernel(RouteParams p) {
-  __shared__ float s_p[kRtWaves][64 * VPL];
-  __shared__ int32_t s_c[64 * VPL];
+template <class T, int LPR, int VPL, int L, bool SIGMOID>
+__global__ __launch_bounds__(kRtThreads, 4) void route_kernel(RouteParams p) {
+  using V = RtVec<T>;
+  using K = typename V::key;
+  constexpr int RPW = 64 / LPR;        // rows of a wave
+  constexpr int WIDTH = LPR * VPL;
+  constexpr int G = VPL < L ? VPL : L; // logits sorted at a time
+  __shared__ float s_p[kRtWaves][WIDTH];
+  __shared__ int32_t s_c[WIDTH];
   __shared__ int32_t s_n[kRtWaves];
   __shared__ float s_z[kRtWaves];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const bool sigmoid = p.sigmoid != 0;
-  for (int e = threadIdx.x; e < 64 * VPL; e += kRtThreads) s_c[e] = 0;
+  const int l = lane % LPR, group = lane / LPR;
+  const T* logits = static_cast<const T*>(p.logits);
+  if (p.stats) {
+    for (int e = threadIdx.x; e < WIDTH; e += kRtThreads) s_c[e] = 0;
+    __syncthreads();
+  }
+  float psum[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) psum[i] = 0.0f;
+  int n = 0;
+  float z2 = 0.0f;
+  const int64_t step = (int64_t)gridDim.x * kRtWaves * RPW;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRtWaves + wave) * RPW; t0 < p.T; t0 += step) {
+    const int64_t t = t0 + group;
+    const bool on = t < p.T && (p.mask == nullptr || p.mask[t] != 0);
+    float z[VPL];
+    rt_load_row<T, LPR, VPL>(logits + t * p.ld, p.E, l, on, z);
+    typename K::type top[L];
+#pragma unroll
+    for (int g = 0; g < VPL / G; ++g) {
+      typename K::type v[L];
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int at = g * G + i;
+        v[i] = i < G ? K::make(z[i < G ? at : 0], ((at / V::N) * LPR + l) * V::N + at % V::N) : K::lowest();
+      }
+      rt_sort<K, L>(v);
+      if (g == 0) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) top[i] = v[i];
+      } else {
+        rt_merge<K, L>(top, v);
+      }
+    }
+    rt_merge_lanes<K, L, LPR>(top);
+    const float m = K::value(top[0]);
+    const float base = rt_base<SIGMOID>(m);
+    float s = 0.0f;
+    bool live = false;
+    if (p.stats || (!SIGMOID && !p.renorm)) {  // the sum over all experts
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        z[i] = rt_score<SIGMOID>(z[i], base);
+        s += z[i];
+      }
+      s = rt_sum<LPR>(s);
+      live = s != 0.0f;  // (NaN too)
+    }
+    const float inv = live ? 1.0f / s : 0.0f;
+    if (p.stats) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) psum[i] += z[i] * inv;
+      if (live && l == 0) {
+        ++n;
+        const float lse = base + rt_log(s);
+        if (!SIGMOID) z2 += lse * lse;
+      }
+    }
+    // the chosen experts' weights, and lane l's places l, l + LPR, .. of them
+    const float wbase = SIGMOID && !p.renorm ? 0.0f : base;
+    float w[L], sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      const float zj = K::value(top[j]);
+      w[j] = j < p.k && zj != rt_neg_inf() ? rt_score<SIGMOID>(zj, wbase) : 0.0f;
+      sum += w[j];
+    }
+    float f = p.scale;
+    if (p.renorm)
+      f = sum != 0.0f ? f / sum : 0.0f;
+    else if (!SIGMOID)
+      f *= inv;
+    if (t < p.T) {
+#pragma unroll
+      for (int j0 = 0; j0 < L; j0 += LPR) {
+        float wj = 0.0f;
+        int id = -1;
+#pragma unroll
+        for (int j = j0; j < j0 + LPR && j < L; ++j)
+          if (j - j0 == l) {
+            wj = w[j] * f;
+            id = K::value(top[j]) != rt_neg_inf() ? K::expert(top[j]) : -1;
+          }
+        const int j = j0 + l;
+        if (j < p.k && j < L) {
+          p.ids[t * p.k + j] = id;
+          p.w[t * p.k + j] = id >= 0 ? wj : 0.0f;
+          if (p.stats && id >= 0) atomicAdd(&s_c[id], 1);
+        }
+      }
+    }
+  }
+  if (!p.stats) return;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const float v = rt_sum_rows<LPR>(psum[i]);
+    if (group == 0) s_p[wave][((i / V::N) * LPR + l) * V::N + i % V::N] = v;
+  }
+  const float zz = rt_sum_rows<LPR>(z2);
+  const float nn = rt_sum_rows<LPR>((float)n);  // at most rows per wave: exact
+  if (lane == 0) {
+    s_n[wave] = (int)nn;
+    s_z[wave] = zz;
+  }
+  __syncthreads();
+  rt_write_partial(p, s_p, s_c, s_n, s_z);
+}
+
+// top_k > 16: one wave per row, VPL consecutive experts per lane, top_k
+// rounds of the row's maximum.
+template <class T, int VPL, bool SIGMOID>
+__global__ __launch_bounds__(kRtThreads) void route_wide_kernel(RouteParams p) {
+  using V = RtVec<T>;
+  constexpr int WIDTH = 64 * VPL;
+  __shared__ float s_p[kRtWaves][WIDTH];
+  __shared__ int32_t s_c[WIDTH];
+  __shared__ int32_t s_n[kRtWaves];
+  __shared__ float s_z[kRtWaves];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  for (int e = threadIdx.x; e < WIDTH; e += kRtThreads) s_c[e] = 0;
   __syncthreads();
   float psum[VPL];
 #pragma unroll
@@ -99,61 +205,62 @@ __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteParams p) {
   int n = 0;
   float z2 = 0.0f;
   for (int64_t t = (int64_t)blockIdx.x * kRtWaves + wave; t < p.T; t += (int64_t)gridDim.x * kRtWaves) {
-    int sel = -1;        // lane j < k: the expert in place j and its log score
-    float sel_z = 0.0f;
-    float w = 0.0f;
+    int sel = -1;  // lane j < k: the expert in place j and its logit
+    float sel_z = rt_neg_inf(), w = 0.0f;
     if (p.mask == nullptr || p.mask[t] != 0) {
-      RtRow<VPL> r;
-      r.load((const T*)p.logits + t * p.ld, p.E, lane, sigmoid);
-      // the top-k by the logits themselves; -inf and NaN are never chosen
-      float key[VPL];
-      bool nan = false;
+      const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+      float z[VPL], key[VPL];
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        nan |= r.z[i] != r.z[i];
-        key[i] = r.z[i] == r.z[i] ? r.z[i] : rt_neg_inf();
+        const int e = lane * VPL + i;
+        z[i] = e < p.E ? V::one(row + e) : rt_neg_inf();
+        key[i] = z[i] == z[i] ? z[i] : rt_neg_inf();
       }
       for (int j = 0; j < p.k; ++j) {
         float best = key[0];
 #pragma unroll
         for (int i = 1; i < VPL; ++i) best = fmaxf(best, key[i]);
-        const float top = rt_max(best);
+        const float top = rt_max<64>(best);
         if (top == rt_neg_inf()) break;
         const int owner = __builtin_ctzll(__ballot(best == top));
-        int e = 0;
+        int at = 0;
 #pragma unroll
         for (int i = VPL - 1; i >= 0; --i)
-          if (key[i] == top) e = i;
+          if (key[i] == top) at = i;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-          if (lane == owner && i == e) key[i] = rt_neg_inf();
-        const int id = owner * VPL + __builtin_amdgcn_readlane(e, owner);
+          if (lane == owner && i == at) key[i] = rt_neg_inf();
+        const int id = owner * VPL + __builtin_amdgcn_readlane(at, owner);
         if (lane == j) {
           sel = id;
           sel_z = top;
         }
       }
-      const bool any_nan = __ballot(nan) != 0;
-      const bool live = __ballot(sel >= 0) != 0 || any_nan;
-      const float inv = 1.0f / r.s;
-      if (sel >= 0) {
-        const float a = rt_log_score(sel_z, sigmoid);
-        if (p.renorm)
-          w = expf(a - rt_log_score(__shfl(sel_z, 0, 64), sigmoid));
-        else
-          w = sigmoid ? 1.0f / (1.0f + expf(-sel_z)) : expf(a - r.m) * inv;
+      const float m = __shfl(sel_z, 0, 64);
+      const float base = rt_base<SIGMOID>(m);
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        z[i] = rt_score<SIGMOID>(z[i], base);
+        s += z[i];
       }
-      if (p.renorm) {
-        const float sum = rt_sum(w);
-        if (sel >= 0) w = w / sum;
-      }
-      w *= p.scale;
+      s = rt_sum<64>(s);
+      const bool live = s != 0.0f;
+      const float inv = live ? 1.0f / s : 0.0f;
+      w = sel >= 0 ? rt_score<SIGMOID>(sel_z, SIGMOID && !p.renorm ? 0.0f : base) : 0.0f;
+      const float sum = rt_sum<64>(w);
+      float f = p.scale;
+      if (p.renorm)
+        f = sum != 0.0f ? f / sum : 0.0f;
+      else if (!SIGMOID)
+        f *= inv;
+      w = sel >= 0 ? w * f : 0.0f;
       if (p.stats && live) {
         ++n;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) psum[i] += expf(r.a[i]) * inv;
-        const float lse = r.m + logf(r.s);
-        if (!sigmoid) z2 += lse * lse;
+        for (int i = 0; i < VPL; ++i) psum[i] += z[i] * inv;
+        const float lse = base + rt_log(s);
+        if (!SIGMOID) z2 += lse * lse;
         if (sel >= 0) atomicAdd(&s_c[sel], 1);
       }
     }
@@ -170,195 +277,325 @@ __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteParams p) {
     s_z[wave] = z2;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kRtThreads) {
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kRtWaves; ++i) v += s_p[i][e];
-    p.part_p[(int64_t)blockIdx.x * p.E + e] = v;
-    p.part_c[(int64_t)blockIdx.x * p.E + e] = s_c[e];
-  }
-  if (threadIdx.x == 0) {
-    int nn = 0;
-    float zz = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kRtWaves; ++i) {
-      nn += s_n[i];
-      zz += s_z[i];
-    }
-    p.part_n[blockIdx.x] = nn;
-    p.part_z[blockIdx.x] = zz;
-  }
+  rt_write_partial(p, s_p, s_c, s_n, s_z);
 }
 
-// The partial rows of `grid` workgroups, added in order; the losses.
+// The partial rows of `grid` workgroups, added in order (32 threads an
+// expert take every 32nd row, then are added in order); the workgroup that
+// finishes last forms the losses from the sums of all.
 __global__ __launch_bounds__(kRtFinThreads) void route_finish_kernel(RouteParams p, int grid) {
-  __shared__ double s_b[kRtFinThreads];
-  double b = 0.0;
-  for (int e = threadIdx.x; e < p.E; e += kRtFinThreads) {
-    double v = 0.0;
-    int64_t c = 0;
-    for (int g = 0; g < grid; ++g) {
+  constexpr int ROWS = kRtFinThreads / kRtFinExperts;
+  __shared__ double s_v[ROWS][kRtFinExperts];
+  __shared__ int32_t s_k[ROWS][kRtFinExperts];
+  __shared__ int s_last;
+  const int col = threadIdx.x % kRtFinExperts, row = threadIdx.x / kRtFinExperts;
+  const int e = blockIdx.x * kRtFinExperts + col;
+  double v = 0.0;
+  int32_t c = 0;
+  if (e < p.E)
+#pragma unroll 4
+    for (int g = row; g < grid; g += ROWS) {
       v += (double)p.part_p[(int64_t)g * p.E + e];
       c += p.part_c[(int64_t)g * p.E + e];
     }
-    p.prob_sum[e] = (float)v;
-    p.counts[e] = (int32_t)c;
-    b += (double)c * v;
+  s_v[row][col] = v;
+  s_k[row][col] = c;
+  __syncthreads();
+  if (row == 0) {
+    for (int r = 1; r < ROWS; ++r) {
+      v += s_v[r][col];
+      c += s_k[r][col];
+    }
+    if (e < p.E) {
+      p.prob_sum[e] = (float)v;
+      p.counts[e] = c;
+    }
+    s_v[0][col] = v * (double)c;
   }
-  s_b[threadIdx.x] = b;
   __syncthreads();
   if (threadIdx.x == 0) {
-    double sum = 0.0, z = 0.0;
-    int64_t n = 0;
-    for (int i = 0; i < kRtFinThreads; ++i) sum += s_b[i];
-    for (int g = 0; g < grid; ++g) {
-      n += p.part_n[g];
-      z += (double)p.part_z[g];
+    double b = 0.0;
+    for (int i = 0; i < kRtFinExperts; ++i) b += s_v[0][i];
+    __hip_atomic_store(&p.part_b[blockIdx.x], b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = __hip_atomic_fetch_add(p.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  double z = 0.0;
+  int32_t n = 0;
+  for (int g = threadIdx.x; g < grid; g += kRtFinThreads) {
+    z += (double)p.part_z[g];
+    n += p.part_n[g];
+  }
+  double* s_z = &s_v[0][0];
+  int32_t* s_n = &s_k[0][0];
+  s_z[threadIdx.x] = z;
+  s_n[threadIdx.x] = n;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    z = 0.0;
+    n = 0;
+    for (int i = threadIdx.x; i < kRtFinThreads; i += 64) {
+      z += s_z[i];
+      n += s_n[i];
     }
-    *p.num_routed = (int32_t)n;
-    p.losses[0] = n > 0 ? (float)(sum * (double)p.E / ((double)p.k * (double)n * (double)n)) : 0.0f;
-    p.losses[1] = n > 0 ? (float)(z / (double)n) : 0.0f;
+    double b = (int)threadIdx.x < (int)gridDim.x  // at most 64 workgroups: 1024 experts
+                   ? __hip_atomic_load(&p.part_b[threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                   : 0.0;
+#pragma unroll
+    for (int d = 32; d >= 1; d /= 2) {
+      z += __shfl_xor(z, d, 64);
+      b += __shfl_xor(b, d, 64);
+      n += __shfl_xor(n, d, 64);
+    }
+    if (threadIdx.x == 0) {
+      *p.num_routed = n;
+      p.losses[0] = n > 0 ? (float)(b * (double)p.E / ((double)p.k * (double)n * (double)n)) : 0.0f;
+      p.losses[1] = n > 0 ? (float)(z / (double)n) : 0.0f;
+    }
   }
 }
 
-template <class T, int VPL>
-__global__ __launch_bounds__(kRtThreads) void route_backward_kernel(RouteParams p) {
-  __shared__ float s_u[kRtWaves][64 * VPL];
+// NJ: places of a row per lane (top_k <= NJ * LPR).
+template <class T, int LPR, int VPL, int NJ, bool SIGMOID>
+__global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RouteParams p) {
+  using V = RtVec<T>;
+  constexpr int RPW = 64 / LPR;
+  constexpr int WIDTH = LPR * VPL + 32;  // (rows a bank group apart)
+  __shared__ float s_u[kRtWaves][RPW][WIDTH];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const bool sigmoid = p.sigmoid != 0;
-  float* su = s_u[wave];
-  float cost[VPL];
-  float zcoef = 0.0f;
+  const int l = lane % LPR, group = lane / LPR;
+  float* su = s_u[wave][group];
+  float cost[VPL], zcoef = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
+    const int e = ((i / V::N) * LPR + l) * V::N + i % V::N;
+    su[e] = 0.0f;
     cost[i] = 0.0f;
-    su[lane * VPL + i] = 0.0f;
   }
   if (p.dlosses != nullptr) {
     const float n = (float)max(*p.num_routed, 1);
     const float f = p.dlosses[0] * (float)p.E / ((float)p.k * n * n);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
+      const int e = ((i / V::N) * LPR + l) * V::N + i % V::N;
       if (e < p.E) cost[i] = f * (float)p.counts[e];
     }
-    if (!sigmoid) zcoef = 2.0f * p.dlosses[1] / n;
+    if (!SIGMOID) zcoef = 2.0f * p.dlosses[1] / n;
   }
-  for (int64_t t = (int64_t)blockIdx.x * kRtWaves + wave; t < p.T; t += (int64_t)gridDim.x * kRtWaves) {
-    T* out = (T*)p.dlogits + t * p.dld;
-    const int32_t* ids = p.ids + t * p.k;
-    if (ids[0] < 0) {
+  const int64_t step = (int64_t)gridDim.x * kRtWaves * RPW;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRtWaves + wave) * RPW; t0 < p.T; t0 += step) {
+    const int64_t t = t0 + group;
+    const bool on = t < p.T && p.ids[t * p.k] >= 0;
+    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+    float z[VPL];
+    rt_load_row<T, LPR, VPL>(row, p.E, l, on, z);
+    // the chosen experts in places l, l + LPR, ..
+    int id[NJ];
+    float g[NJ], zj[NJ];
+    float top = rt_neg_inf();
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane * VPL + i < p.E) rt_store(out + lane * VPL + i, 0.0f);
-      continue;
+    for (int jj = 0; jj < NJ; ++jj) {
+      const int j = jj * LPR + l;
+      id[jj] = on && j < p.k ? p.ids[t * p.k + j] : -1;
+      const bool ok = (uint32_t)id[jj] < (uint32_t)p.E;
+      id[jj] = ok ? id[jj] : -1;
+      zj[jj] = ok ? V::one(row + id[jj]) : rt_neg_inf();
+      g[jj] = ok ? p.scale * p.dw[t * p.k + j] : 0.0f;
+      top = fmaxf(top, zj[jj]);
     }
-    const T* row = (const T*)p.logits + t * p.ld;
-    RtRow<VPL> r;
-    r.load(row, p.E, lane, sigmoid);
-    const float inv = 1.0f / r.s;
-    const int id = lane < p.k ? ids[lane] : -1;
-    const bool chosen = id >= 0 && id < p.E;
-    float v = 0.0f, g = 0.0f;
-    if (chosen) {
-      const float z = rt_load(row + id);
-      const float a = rt_log_score(z, sigmoid);
-      g = p.scale * p.dw[t * p.k + lane];
-      if (p.renorm || !sigmoid)
-        v = expf(a - r.m);
-      else
-        v = 1.0f / (1.0f + expf(-z));
+    float m = rt_neg_inf();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, z[i]);
+    m = rt_max<LPR>(m);
+    const float base = rt_base<SIGMOID>(m);
+    float x[VPL], s = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      x[i] = rt_score<SIGMOID>(z[i], base);
+      s += x[i];
+      dot += x[i] * cost[i];
     }
-    float u, total = 0.0f;
+    s = rt_sum<LPR>(s);
+    const float inv = s != 0.0f ? 1.0f / s : 0.0f;
+    dot = rt_sum<LPR>(dot) * inv;
+    float common = -dot;
+    if (!SIGMOID) common += zcoef * (base + rt_log(s));
+    // u_j
+    float v[NJ], sum = 0.0f, gv = 0.0f;
+    const float vbase = p.renorm ? rt_base<SIGMOID>(rt_max<LPR>(top)) : SIGMOID ? 0.0f : base;
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj) {
+      v[jj] = id[jj] >= 0 ? rt_score<SIGMOID>(zj[jj], vbase) : 0.0f;
+      sum += v[jj];
+      gv += g[jj] * v[jj];
+    }
     if (p.renorm) {
-      // softmax over the chosen, relative to their own maximum
-      float a = chosen ? rt_log_score(rt_load(row + id), sigmoid) : rt_neg_inf();
-      const float top = rt_max(a);
-      v = chosen ? expf(a - top) : 0.0f;
-      v = v / rt_sum(v);
-      const float gv = rt_sum(g * v);
-      u = v * (g - gv);
-    } else if (!sigmoid) {
-      u = v * inv * g;
-      total = rt_sum(u);
+      sum = rt_sum<LPR>(sum);
+      const float is = sum != 0.0f ? 1.0f / sum : 0.0f;
+      gv = rt_sum<LPR>(gv) * is;
+#pragma unroll
+      for (int jj = 0; jj < NJ; ++jj) v[jj] = v[jj] * is * (g[jj] - gv);
+    } else if (!SIGMOID) {
+      common -= rt_sum<LPR>(gv) * inv;
+#pragma unroll
+      for (int jj = 0; jj < NJ; ++jj) v[jj] *= inv * g[jj];
     } else {
-      u = v * g;
+#pragma unroll
+      for (int jj = 0; jj < NJ; ++jj) v[jj] *= g[jj];
     }
-    if (chosen) su[id] = u;
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj)
+      if (id[jj] >= 0) su[id[jj]] = v[jj];
     __builtin_amdgcn_wave_barrier();
-    float q[VPL], dot = 0.0f;
+    T* out = static_cast<T*>(p.dlogits) + t * p.dld;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      q[i] = expf(r.a[i]) * inv;
-      dot += q[i] * cost[i];
-    }
-    dot = rt_sum(dot);
-    float common = -dot - total;
-    if (!sigmoid) common += zcoef * (r.m + logf(r.s));
+    for (int c = 0; c < VPL / V::N; ++c) {
+      const int e = (c * LPR + l) * V::N;
+      typename V::vec o;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
-      if (e < p.E) {
-        float d = q[i] * (cost[i] + common) + su[e];
-        if (sigmoid) d *= 1.0f / (1.0f + expf(r.z[i]));
-        rt_store(out + e, d);
+      for (int i = 0; i < V::N; ++i) {
+        const int at = c * V::N + i;
+        float d = x[at] * inv * (cost[at] + common) + su[e + i];
+        if (SIGMOID) d *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[at] * 1.44269504f));  // 1 - sigmoid(z)
+        d = on ? d : 0.0f;
+        if (e + V::N <= p.E)
+          V::put(o, i, d);
+        else if (t < p.T && e + i < p.E)
+          V::put(out + e + i, d);
       }
+      if (t < p.T && e + V::N <= p.E) *reinterpret_cast<typename V::vec*>(out + e) = o;
     }
     __builtin_amdgcn_wave_barrier();
-    if (chosen) su[id] = 0.0f;
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj)
+      if (id[jj] >= 0) su[id[jj]] = 0.0f;
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-static uint32_t rt_grid(int64_t T) {
-  const int64_t want = (T + kRtWaves - 1) / kRtWaves;
+// Rows that one workgroup takes at a time.
+static int rt_rows(int E, bool wide) { return wide ? kRtWaves : kRtWaves * (E <= 128 ? 8 : E <= 256 ? 4 : E <= 512 ? 2 : 1); }
+
+static uint32_t rt_grid(int64_t T, int rows) {
+  const int64_t want = (T + rows - 1) / rows;
   return (uint32_t)(want < kRtMaxGrid ? want : kRtMaxGrid);
 }
 
-// Workspace: partial counts and probability sums [grid][E], tokens and z
-// sums [grid] (4-byte elements).
+// Workspace for either forward kernel: the finishing kernel's 64 partial
+// products (8 bytes each) and ticket, the partial probability sums and
+// counts [grid][E], z sums and tokens [grid].
 int64_t route_workspace_bytes(int64_t T, int32_t E) {
-  return (int64_t)rt_grid(T) * ((int64_t)E + 1) * 8;
+  return 64 * 8 + 8 + (int64_t)rt_grid(T, kRtWaves) * ((int64_t)E + 1) * 8;
 }
 
+template <int N>
+using rt_c = std::integral_constant<int, N>;
+
+// f(type, LPR, VPL) for the row layout of E experts.
 template <class F>
-static hipError_t rt_dispatch(int E, bool bf16, F&& f) {
-  auto by_type = [&](auto vpl) {
-    if (bf16) f(uint16_t{}, vpl); else f(float{}, vpl);
+static void rt_layout(int E, bool bf16, F&& f) {
+  auto by_type = [&](auto lpr, auto vpl) {
+    if (bf16)
+      f(uint16_t{}, lpr, vpl);
+    else
+      f(float{}, lpr, vpl);
   };
-  if (E <= 64) by_type(std::integral_constant<int, 1>{});
-  else if (E <= 128) by_type(std::integral_constant<int, 2>{});
-  else if (E <= 256) by_type(std::integral_constant<int, 4>{});
-  else if (E <= 512) by_type(std::integral_constant<int, 8>{});
-  else by_type(std::integral_constant<int, 16>{});
-  return hipGetLastError();
+  if (E <= 64)
+    by_type(rt_c<8>{}, rt_c<8>{});
+  else if (E <= 128)
+    by_type(rt_c<8>{}, rt_c<16>{});
+  else if (E <= 256)
+    by_type(rt_c<16>{}, rt_c<16>{});
+  else if (E <= 512)
+    by_type(rt_c<32>{}, rt_c<16>{});
+  else
+    by_type(rt_c<64>{}, rt_c<16>{});
 }
 
 hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t stream) {
-  const uint32_t grid = rt_grid(p.T);
+  const bool wide = p.k > kRtListMax;
+  const uint32_t grid = rt_grid(p.T, rt_rows(p.E, wide));
   if (p.stats) {
-    p.part_p = static_cast<float*>(workspace);
+    p.part_b = static_cast<double*>(workspace);
+    p.ticket = reinterpret_cast<int32_t*>(p.part_b + 64);
+    p.part_p = reinterpret_cast<float*>(p.ticket + 2);
     p.part_c = reinterpret_cast<int32_t*>(p.part_p + (int64_t)grid * p.E);
     p.part_z = reinterpret_cast<float*>(p.part_c + (int64_t)grid * p.E);
     p.part_n = reinterpret_cast<int32_t*>(p.part_z + grid);
   }
-  hipError_t err = hipSuccess;
-  if (grid > 0)
-    err = rt_dispatch(p.E, bf16, [&](auto t, auto vpl) {
-      hipLaunchKernelGGL((route_kernel<decltype(t), decltype(vpl)::value>), dim3(grid), dim3(kRtThreads), 0, stream, p);
+  // (no tokens: one workgroup without a row still writes the empty statistics)
+  const uint32_t blocks = grid > 0 ? grid : (p.stats ? 1 : 0);
+  if (blocks == 0) return hipSuccess;
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kRtThreads), 0, stream, p);
+  };
+  auto by_score = [&](auto with) {
+    if (p.sigmoid)
+      with(std::true_type{});
+    else
+      with(std::false_type{});
+  };
+  if (wide) {
+    auto go = [&](auto t, auto vpl) {
+      by_score([&](auto sig) { launch(route_wide_kernel<decltype(t), decltype(vpl)::value, decltype(sig)::value>); });
+    };
+    auto by_type = [&](auto vpl) {
+      if (bf16)
+        go(uint16_t{}, vpl);
+      else
+        go(float{}, vpl);
+    };
+    if (p.E <= 64)
+      by_type(rt_c<1>{});
+    else if (p.E <= 256)
+      by_type(rt_c<4>{});
+    else
+      by_type(rt_c<16>{});
+  } else {
+    rt_layout(p.E, bf16, [&](auto t, auto lpr, auto vpl) {
+      by_score([&](auto sig) {
+        using T = decltype(t);
+        constexpr int R = decltype(lpr)::value, N = decltype(vpl)::value;
+        constexpr bool S = decltype(sig)::value;
+        if (p.k <= 4)
+          launch(route_kernel<T, R, N, 4, S>);
+        else if (p.k <= 8)
+          launch(route_kernel<T, R, N, 8, S>);
+        else
+          launch(route_kernel<T, R, N, 16, S>);
+      });
     });
+  }
+  hipError_t err = hipGetLastError();
   if (err != hipSuccess || !p.stats) return err;
-  hipLaunchKernelGGL(route_finish_kernel, dim3(1), dim3(kRtFinThreads), 0, stream, p, (int)grid);
+  hipLaunchKernelGGL(route_finish_kernel, dim3((p.E + kRtFinExperts - 1) / kRtFinExperts), dim3(kRtFinThreads), 0,
+                     stream, p, (int)blocks);
   return hipGetLastError();
 }
 
 hipError_t launch_route_backward(const RouteParams& p, bool bf16, hipStream_t stream) {
-  const uint32_t grid = rt_grid(p.T);
+  const uint32_t grid = rt_grid(p.T, rt_rows(p.E, false));
   if (grid == 0) return hipSuccess;
-  return rt_dispatch(p.E, bf16, [&](auto t, auto vpl) {
-    hipLaunchKernelGGL((route_backward_kernel<decltype(t), decltype(vpl)::value>), dim3(grid), dim3(kRtThreads), 0,
-                       stream, p);
+  rt_layout(p.E, bf16, [&](auto t, auto lpr, auto vpl) {
+    using T = decltype(t);
+    constexpr int R = decltype(lpr)::value, N = decltype(vpl)::value;
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kRtThreads), 0, stream, p); };
+    auto by_score = [&](auto nj) {
+      constexpr int J = decltype(nj)::value;
+      if (p.sigmoid)
+        launch(route_backward_kernel<T, R, N, J, true>);
+      else
+        launch(route_backward_kernel<T, R, N, J, false>);
+    };
+    if (p.k <= R)
+      by_score(rt_c<1>{});
+    else if (p.k <= 2 * R)
+      by_score(rt_c<2>{});
+    else
+      by_score(rt_c<64 / R>{});
   });
+  return hipGetLastError();
 }
 
 }  // namespace moe
