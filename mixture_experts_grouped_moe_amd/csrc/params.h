@@ -112,6 +112,11 @@ struct ActParams {
   int64_t dh_ld;
   uint16_t* dpre;
   int64_t dpre_ld;
+  // set by the launch: its first row, its 8-column pieces, those of a row and
+  // the division by them
+  int64_t row0;
+  uint32_t units, row_units, magic;
+  int32_t shift;
 };
 
 hipError_t launch_align(const int32_t* ids, int32_t S, int32_t E, int32_t B, int32_t* sorted_ids,

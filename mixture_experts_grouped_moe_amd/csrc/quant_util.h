@@ -2,6 +2,8 @@
 // quantizer (quant.hip) and the activation with a checkpoint (act.hip).
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace moe {
@@ -62,6 +64,39 @@ __device__ __forceinline__ uint32_t mx_quantize_block(const u32x4_t (&v)[4], u32
       out[j / 2][2 * (j % 2) + w / 2] = __builtin_bit_cast(uint32_t, r);
     }
   return (uint32_t)(X + 127);
+}
+
+// The same for a block spread over four neighbouring lanes (a lane quad, all
+// active), 8 elements each: v -> this lane's 8 codes in out; the result, the
+// block's scale byte, is the same in the four.
+__device__ __forceinline__ uint32_t mx_quantize_quarter(const u32x4_t v, u32x2_t& out) {
+  auto mag = [](uint32_t d) { return __builtin_bit_cast(q_v2u16, d & 0x7FFF7FFFu); };
+  q_v2u16 m = __builtin_elementwise_max(__builtin_elementwise_max(mag(v[0]), mag(v[1])),
+                                        __builtin_elementwise_max(mag(v[2]), mag(v[3])));
+  auto other = [&](auto ctrl) {
+    const int x = __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, m), decltype(ctrl)::value, 0xF, 0xF, true);
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(q_v2u16, x));
+  };
+  other(std::integral_constant<int, 0xB1>{});  // lane ^ 1
+  other(std::integral_constant<int, 0x4E>{});  // lane ^ 2
+  const uint32_t amax = max((uint32_t)m[0], (uint32_t)m[1]);
+  const int e = (int)(amax >> 7);
+  const int X = e == 0 ? -127 : max(e - 127 - 8, -127);  // (255 - 135 < 127)
+  const float scale = __uint_as_float((uint32_t)(X + 127) << 23);
+  const uint32_t lim = ((uint32_t)(135 + X) << 7) | 0x60u;
+  const uint32_t lim2 = lim | (lim << 16);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const uint32_t lo = clamp_pair(v[2 * w], lim2), hi = clamp_pair(v[2 * w + 1], lim2);
+    q_v2s r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(q_v2bf, lo), scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(q_v2bf, hi), scale, true);
+    out[w] = __builtin_bit_cast(uint32_t, r);
+  }
+  const bool bad = amax >= 0x7F80u;  // a NaN or an infinity in the block
+  out[0] = bad ? 0x7F7F7F7Fu : out[0];
+  out[1] = bad ? 0x7F7F7F7Fu : out[1];
+  return bad ? 0xFFu : (uint32_t)(X + 127);
 }
 
 }  // namespace moe

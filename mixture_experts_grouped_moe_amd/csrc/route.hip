@@ -136,37 +136,37 @@ __global__ __launch_bounds__(kRtThreads, 4) void route_kernel(RouteParams p) {
         if (!SIGMOID) z2 += lse * lse;
       }
     }
-    // the chosen experts' weights, and lane l's places l, l + LPR, .. of them
+    // the chosen experts: lane l takes places l, l + LPR, .. of the row's list
+    constexpr int NJ = (L + LPR - 1) / LPR;
     const float wbase = SIGMOID && !p.renorm ? 0.0f : base;
-    float w[L], sum = 0.0f;
+    int id[NJ];
+    float w[NJ], sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-      const float zj = K::value(top[j]);
-      w[j] = j < p.k && zj != rt_neg_inf() ? rt_score<SIGMOID>(zj, wbase) : 0.0f;
-      sum += w[j];
+    for (int jj = 0; jj < NJ; ++jj) {
+      typename K::type key = top[jj * LPR];
+#pragma unroll
+      for (int j = 1; j < LPR && jj * LPR + j < L; ++j)
+        if (l == j) key = top[jj * LPR + j];
+      const float zj = K::value(key);
+      const bool ok = jj * LPR + l < p.k && (LPR <= L || l < L) && zj != rt_neg_inf();
+      id[jj] = ok ? K::expert(key) : -1;
+      w[jj] = ok ? rt_score<SIGMOID>(zj, wbase) : 0.0f;
+      sum += w[jj];
     }
     float f = p.scale;
-    if (p.renorm)
+    if (p.renorm) {
+      sum = rt_sum<LPR>(sum);
       f = sum != 0.0f ? f / sum : 0.0f;
-    else if (!SIGMOID)
+    } else if (!SIGMOID) {
       f *= inv;
-    if (t < p.T) {
+    }
 #pragma unroll
-      for (int j0 = 0; j0 < L; j0 += LPR) {
-        float wj = 0.0f;
-        int id = -1;
-#pragma unroll
-        for (int j = j0; j < j0 + LPR && j < L; ++j)
-          if (j - j0 == l) {
-            wj = w[j] * f;
-            id = K::value(top[j]) != rt_neg_inf() ? K::expert(top[j]) : -1;
-          }
-        const int j = j0 + l;
-        if (j < p.k && j < L) {
-          p.ids[t * p.k + j] = id;
-          p.w[t * p.k + j] = id >= 0 ? wj : 0.0f;
-          if (p.stats && id >= 0) atomicAdd(&s_c[id], 1);
-        }
+    for (int jj = 0; jj < NJ; ++jj) {
+      const int j = jj * LPR + l;
+      if (t < p.T && j < p.k) {
+        p.ids[t * p.k + j] = id[jj];
+        p.w[t * p.k + j] = id[jj] >= 0 ? w[jj] * f : 0.0f;
+        if (p.stats && id[jj] >= 0) atomicAdd(&s_c[id[jj]], 1);
       }
     }
   }

@@ -28,7 +28,7 @@ __device__ __forceinline__ RtPair rt_pair(uint32_t x) {
     return {r[0], r[1]};
   } else {
     constexpr int ctrl = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;
-    return {x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, 0xF, 0xF, true)};
+    return {x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, ctrl, 0xF, 0xF, true)};
   }
 }
 
@@ -57,7 +57,7 @@ __device__ __forceinline__ float rt_max(float x) {
 template <int LPR, int D = LPR>
 __device__ __forceinline__ float rt_sum_rows(float x) {
   if constexpr (D == 8) {  // rotate the 16-lane row by 8: l and l ^ 8
-    const int y = __builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), 0x128, 0xF, 0xF, true);
+    const int y = __builtin_amdgcn_mov_dpp((int)__float_as_uint(x), 0x128, 0xF, 0xF, true);
     return rt_sum_rows<LPR, 16>(x + __uint_as_float((uint32_t)y));
   } else if constexpr (D < 64) {
     const RtPair p = rt_pair<D>(__float_as_uint(x));
@@ -70,13 +70,16 @@ __device__ __forceinline__ float rt_sum_rows(float x) {
 // Keys: a total order by logit (largest first), equal logits by expert
 // (lowest first), with the expert recoverable. NaN ranks as -inf; -0 as 0.
 //
+// The bits of z with NaN as -inf and -0 as 0 (the sum is never -0 and quiet,
+// and the maximum takes its other operand for a NaN).
+__device__ __forceinline__ uint32_t rt_rankable(float z) { return __float_as_uint(fmaxf(z + 0.0f, rt_neg_inf())); }
+
 // bf16 logits: the ordered 16 bits above the inverted index, as a uint32.
 struct RtKey16 {
   using type = uint32_t;
   __device__ static type lowest() { return 0x007F0000u; }  // -inf, no expert
   __device__ static type make(float z, int e) {
-    z = (z == z ? z : rt_neg_inf()) + 0.0f;
-    const uint32_t u = __float_as_uint(z);
+    const uint32_t u = rt_rankable(z);
     const uint32_t o = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
     return (o & 0xFFFF0000u) | (0xFFFFu - (uint32_t)e);
   }
@@ -105,8 +108,7 @@ struct RtKey32 {
   }
   __device__ static type lowest() { return bits(0xFF800000u, 0xFFFFFFFFu); }
   __device__ static type make(float z, int e) {
-    z = (z == z ? z : rt_neg_inf()) + 0.0f;
-    const uint32_t u = __float_as_uint(z);
+    const uint32_t u = rt_rankable(z);
     // a larger low half is a larger magnitude: the inverted index for
     // positive logits, the index itself for negative ones
     return bits(u, ~(uint32_t)e ^ (uint32_t)((int32_t)u >> 31));
@@ -203,6 +205,15 @@ struct RtVec<uint16_t> {
 template <class T, int LPR, int VPL>
 __device__ __forceinline__ void rt_load_row(const T* row, int E, int l, bool on, float (&z)[VPL]) {
   using V = RtVec<T>;
+  if (E == LPR * VPL && __all(on)) {  // the usual case, without a choice per lane
+#pragma unroll
+    for (int c = 0; c < VPL / V::N; ++c) {
+      const typename V::vec v = *reinterpret_cast<const typename V::vec*>(row + (c * LPR + l) * V::N);
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) z[c * V::N + i] = V::get(v, i);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) z[i] = rt_neg_inf();
   if (!on) return;
