@@ -31,7 +31,7 @@ FLAGS = [
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
 SOURCES = ["api.cpp", "align.hip", "gemm.hip", "decode.hip", "decode_layer.hip", "combine.hip", "wgrad.hip", "pack.hip",
-           "quant.hip", "gemm_f8.hip", "api_train.cpp", "route.hip", "act.hip"]
+           "quant.hip", "gemm_f8.hip", "api_train.cpp", "route.hip", "act.hip", "wgrad_mxfp8.hip"]
 
 
 def _hipcc():

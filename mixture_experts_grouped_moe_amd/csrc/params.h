@@ -61,7 +61,7 @@ struct WgradParams {
   uint32_t topk_magic;  // slot s's token row s / top_k = (s * topk_magic) >> topk_shift
   int32_t topk_shift;
   float* dw;
-  // x as MXFP8 (wgrad_kernel<true>): codes through x / x_ld (bytes), scales here
+  // x as MXFP8 (wgrad_mxfp8.hip): codes through x / x_ld (bytes), scales here
   const uint8_t* xs;
   int64_t xs_ld;
 };

@@ -57,17 +57,10 @@
 //    rows and columns that are never stored.
 #include "common.h"
 #include "params.h"
+#include "wgrad_util.h"
 
 namespace moe {
 
-constexpr int kWgBM = 64;                    // routing block
-constexpr int kWgUM = 32;                    // slots per pipeline unit
-constexpr int kWgTN = 256;                   // dW rows (N) per tile
-constexpr int kWgTK = 256;                   // dW columns (K) per tile
-constexpr int kWgGRowB = kWgTN * 2;          // 512 B: a slot's grad piece
-constexpr int kWgXRowB = kWgTK * 2;          // 512 B: a slot's x piece
-constexpr int kWgGUnitB = kWgUM * kWgGRowB;  // 16 KB
-constexpr int kWgXUnitB = kWgUM * kWgXRowB;  // 16 KB
 constexpr int kWgStageB = kWgGUnitB + kWgXUnitB;
 constexpr int kWgStages = 4;                 // two pairs of units
 constexpr int kWgWaves = 8;
@@ -76,96 +69,11 @@ constexpr int kWgGLoads = kWgGUnitB / 1024 / kWgWaves;  // DMA instructions per 
 constexpr int kWgXLoads = kWgXUnitB / 1024 / kWgWaves;  //   + 2 x (2 rows each)
 constexpr int kWgStores = 8 * 4;             // 16-byte stores per lane per tile
 constexpr int kWgPerCU = 1;                  // resident workgroups per CU
-constexpr int kWgMaxExperts = 1024;
-constexpr int kWgRawUnitB = kWgUM * kWgTK;   // 8 KB: a unit of x as E4M3 codes
-constexpr int kWgRawPairB = 2 * (kWgRawUnitB + kWgThreads * 4);  // a pair of units: codes, one scale dword per lane
-constexpr int kWgGroupN = 8;                 // N tiles per group of the tile order
-constexpr uint32_t kWgOOB = 0x80000000u;     // buffer offset past x, grad and one expert's dW (each below 2 GB)
-constexpr int kWgStoreNT = 2;                // cache-policy bits of the dW stores: non-temporal
 static_assert(kWgGLoads == 2 && kWgXLoads == 2, "each wave loads the same 4 slot rows of both parts");
 
-typedef __attribute__((address_space(3))) uint8_t wg_lds_u8_t;
-typedef __attribute__((__vector_size__(4 * sizeof(short)))) short wg_s16x4_t;
-
-// Physical 16-byte unit of logical unit u in LDS row (slot) m. A
-// transposing read covers 4 consecutive slots x 2 consecutive units per
-// 16-lane group; XOR-ing the unit with 4 (m % 4) moves the four slots' pieces
-// 64 bytes apart, onto distinct banks (rows are 256 or 512 bytes long).
-__device__ __forceinline__ int wg_swz(int m, int u) { return u ^ ((m % 4) * 4); }
-
-// 16 bytes per lane from `rsrc` at `voff` into LDS at lds_base + 16 * lane.
-__device__ __forceinline__ void wg_dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds"
-               :: "v"(voff), "s"(__builtin_amdgcn_readfirstlane(lds_base)), "s"(rsrc) : "m0");
-}
-
-typedef __attribute__((__vector_size__(4 * sizeof(int)))) int wg_i32x4_t;
-
-// 4 consecutive int32 at byte `off` of buffer `rsrc` through the scalar
-// cache (a read). Asynchronous: the result must not be used before an
-// lgkmcnt(0) wait that lists it (wg_wait_barrier).
-__device__ __forceinline__ wg_i32x4_t wg_scalar_ids4(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
-  wg_i32x4_t v;
-  asm volatile("s_buffer_load_dwordx4 %0, %1, %2"
-               : "=s"(v) : "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(off)));
-  return v;
-}
-
-// Wait until at most N of this wave's vector-memory operations are in
-// flight and every LDS and scalar-memory operation is done, then barrier;
-// `a` and `b` (prefetched scalar loads) are final from here on.
-template <int N>
-__device__ __forceinline__ void wg_wait_barrier(wg_i32x4_t& a, wg_i32x4_t& b) {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%2) lgkmcnt(0)\n\ts_barrier" : "+s"(a), "+s"(b) : "n"(N) : "memory");
-}
-
-// Operand of 8 consecutive slots [m0, m0 + 8) of tile column c0 + lane % 32,
-// for the 32-wide MFMA fragment: lane l takes column c0 + l % 32 and slots
-// m0 + 8 (l / 32) + i. Built from two transposing reads (slots +0..3, +4..7)
-// of an LDS part whose rows are ROWB bytes.
-template <int ROWB>
-__device__ __forceinline__ bf16x8_t wg_operand(const wg_lds_u8_t* part, int c0, int m0, int lane) {
-  const int g = lane / 16, s = lane % 16;
-  const int col = c0 + 16 * (g % 2) + 4 * (s % 4);
-  const int slot = m0 + 8 * (g / 2) + s / 4;
-  bf16x8_t r;
-  wg_s16x4_t v[2];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int m = slot + 4 * half;
-    const int byte = m * ROWB + wg_swz(m, col / 8) * 16 + (col % 8) * 2;
-    v[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) wg_s16x4_t*)(part + byte));
-  }
-  __builtin_memcpy(&r, v, 16);
-  return r;
-}
-
-// A tile of dW and its expert's block range.
-struct WgTile {
-  int e, n0, k0, b0, b1;
-};
-
-// One byte per lane from `rsrc` at `voff` into LDS, zero-extended to the dword
-// at lds_base + 4 * lane.
-__device__ __forceinline__ void wg_dma_byte(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_ubyte %0, %2, 0 offen lds"
-               :: "v"(voff), "s"(__builtin_amdgcn_readfirstlane(lds_base)), "s"(rsrc) : "m0");
-}
-
-// MX: x comes as E4M3 codes with E8M0 scales. Its pieces (half the bytes) go
-// one pair of units further ahead into an LDS area of their own by the same
-// DMA; before a pair's products, each wave decodes the pieces of the next
-// pair that it loaded itself (so no barrier is needed between) to bf16, which
-// is exact, into the stage where the products will read them. Every element
-// is decoded once per tile; decoding at the operand reads would repeat it in
-// the four waves that share a column.
-template <bool MX>
 __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams p) {
   // four stages of [grad unit | x unit], slot-major
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kWgStages][kWgStageB];
-  __shared__ __attribute__((aligned(1024))) uint8_t raw[MX ? kWgRawPairB : 16];
   __shared__ int32_t s_start[kWgMaxExperts + 1];  // first block of expert e (s_start[E] = end)
 
   const int tid = threadIdx.x;
@@ -173,67 +81,20 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int l32 = lane % 32, h = lane / 32;
 
-  // ---- expert block ranges: experts (lo, hi] start at every block b where
-  //      the expert id changes (lo = previous id, hi = this id, or E for the
-  //      first sentinel); experts past the last boundary start at max_blocks
-  for (int e = tid; e <= p.E; e += kWgThreads) s_start[e] = p.max_blocks;
-  __syncthreads();
-  for (int b = tid; b < p.max_blocks; b += kWgThreads) {
-    const int cur = p.expert_ids[b];
-    const int prev = b > 0 ? p.expert_ids[b - 1] : -1;
-    const int hi = (cur < 0 || cur > p.E) ? p.E : cur;
-    const int lo = (b == 0 || prev < 0) ? -1 : prev;
-    if ((b == 0 || prev != cur) && !(prev < 0 && cur < 0 && b > 0))
-      for (int e = lo + 1; e <= hi; ++e) s_start[e] = b;
-  }
-  __syncthreads();
+  wg_block_ranges<kWgThreads>(p, s_start);
+  const WgOrder order(p, s_start);
+  const int total = order.total;
+  auto tile_index = [&](int it) { return order.index(it); };
+  auto tile_at = [&](int T) { return order.at(T); };
 
-  // Tile order: expert-major; within an expert, groups of kWgGroupN N tiles
-  // walked N-fastest then K, so any kWgGroupN x (64 / kWgGroupN) consecutive
-  // tiles share a few grad and x slices. XCD x (= hardware id % 8) owns the
-  // x-th eighth of the sequence, and its G/8 workgroups take consecutive
-  // tiles of it round by round (G = gridDim.x).
-  const int per_e = p.tiles_n * p.tiles_k;
-  const int total = p.E * per_e;  // below 2^31 (checked by the host API)
-  const int G = gridDim.x;
-  const int xcd = blockIdx.x % 8, local = blockIdx.x / 8;
-  const int chunk = (total + 7) / 8;
-  auto tile_index = [&](int it) -> int {
-    const int q = it * (G / 8) + local;
-    const int T = xcd * chunk + q;
-    return (q < chunk && T < total) ? T : total;
-  };
-  auto tile_at = [&](int T) {
-    WgTile t;
-    t.e = T / per_e;
-    const int r = T % per_e;
-    const int in_group = kWgGroupN * p.tiles_k;
-    const int first_n = (r / in_group) * kWgGroupN;
-    const int gsize = min(p.tiles_n - first_n, kWgGroupN);
-    t.n0 = (first_n + (r % in_group) % gsize) * kWgTN;
-    t.k0 = ((r % in_group) / gsize) * kWgTK;
-    t.b0 = __builtin_amdgcn_readfirstlane(s_start[t.e]);
-    t.b1 = __builtin_amdgcn_readfirstlane(s_start[t.e + 1]);
-    return t;
-  };
-
-  // (the buffers end with their last row's last element: a view's last row
-  // may end with its allocation)
-  const int64_t T = p.S / p.top_k;
-  constexpr int XB = MX ? 1 : 2;  // bytes of an element of x
-  auto span = [](int64_t rows, int64_t ld, int64_t width, int bytes) {
-    return (int)(uint32_t)(rows > 0 ? ((rows - 1) * ld + width) * bytes : 0);
-  };
-  const __amdgpu_buffer_rsrc_t g_rsrc =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.grad, 0, span(p.S, p.grad_ld, p.N, 2), 0x00020000);
-  const __amdgpu_buffer_rsrc_t x_rsrc =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, span(T, p.x_ld, p.K, XB), 0x00020000);
-  const __amdgpu_buffer_rsrc_t xs_rsrc =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.xs, 0, MX ? span(T, p.xs_ld, p.K / 32, 1) : 0, 0x00020000);
+  const __amdgpu_buffer_rsrc_t g_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)p.grad, 0, (int)(uint32_t)((int64_t)p.S * p.grad_ld * 2), 0x00020000);
+  const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)p.x, 0, (int)(uint32_t)((int64_t)(p.S / p.top_k) * p.x_ld * 2), 0x00020000);
   const __amdgpu_buffer_rsrc_t sorted_rsrc = __builtin_amdgcn_make_buffer_rsrc(
       (void*)p.sorted, 0, (int)(uint32_t)((int64_t)p.max_blocks * kWgBM * 4), 0x00020000);
   const uint32_t lds_base = (uint32_t)(uintptr_t)(wg_lds_u8_t*)&lds[0][0];
-  const uint32_t g_row = (uint32_t)(p.grad_ld * 2), x_row = (uint32_t)(p.x_ld * XB);
+  const uint32_t g_row = (uint32_t)(p.grad_ld * 2), x_row = (uint32_t)(p.x_ld * 2);
 
   // ---- loader: walks the same tiles' units one pair ahead of the
   //      computation. Unit u of a tile is slots [32u, 32u + 32) of its block
@@ -280,112 +141,40 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
   ld_ids_pair(ids, ids_b);
   wg_wait_barrier<0>(ids, ids_b);
 
-  // token row of slot s
-  auto token_row = [&](uint32_t sl) {
-    const uint64_t prod = ((uint64_t)__umulhi(sl, p.topk_magic) << 32) | (sl * p.topk_magic);
-    return (uint32_t)(prod >> p.topk_shift);
-  };
-  // scalar row offsets of the wave's 4 slots of a unit within the tile's
-  // column range (a PAD slot s = S lands at or past the end of the buffers;
-  // past the last tile the ids are 0 and the bases put every lane past
-  // the buffers: s * row + kWgOOB stays below 2^32)
-  auto issue_grad = [&](int stage, const wg_i32x4_t& uid, uint32_t g_base) {
-    uint32_t go[4];
+  auto issue_unit = [&](int stage, const wg_i32x4_t& uid) {
+    // scalar row offsets of the wave's 8 slots within the tile's column
+    // range (a PAD slot s = S lands at or past the end of both buffers)
+    // (past the last tile the ids are 0 and the bases put every lane past
+    // the buffers: s * row + kWgOOB stays below 2^32)
+    const uint32_t g_base = ld_live ? (uint32_t)ld.n0 * 2 : kWgOOB;
+    const uint32_t x_base = ld_live ? (uint32_t)ld.k0 * 2 : kWgOOB;
+    uint32_t go[4], xo[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) go[r] = (uint32_t)uid[r] * g_row + g_base;
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t s = (uint32_t)uid[r];
+      const uint64_t prod = ((uint64_t)__umulhi(s, p.topk_magic) << 32) | (s * p.topk_magic);
+      const uint32_t xrow = (uint32_t)(prod >> p.topk_shift);
+      go[r] = s * g_row + g_base;
+      xo[r] = xrow * x_row + x_base;
+    }
     const uint32_t dst = lds_base + (uint32_t)(stage * kWgStageB);
 #pragma unroll
     for (int i = 0; i < kWgGLoads; ++i)
       wg_dma16(g_rsrc, pick(xm1, go[2 * i + 1], go[2 * i]) + (i % 2 ? x_col1 : x_col0),
                dst + (uint32_t)((wave * kWgGLoads + i) * 1024));
-  };
-  auto issue_x = [&](int stage, const wg_i32x4_t& uid, uint32_t x_base) {
-    uint32_t xo[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) xo[r] = token_row((uint32_t)uid[r]) * x_row + x_base;
-    const uint32_t dst = lds_base + (uint32_t)(stage * kWgStageB);
 #pragma unroll
     for (int i = 0; i < kWgXLoads; ++i)
       wg_dma16(x_rsrc, pick(xm1, xo[2 * i + 1], xo[2 * i]) + (i % 2 ? x_col1 : x_col0),
                dst + (uint32_t)(kWgGUnitB + (wave * kWgXLoads + i) * 1024));
   };
-  // MX: the wave's 4 rows of 256 code bytes in one load (16 lanes a row), and
-  // for every lane the scale byte of its 16 columns
-  const uint32_t raw_base = (uint32_t)(uintptr_t)(wg_lds_u8_t*)&raw[0];
-  const uint32_t ym1 = lane & 16 ? ~0u : 0u;
-  auto issue_raw = [&](int unit, const wg_i32x4_t& uid, uint32_t x_base, uint32_t s_base) {
-    uint32_t xo[4], so[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint32_t row = token_row((uint32_t)uid[r]);
-      xo[r] = row * x_row + x_base;
-      so[r] = row * (uint32_t)p.xs_ld + s_base;
-    }
-    wg_dma16(x_rsrc, pick(xm1, pick(ym1, xo[3], xo[2]), pick(ym1, xo[1], xo[0])) + (uint32_t)(lane % 16) * 16,
-             raw_base + (uint32_t)(unit * kWgRawUnitB + wave * 1024));
-    wg_dma_byte(xs_rsrc, pick(xm1, pick(ym1, so[3], so[2]), pick(ym1, so[1], so[0])) + (uint32_t)(lane % 16) / 2,
-                raw_base + (uint32_t)(2 * kWgRawUnitB + unit * kWgThreads * 4 + wave * 256));
-  };
-  // MX: this wave's pieces of the pair in `raw`, decoded into the x parts of
-  // stages stage, stage + 1
-  auto decode_raw = [&](int stage) {
-    const wg_lds_u8_t* src = (const wg_lds_u8_t*)&raw[0];
-#pragma unroll
-    for (int unit = 0; unit < 2; ++unit) {
-      const u32x4_t c = *(const __attribute__((address_space(3))) u32x4_t*)(src + unit * kWgRawUnitB + wave * 1024 +
-                                                                            lane * 16);
-      const uint32_t b = *(const __attribute__((address_space(3))) uint32_t*)(src + 2 * kWgRawUnitB +
-                                                                              (unit * kWgThreads + wave * 64 + lane) * 4);
-      const float scale = e8m0_as_scale(b);
-      const bf16x8_t v0 = dequant_e4m3x8(c[0], c[1], scale), v1 = dequant_e4m3x8(c[2], c[3], scale);
-      const int m = wave * 4 + lane / 16, u = 2 * (lane % 16);
-      wg_lds_u8_t* dst = (wg_lds_u8_t*)&lds[stage + unit][kWgGUnitB + m * kWgXRowB];
-      *(__attribute__((address_space(3))) bf16x8_t*)(dst + wg_swz(m, u) * 16) = v0;
-      *(__attribute__((address_space(3))) bf16x8_t*)(dst + wg_swz(m, u + 1) * 16) = v1;
-    }
-    // the reads are done before the next pair's codes may overwrite `raw`
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  };
-  // moves the loader to the next pair and starts its ids' loads, complete by
-  // the next wait
-  auto ld_next = [&]() {
+  auto issue_pair = [&](int stage) {  // stages stage, stage + 1
+    issue_unit(stage, ids);
+    issue_unit(stage + 1, ids_b);
     if (ld_live) {
       ld_u += 2;
       ld_skip_empty();
-      ld_ids_pair(ids, ids_b);
+      ld_ids_pair(ids, ids_b);  // complete by the next wait
     }
-  };
-  // !MX: the pair the loader points at, into stages stage, stage + 1
-  auto issue_pair = [&](int stage) {
-    const uint32_t g_base = ld_live ? (uint32_t)ld.n0 * 2 : kWgOOB;
-    const uint32_t x_base = ld_live ? (uint32_t)ld.k0 * 2 : kWgOOB;
-    issue_grad(stage, ids, g_base);
-    issue_x(stage, ids, x_base);
-    issue_grad(stage + 1, ids_b, g_base);
-    issue_x(stage + 1, ids_b, x_base);
-    ld_next();
-  };
-  // MX: the codes of the pair the loader points at, whose ids and grad base
-  // are kept for its gradient loads one pair later
-  wg_i32x4_t g_ids, g_ids_b;
-  uint32_t g_base_kept = 0;
-  auto issue_raw_pair = [&]() {
-    const uint32_t x_base = ld_live ? (uint32_t)ld.k0 : kWgOOB;
-    const uint32_t s_base = ld_live ? (uint32_t)ld.k0 / 32 : kWgOOB;
-    issue_raw(0, ids, x_base, s_base);
-    issue_raw(1, ids_b, x_base, s_base);
-    g_ids = ids;
-    g_ids_b = ids_b;
-    g_base_kept = ld_live ? (uint32_t)ld.n0 * 2 : kWgOOB;
-    ld_next();
-  };
-  // MX: the next pair's gradients and decoded x into stages stage, stage + 1,
-  // then the codes of the pair after it
-  auto advance_mx = [&](int stage) {
-    issue_grad(stage, g_ids, g_base_kept);
-    issue_grad(stage + 1, g_ids_b, g_base_kept);
-    decode_raw(stage);
-    issue_raw_pair();
   };
 
   // waves 4 x 2: wave (wn, wk) computes dW rows n0 + wn*64 .. + 63 and
@@ -420,13 +209,7 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
   //      before them); the barrier makes every wave's DMA visible and
   //      guarantees all waves finished the previous pair, whose two stages
   //      the loads issued next overwrite.
-  if constexpr (MX) {
-    issue_raw_pair();
-    wg_wait_barrier<0>(ids, ids_b);
-    advance_mx(0);
-  } else {
-    issue_pair(0);
-  }
+  issue_pair(0);
   int st = 0;  // first stage of the next pair computed
   bool stored = false;
   for (int it = 0; tile_index(it) < total; ++it) {
@@ -445,10 +228,7 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
       } else {
         wg_wait_barrier<0>(ids, ids_b);
       }
-      if constexpr (MX)  // the stages of the pair computed last, now free
-        advance_mx(st ^ 2);
-      else
-        issue_pair(st ^ 2);
+      issue_pair(st ^ 2);  // the pair computed last, now free
       contract(st);
       contract(st + 1);
       st ^= 2;
@@ -496,19 +276,11 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
 
 int wgrad_block_m() { return kWgBM; }
 
-template <bool MX>
-static hipError_t wg_launch(const WgradParams& p_in, hipStream_t stream) {
+hipError_t launch_wgrad(const WgradParams& p_in, hipStream_t stream) {
   WgradParams p = p_in;
   p.tiles_n = (p.N + kWgTN - 1) / kWgTN;
   p.tiles_k = (p.K + kWgTK - 1) / kWgTK;
-  // division by top_k as a multiply-high: with l = ceil(log2 d) and
-  // m = ceil(2^(31+l) / d), floor(s / d) = (s m) >> (31 + l) for every
-  // s < 2^31 (Granlund and Montgomery, "Division by invariant integers using
-  // multiplication", 1994, Theorem 4.2 with N = 31)
-  int l = 0;
-  while ((1 << l) < p.top_k) ++l;
-  p.topk_magic = (uint32_t)((((uint64_t)1 << (31 + l)) + (uint64_t)p.top_k - 1) / (uint64_t)p.top_k);
-  p.topk_shift = 31 + l;
+  wg_set_division(p);
   const int64_t tiles = (int64_t)p.E * p.tiles_n * p.tiles_k;
   if (tiles == 0) return hipSuccess;
   int dev = 0, cus = 0;
@@ -519,11 +291,8 @@ static hipError_t wg_launch(const WgradParams& p_in, hipStream_t stream) {
   // stretch of tiles per XCD per round)
   int64_t grid = (int64_t)cus * kWgPerCU;
   grid = (grid + 7) / 8 * 8;
-  hipLaunchKernelGGL(wgrad_kernel<MX>, dim3((uint32_t)grid), dim3(kWgThreads), 0, stream, p);
+  hipLaunchKernelGGL(wgrad_kernel, dim3((uint32_t)grid), dim3(kWgThreads), 0, stream, p);
   return hipGetLastError();
 }
-
-hipError_t launch_wgrad(const WgradParams& p, hipStream_t stream) { return wg_launch<false>(p, stream); }
-hipError_t launch_wgrad_mxfp8(const WgradParams& p, hipStream_t stream) { return wg_launch<true>(p, stream); }
 
 }  // namespace moe

@@ -29,7 +29,7 @@ import functools
 
 import torch
 
-from . import _ACTS, _check, _need, lib, MOE_BF16, MOE_FP32, moe_wgrad_block_m
+from . import _ACTS, _check, _need, lib, MOE_BF16, MOE_FP32
 
 __all__ = [
     "moe_route", "moe_route_workspace_bytes", "moe_route_backward", "moe_combine_routed", "moe_combine_backward",
@@ -62,12 +62,25 @@ def _bind():
 _bind()
 
 
+# Calls on small inputs are bound by the host: launching takes 4.3 us, so what
+# the binding adds to it is kept short (a stream object would take 2.8 us,
+# torch.empty 0.4 us more than torch.empty_strided).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+@functools.lru_cache(maxsize=None)
+def _one_device():
+    return torch.cuda.device_count() < 2
+
+
 def _on_stream(f):
     """Runs f with `stream` (default: the current stream of the first tensor's
     device) and its device current, so that what f allocates belongs to the
     stream that its kernels run on."""
     @functools.wraps(f)
     def call(*args, stream=None, **kw):
+        if stream is None and _one_device():
+            return f(*args, **kw)
         first = args[0] if args else next(iter(kw.values()), None)
         on_gpu = isinstance(first, torch.Tensor) and first.is_cuda
         if stream is None:
@@ -82,41 +95,51 @@ def _on_stream(f):
     return call
 
 
-# the current stream's handle alone: a torch.cuda.Stream object takes 2.8 us of
-# a call that spends 4.3 us launching its kernel
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream():
+def _stream(t):
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(t.get_device())
 
 
 def _same_device(first, *others):
-    dev = first.device
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
 
 
-def _ld(t):
-    """Row stride of a 2-d tensor; of a single row, whose stride means nothing, a legal one."""
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+def _new(t, rows, width, dtype):
+    """An uninitialised [rows, width] on t's device."""
+    return torch.empty_strided((rows, width), (width, 1), dtype=dtype, device=t.device)
+
+
+def _mat(t, name, dtype, rows=None, width=None):
+    """Checks a 2-d device tensor whose rows are contiguous, of at least `rows`
+    rows and exactly `width` columns where given; (rows, columns, row stride).
+    A single row's stride means nothing: a legal one is returned."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or t.dim() != 2:
+        _need(t, name, dtype, 2)
+    (r, c), (ld, one) = t.shape, t.stride()
+    if one != 1 and r * c:
+        _need(t, name, dtype, 2)
+    if rows is not None and (r < rows or c != width):
+        raise ValueError(f"{name} must be [{rows}, {width}], got {[r, c]}")
+    return r, c, ld if r > 1 else -(-c // 16) * 16
 
 
 def _flat(t, name, dtype, shape):
-    """A contiguous tensor of this dtype and shape."""
-    _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    """Checks a contiguous device tensor of this shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or t.dim() != len(shape):
+        _need(t, name, dtype, len(shape))
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)}, got {list(t.shape)}")
 
 
-def _rows(t, name, dtype, rows, width):
-    """A 2-d tensor of exactly this width and at least these rows."""
-    _need(t, name, dtype, 2)
-    if t.shape[0] < rows or t.shape[1] != width:
-        raise ValueError(f"{name} must be [{rows}, {width}], got {list(t.shape)}")
+def _logits(t):
+    """(T, E, row stride) of the router's logits."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _LOGITS:
+        raise TypeError("logits must be a float32 or bfloat16 tensor")
+    return _mat(t, "logits", t.dtype)
 
 
 def moe_route_workspace_bytes(num_tokens, num_experts):
@@ -143,19 +166,12 @@ def moe_route(logits, top_k, score="softmax", renormalize=True, scale=1.0, mask=
     two or six tensors; `workspace` a uint8 tensor of moe_route_workspace_bytes
     (calls that may run at the same time need one each).
     """
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGITS:
-        raise TypeError("logits must be a float32 or bfloat16 tensor")
-    _need(logits, "logits", logits.dtype, 2)
-    T, E = logits.shape
+    T, E, ld = _logits(logits)
     k, dev = int(top_k), logits.device
-    if mask is not None:
-        if not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.uint8, torch.bool):
-            raise TypeError("mask must be a uint8 or bool tensor")
-        _flat(mask, "mask", mask.dtype, (T,))
     if out is None:
         if not 1 <= k <= E:
             raise ValueError(f"need 1 <= top_k ({k}) <= num_experts ({E})")
-        out = (torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev))
+        out = (_new(logits, T, k, torch.int32), _new(logits, T, k, torch.float32))
         if balance:
             out += (torch.empty(E, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.int32, device=dev),
                     torch.empty(E, dtype=torch.float32, device=dev), torch.empty(2, dtype=torch.float32, device=dev))
@@ -169,9 +185,14 @@ def moe_route(logits, top_k, score="softmax", renormalize=True, scale=1.0, mask=
                 ((T, k), (T, k), (E,), (1,), (E,), (2,))):
             _flat(t, name, dtype, shape)
         _same_device(logits, *out)
-    _same_device(logits, mask)
-    stats = (None,) * 4
-    ws_p, ws_n = None, 0
+    mask_p = None
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.uint8, torch.bool):
+            raise TypeError("mask must be a uint8 or bool tensor")
+        _flat(mask, "mask", mask.dtype, (T,))
+        _same_device(logits, mask)
+        mask_p = mask.data_ptr()
+    stats, ws_p, ws_n = (None,) * 4, None, 0
     if balance:
         stats = [t.data_ptr() for t in out[2:]]
         if workspace is None:
@@ -180,10 +201,9 @@ def moe_route(logits, top_k, score="softmax", renormalize=True, scale=1.0, mask=
             _need(workspace, "workspace", torch.uint8, 1)
             _same_device(logits, workspace)
         ws_p, ws_n = workspace.data_ptr(), workspace.numel()
-    _check(lib.moe_route(logits.data_ptr(), _LOGITS[logits.dtype], _ld(logits),
-                         mask.data_ptr() if mask is not None else None, T, E, k, _SCORES[score], bool(renormalize),
-                         float(scale), out[0].data_ptr(), out[1].data_ptr(), bool(balance), *stats, ws_p, ws_n,
-                         _stream()))
+    _check(lib.moe_route(logits.data_ptr(), _LOGITS[logits.dtype], ld, mask_p, T, E, k, _SCORES[score],
+                         bool(renormalize), scale, out[0].data_ptr(), out[1].data_ptr(), bool(balance), *stats, ws_p,
+                         ws_n, _stream(logits)))
     return out
 
 
@@ -195,14 +215,11 @@ def moe_route_backward(logits, topk_ids, dtopk_w, score="softmax", renormalize=T
     fp32 [2] of the losses (with the forward pass's counts and num_routed).
     logits, topk_ids, score, renormalize and scale as in the forward pass;
     the experts chosen there are held constant."""
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGITS:
-        raise TypeError("logits must be a float32 or bfloat16 tensor")
-    _need(logits, "logits", logits.dtype, 2)
-    _need(topk_ids, "topk_ids", torch.int32, 2)
-    T, E = logits.shape
-    k = topk_ids.shape[1]
+    T, E, ld = _logits(logits)
+    k = _mat(topk_ids, "topk_ids", torch.int32)[1]
     _flat(topk_ids, "topk_ids", torch.int32, (T, k))
     _flat(dtopk_w, "dtopk_w", torch.float32, (T, k))
+    losses = (None,) * 3
     if dlosses is not None:
         if counts is None or num_routed is None:
             raise ValueError("dlosses needs counts and num_routed")
@@ -210,17 +227,15 @@ def moe_route_backward(logits, topk_ids, dtopk_w, score="softmax", renormalize=T
         _flat(counts, "counts", torch.int32, (E,))
         _flat(num_routed, "num_routed", torch.int32, (1,))
         _same_device(logits, dlosses, counts, num_routed)
+        losses = counts.data_ptr(), num_routed.data_ptr(), dlosses.data_ptr()
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        out, old = _new(logits, T, E, logits.dtype), E
     else:
-        _rows(out, "out", logits.dtype, T, E)
+        old = _mat(out, "out", logits.dtype, T, E)[2]
     _same_device(logits, topk_ids, dtopk_w, out)
-    _check(lib.moe_route_backward(logits.data_ptr(), _LOGITS[logits.dtype], _ld(logits), T, E, k, _SCORES[score],
-                                  bool(renormalize), float(scale), topk_ids.data_ptr(), dtopk_w.data_ptr(),
-                                  counts.data_ptr() if dlosses is not None else None,
-                                  num_routed.data_ptr() if dlosses is not None else None,
-                                  dlosses.data_ptr() if dlosses is not None else None, out.data_ptr(), _ld(out),
-                                  _stream()))
+    _check(lib.moe_route_backward(logits.data_ptr(), _LOGITS[logits.dtype], ld, T, E, k, _SCORES[score],
+                                  bool(renormalize), scale, topk_ids.data_ptr(), dtopk_w.data_ptr(), *losses,
+                                  out.data_ptr(), old, _stream(logits)))
     return out
 
 
@@ -229,20 +244,19 @@ def moe_combine_routed(c, topk_w, topk_ids, num_experts, out=None):
     """moe_combine over the slots whose id lies in [0, num_experts): y[t] =
     sum_j topk_w[t, j] * c[t * top_k + j] (fp32, bf16 out). The other slots'
     rows of c, which the grouped GEMM leaves as they were, are not read."""
-    _need(c, "c", torch.bfloat16, 2)
-    _need(topk_ids, "topk_ids", torch.int32, 2)
-    T, k = topk_ids.shape
+    T, k, _ = _mat(topk_ids, "topk_ids", torch.int32)
     _flat(topk_ids, "topk_ids", torch.int32, (T, k))
     _flat(topk_w, "topk_w", torch.float32, (T, k))
-    N = c.shape[1]
-    _rows(c, "c", torch.bfloat16, T * k, N)
+    rows, N, cld = _mat(c, "c", torch.bfloat16)
+    if rows < T * k:
+        raise ValueError(f"c must hold {T * k} rows, got {rows}")
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=c.device)
+        out, old = _new(c, T, N, torch.bfloat16), N
     else:
-        _rows(out, "out", torch.bfloat16, T, N)
+        old = _mat(out, "out", torch.bfloat16, T, N)[2]
     _same_device(c, topk_w, topk_ids, out)
-    _check(lib.moe_combine_routed(c.data_ptr(), _ld(c), topk_w.data_ptr(), topk_ids.data_ptr(), T, k,
-                                  int(num_experts), N, out.data_ptr(), _ld(out), _stream()))
+    _check(lib.moe_combine_routed(c.data_ptr(), cld, topk_w.data_ptr(), topk_ids.data_ptr(), T, k, int(num_experts),
+                                  N, out.data_ptr(), old, _stream(c)))
     return out
 
 
@@ -255,29 +269,26 @@ def moe_combine_backward(dy, c, topk_w, topk_ids=None, num_experts=None, out=Non
     [T, top_k]; with topk_ids (int32 [T, top_k]) and num_experts, slots routed
     nowhere get zeros and their rows of c are not read. Returns (dC, dtopk_w);
     `out` may give both (not overlapping the inputs)."""
-    _need(dy, "dy", torch.bfloat16, 2)
-    _need(topk_w, "topk_w", torch.float32, 2)
-    T, k = topk_w.shape
-    N = dy.shape[1]
+    T, k, _ = _mat(topk_w, "topk_w", torch.float32)
     _flat(topk_w, "topk_w", torch.float32, (T, k))
-    _rows(dy, "dy", torch.bfloat16, T, N)
-    _rows(c, "c", torch.bfloat16, T * k, N)
+    N = _mat(dy, "dy", torch.bfloat16)[1]
+    dyld = _mat(dy, "dy", torch.bfloat16, T, N)[2]
+    cld = _mat(c, "c", torch.bfloat16, T * k, N)[2]
+    ids_p, E = None, 0
     if topk_ids is not None:
         if num_experts is None:
             raise ValueError("topk_ids needs num_experts")
         _flat(topk_ids, "topk_ids", torch.int32, (T, k))
+        ids_p, E = topk_ids.data_ptr(), int(num_experts)
     if out is None:
-        out = (torch.empty((T * k, N), dtype=torch.bfloat16, device=dy.device),
-               torch.empty((T, k), dtype=torch.float32, device=dy.device))
+        dc, dw, dcld = _new(dy, T * k, N, torch.bfloat16), _new(dy, T, k, torch.float32), N
     else:
-        _rows(out[0], "dC", torch.bfloat16, T * k, N)
-        _flat(out[1], "dtopk_w", torch.float32, (T, k))
-    dc, dw = out
+        dc, dw = out
+        dcld = _mat(dc, "dC", torch.bfloat16, T * k, N)[2]
+        _flat(dw, "dtopk_w", torch.float32, (T, k))
     _same_device(dy, c, topk_w, topk_ids, dc, dw)
-    _check(lib.moe_combine_backward(dy.data_ptr(), _ld(dy), c.data_ptr(), _ld(c), topk_w.data_ptr(),
-                                    topk_ids.data_ptr() if topk_ids is not None else None, T, k,
-                                    int(num_experts) if topk_ids is not None else 0, N, dc.data_ptr(), _ld(dc),
-                                    dw.data_ptr(), _stream()))
+    _check(lib.moe_combine_backward(dy.data_ptr(), dyld, c.data_ptr(), cld, topk_w.data_ptr(), ids_p, T, k, E, N,
+                                    dc.data_ptr(), dcld, dw.data_ptr(), _stream(dy)))
     return dc, dw
 
 
@@ -291,22 +302,20 @@ def moe_act_mxfp8(pre, activation, out=None):
     q uint8 E4M3 codes [R, N] and scales uint8 E8M0 [R, N / 32], the bits of
     moe_quantize_mxfp8(pre). `out` may give the three."""
     act = _ACTS[activation]
-    _need(pre, "pre", torch.bfloat16, 2)
-    R, N = pre.shape
-    H = N // 2 if activation == "swiglu" else N
+    R, N, pld = _mat(pre, "pre", torch.bfloat16)
+    H = N // 2 if act == 1 else N
     if out is None:
-        dev = pre.device
-        out = (torch.empty((R, H), dtype=torch.bfloat16, device=dev),
-               torch.empty((R, N), dtype=torch.uint8, device=dev),
-               torch.empty((R, N // 32), dtype=torch.uint8, device=dev))
+        h, hld = _new(pre, R, H, torch.bfloat16), H
+        q, qld = _new(pre, R, N, torch.uint8), N
+        s, sld = _new(pre, R, N // 32, torch.uint8), N // 32
     else:
-        _rows(out[0], "h", torch.bfloat16, R, H)
-        _rows(out[1], "q", torch.uint8, R, N)
-        _rows(out[2], "scales", torch.uint8, R, N // 32)
-        _same_device(pre, *out)
-    h, q, s = out
-    _check(lib.moe_act_mxfp8(act, pre.data_ptr(), _ld(pre), R, N, h.data_ptr(), _ld(h), q.data_ptr(), _ld(q),
-                             s.data_ptr(), _ld(s), _stream()))
+        h, q, s = out
+        hld = _mat(h, "h", torch.bfloat16, R, H)[2]
+        qld = _mat(q, "q", torch.uint8, R, N)[2]
+        sld = _mat(s, "scales", torch.uint8, R, N // 32)[2]
+        _same_device(pre, h, q, s)
+    _check(lib.moe_act_mxfp8(act, pre.data_ptr(), pld, R, N, h.data_ptr(), hld, q.data_ptr(), qld, s.data_ptr(), sld,
+                             _stream(pre)))
     return h, q, s
 
 
@@ -319,24 +328,21 @@ def moe_act_mxfp8_backward(q, scales, dh, activation, out=None, recompute=True):
     checkpoint for the second weights' gradient (None with recompute=False).
     `out` may give both."""
     act = _ACTS[activation]
-    _need(q, "q", torch.uint8, 2)
-    R, N = q.shape
-    H = N // 2 if activation == "swiglu" else N
-    _rows(scales, "scales", torch.uint8, R, N // 32)
-    _rows(dh, "dh", torch.bfloat16, R, H)
+    R, N, qld = _mat(q, "q", torch.uint8)
+    H = N // 2 if act == 1 else N
+    sld = _mat(scales, "scales", torch.uint8, R, N // 32)[2]
+    dhld = _mat(dh, "dh", torch.bfloat16, R, H)[2]
     if out is None:
-        dpre = torch.empty((R, N), dtype=torch.bfloat16, device=q.device)
-        h = torch.empty((R, H), dtype=torch.bfloat16, device=q.device) if recompute else None
+        dpre, dld = _new(q, R, N, torch.bfloat16), N
+        h, hld = (_new(q, R, H, torch.bfloat16), H) if recompute else (None, 0)
     else:
         dpre, h = out
-        _rows(dpre, "dpre", torch.bfloat16, R, N)
-        if h is not None:
-            _rows(h, "h", torch.bfloat16, R, H)
+        dld = _mat(dpre, "dpre", torch.bfloat16, R, N)[2]
+        hld = _mat(h, "h", torch.bfloat16, R, H)[2] if h is not None else 0
     _same_device(q, scales, dh, dpre, h)
-    _check(lib.moe_act_mxfp8_backward(act, q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales), dh.data_ptr(),
-                                      _ld(dh), R, N, dpre.data_ptr(), _ld(dpre),
-                                      h.data_ptr() if h is not None else None, _ld(h) if h is not None else 0,
-                                      _stream()))
+    _check(lib.moe_act_mxfp8_backward(act, q.data_ptr(), qld, scales.data_ptr(), sld, dh.data_ptr(), dhld, R, N,
+                                      dpre.data_ptr(), dld, h.data_ptr() if h is not None else None, hld,
+                                      _stream(q)))
     return dpre, h
 
 
@@ -347,24 +353,25 @@ def moe_wgrad_mxfp8(xq, xs, grad, routing, num_tokens, top_k, num_experts, out=N
     [T, K], xs: uint8 E8M0 [T, K / 32] (moe_quantize_mxfp8); grad, routing and
     out as for moe_wgrad."""
     T, k, E = int(num_tokens), int(top_k), int(num_experts)
-    _need(xq, "xq", torch.uint8, 2)
-    _need(grad, "grad", torch.bfloat16, 2)
-    N, K = grad.shape[1], xq.shape[1]
-    _rows(xq, "xq", torch.uint8, T, K)
-    _rows(xs, "xs", torch.uint8, T, K // 32)
-    _rows(grad, "grad", torch.bfloat16, T * k, N)
+    K = _mat(xq, "xq", torch.uint8)[1]
+    N = _mat(grad, "grad", torch.bfloat16)[1]
+    xld = _mat(xq, "xq", torch.uint8, T, K)[2]
+    sld = _mat(xs, "xs", torch.uint8, T, K // 32)[2]
+    gld = _mat(grad, "grad", torch.bfloat16, T * k, N)[2]
     sorted_ids, expert_ids, post_pad = routing
     for t, name in zip(routing, ("sorted_token_ids", "expert_ids", "num_tokens_post_pad")):
         _need(t, name, torch.int32, 1)
-    bm = moe_wgrad_block_m()
-    if sorted_ids.numel() < expert_ids.numel() * bm:
+    blocks, bm = expert_ids.numel(), lib.moe_wgrad_block_m()
+    if sorted_ids.numel() < blocks * bm:
         raise ValueError("routing arrays do not match moe_wgrad_block_m()")
     if out is None:
+        if E < 0:
+            raise ValueError(f"num_experts ({E}) is negative")
         out = torch.empty((E, N, K), dtype=torch.float32, device=xq.device)
     else:
         _flat(out, "out", torch.float32, (E, N, K))
-    _same_device(xq, xs, grad, *routing, out)
-    _check(lib.moe_wgrad_mxfp8(xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), grad.data_ptr(), _ld(grad),
-                               sorted_ids.data_ptr(), expert_ids.data_ptr(), post_pad.data_ptr(), T, k, E, N, K, bm,
-                               expert_ids.numel(), out.data_ptr(), _stream()))
+    _same_device(xq, xs, grad, sorted_ids, expert_ids, post_pad, out)
+    _check(lib.moe_wgrad_mxfp8(xq.data_ptr(), xld, xs.data_ptr(), sld, grad.data_ptr(), gld, sorted_ids.data_ptr(),
+                               expert_ids.data_ptr(), post_pad.data_ptr(), T, k, E, N, K, bm, blocks, out.data_ptr(),
+                               _stream(xq)))
     return out
