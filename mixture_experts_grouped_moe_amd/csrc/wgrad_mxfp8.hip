@@ -2,10 +2,13 @@
 // grad[s]^T xhat[s / top_k], fp32, with the activations kept as MXFP8 (E4M3
 // codes, one E8M0 scale per 32 columns).
 //
-// The tiles, their order, the ownership of dW and the transposing operand
-// reads are those of wgrad.hip (256 x 256 tiles, one persistent workgroup of
-// 8 waves per CU, every tile accumulated over its expert's routing blocks on
+// The tiles, the ownership of dW and the transposing operand reads are those
+// of wgrad.hip (256 x 256 tiles, one persistent workgroup of 8 waves per CU,
+// every tile accumulated over its expert's routing blocks on
 // v_mfma_f32_32x32x16_bf16 and written once). What differs:
+//  * Every XCD takes an eighth of each expert's tiles (WgSplitOrder): whole
+//    experts per XCD, as in wgrad.hip, left the fullest XCD 16% more blocks
+//    than the average on routing whose experts have 430 to 1750 slots.
 //  * x arrives as codes, half the bytes. An MFMA operand holds 8 slots of one
 //    column, and every slot has a scale of its own, so decoding at the operand
 //    would take a conversion per element in each of the four waves that share
@@ -81,7 +84,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   const int l32 = lane % 32, h = lane / 32;
 
   wg_block_ranges<kMxThreads>(p, s_start);
-  const WgOrder order(p, s_start);
+  const WgSplitOrder order(p, s_start);
 
   // The buffers end with their last row's last element (a view's last row
   // may end with its allocation); PAD slots (s = S) lie past them.

@@ -143,6 +143,41 @@ struct WgOrder {
   }
 };
 
+// Tile order for experts of unequal sizes: every XCD takes an eighth of each
+// expert's tiles (numbered as in WgOrder), so all XCDs have the same work
+// whatever the counts, where WgOrder gives each XCD whole experts. With
+// tiles [lo(y), lo(y + 1)), lo(y) = per_e y / 8, the y-th eighth of an expert,
+// XCD x takes eighth (x + e) % 8 of expert e, so that 8 consecutive experts
+// give it per_e tiles also where 8 does not divide per_e. Its workgroups take
+// consecutive tiles of its sequence round by round.
+struct WgSplitOrder {
+  WgOrder base;
+  int per_e, step, xcd, local;
+  int total;  // tiles of this XCD
+  __device__ __forceinline__ WgSplitOrder(const WgradParams& p, const int32_t* s_start) : base(p, s_start) {
+    per_e = base.per_e;
+    step = base.G / 8;
+    xcd = base.xcd;
+    local = base.local;
+    total = p.E / 8 * per_e;
+    for (int e = p.E / 8 * 8; e < p.E; ++e) total += lo((xcd + e) % 8 + 1) - lo((xcd + e) % 8);
+  }
+  __device__ __forceinline__ int lo(int y) const { return (int)((int64_t)per_e * y / 8); }
+  // this workgroup's it-th tile of the XCD's sequence, or total past its last
+  __device__ __forceinline__ int index(int it) const {
+    const int64_t q = (int64_t)it * step + local;
+    return q < total ? (int)q : total;
+  }
+  __device__ __forceinline__ WgTile at(int q) const {
+    int e = q / per_e * 8, r = q % per_e;
+    for (;; ++e) {
+      const int y = (xcd + e) % 8, n = lo(y + 1) - lo(y);
+      if (r < n) return base.at(e * per_e + lo(y) + r);
+      r -= n;
+    }
+  }
+};
+
 // The division by top_k of the slots' token rows: with l = ceil(log2 d) and
 // m = ceil(2^(31+l) / d), floor(s / d) = (s m) >> (31 + l) for every
 // s < 2^31 (Granlund and Montgomery, "Division by invariant integers using
