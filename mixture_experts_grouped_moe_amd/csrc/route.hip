@@ -11,7 +11,10 @@
 // carry the expert's index below the logit (route_util.h), so ties need no
 // extra step and ordering a pair takes two instructions. Taking the maximum k
 // times over one row per wave cost 335 us on 65536 x 256 fp32 logits with
-// top 8 and statistics; the logits' bytes take 14 us at the copy rate.
+// top 8 and statistics; this takes 27 us (23 and the finishing launch), where
+// the logits' bytes alone take 14 us at the rate of a large copy. What bounds
+// it is instructions: about 130 a row, two thirds of the kernel's time at one
+// per SIMD and 4 cycles. Loading a row ahead of its use changed nothing.
 // Wider top_k (up to 64): k rounds of a wave's maximum, one row per wave.
 //
 // Backward: the same layout. The probabilities are not kept by the forward
@@ -67,7 +70,7 @@ __device__ __forceinline__ void rt_write_partial(const RouteParams& p, const flo
 }
 
 template <class T, int LPR, int VPL, int L, bool SIGMOID>
-__global__ __launch_bounds__(kRtThreads, 4) void route_kernel(RouteParams p) {
+__global__ __launch_bounds__(kRtThreads, VPL > 16 ? 2 : 4) void route_kernel(RouteParams p) {
   using V = RtVec<T>;
   using K = typename V::key;
   constexpr int RPW = 64 / LPR;        // rows of a wave
@@ -474,13 +477,22 @@ __global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RoutePara
   }
 }
 
-// Rows that one workgroup takes at a time.
-static int rt_rows(int E, bool wide) { return wide ? kRtWaves : kRtWaves * (E <= 128 ? 8 : E <= 256 ? 4 : E <= 512 ? 2 : 1); }
+// Rows that one workgroup takes at a time (rt_layout, 16 and 32 logits a lane).
+static int rt_rows(int E) { return kRtWaves * (E <= 128 ? 8 : E <= 256 ? 4 : E <= 512 ? 2 : 1); }
+static int rt_rows_deep(int E) { return kRtWaves * (E <= 256 ? 8 : E <= 512 ? 4 : 2); }
 
-static uint32_t rt_grid(int64_t T, int rows) {
+static uint32_t rt_grid(int64_t T, int rows, int most = kRtMaxGrid) {
   const int64_t want = (T + rows - 1) / rows;
-  return (uint32_t)(want < kRtMaxGrid ? want : kRtMaxGrid);
+  return (uint32_t)(want < most ? want : most);
 }
+
+// Forward pass above 128 experts: 32 logits a lane instead of 16 sorts more
+// in a lane and merges less between lanes, a quarter fewer instructions, but
+// has fewer waves. It pays from where 16 a lane fill their largest grid
+// (statistics included; fp32, 256 experts top 8: 65536 tokens 29.7 -> 26.6 us,
+// 16384 16.8 -> 14.6, 4096 10.6 -> 12.6; 1024 experts: 65536 tokens
+// 112 -> 87 us, 4096 20.0 -> 16.3, 512 11.3 -> 12.5).
+static bool rt_deep(int64_t T, int E) { return E > 128 && T >= (int64_t)kRtMaxGrid * rt_rows(E); }
 
 // Workspace for either forward kernel: the finishing kernel's 64 partial
 // products (8 bytes each) and ticket, the partial probability sums and
@@ -492,9 +504,9 @@ int64_t route_workspace_bytes(int64_t T, int32_t E) {
 template <int N>
 using rt_c = std::integral_constant<int, N>;
 
-// f(type, LPR, VPL) for the row layout of E experts.
+// f(type, LPR, VPL) for the row layout of E experts: VPL at most 16, or 32.
 template <class F>
-static void rt_layout(int E, bool bf16, F&& f) {
+static void rt_layout(int E, bool bf16, bool deep, F&& f) {
   auto by_type = [&](auto lpr, auto vpl) {
     if (bf16)
       f(uint16_t{}, lpr, vpl);
@@ -505,6 +517,12 @@ static void rt_layout(int E, bool bf16, F&& f) {
     by_type(rt_c<8>{}, rt_c<8>{});
   else if (E <= 128)
     by_type(rt_c<8>{}, rt_c<16>{});
+  else if (deep && E <= 256)
+    by_type(rt_c<8>{}, rt_c<32>{});
+  else if (deep && E <= 512)
+    by_type(rt_c<16>{}, rt_c<32>{});
+  else if (deep)
+    by_type(rt_c<32>{}, rt_c<32>{});
   else if (E <= 256)
     by_type(rt_c<16>{}, rt_c<16>{});
   else if (E <= 512)
@@ -515,7 +533,10 @@ static void rt_layout(int E, bool bf16, F&& f) {
 
 hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t stream) {
   const bool wide = p.k > kRtListMax;
-  const uint32_t grid = rt_grid(p.T, rt_rows(p.E, wide));
+  const bool deep = !wide && rt_deep(p.T, p.E);
+  const uint32_t grid = wide   ? rt_grid(p.T, kRtWaves)
+                        : deep ? rt_grid(p.T, rt_rows_deep(p.E), kRtMaxGrid / 2)  // (registers: half the waves)
+                               : rt_grid(p.T, rt_rows(p.E));
   if (p.stats) {
     p.part_b = static_cast<double*>(workspace);
     p.ticket = reinterpret_cast<int32_t*>(p.part_b + 64);
@@ -553,7 +574,7 @@ hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t s
     else
       by_type(rt_c<16>{});
   } else {
-    rt_layout(p.E, bf16, [&](auto t, auto lpr, auto vpl) {
+    rt_layout(p.E, bf16, deep, [&](auto t, auto lpr, auto vpl) {
       by_score([&](auto sig) {
         using T = decltype(t);
         constexpr int R = decltype(lpr)::value, N = decltype(vpl)::value;
@@ -575,9 +596,9 @@ hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t s
 }
 
 hipError_t launch_route_backward(const RouteParams& p, bool bf16, hipStream_t stream) {
-  const uint32_t grid = rt_grid(p.T, rt_rows(p.E, false));
+  const uint32_t grid = rt_grid(p.T, rt_rows(p.E));
   if (grid == 0) return hipSuccess;
-  rt_layout(p.E, bf16, [&](auto t, auto lpr, auto vpl) {
+  rt_layout(p.E, bf16, false, [&](auto t, auto lpr, auto vpl) {
     using T = decltype(t);
     constexpr int R = decltype(lpr)::value, N = decltype(vpl)::value;
     auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kRtThreads), 0, stream, p); };

@@ -143,6 +143,23 @@ def test_route_no_tokens_and_many_rows_per_wave(T):
     check_route_backward(z, 3, fwd)
 
 
+# from these lengths on a lane takes 32 logits of a row, one top_k for each list length
+@pytest.mark.parametrize("T,E,k,score", [(16397, 160, 6, "softmax"), (16384, 256, 11, "sigmoid"),
+                                         (8205, 500, 10, "softmax"), (8192, 300, 4, "sigmoid"),
+                                         (4103, 1000, 3, "softmax"), (4096, 1024, 8, "sigmoid"),
+                                         (16390, 129, 16, "softmax")])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_route_long_batches(T, E, k, score, dtype):
+    z = logits(T, E, T + E, dtype)
+    z[3, 5:] = float("-inf")  # five experts left, fewer than k
+    z[T - 2] = float("-inf")
+    z[T // 2, :] = 0.25       # all equal
+    mask = (torch.rand(T, generator=synth.gen(T + E, "mask")) < 0.9).cuda()
+    mask[:8] = True
+    check_route(z, k, score, True, 1.5, mask)
+    check_route(z, k, score, False)
+
+
 def test_route_ties_take_the_lowest_expert():
     # logits of few distinct values, both zeros among them
     g = synth.gen(5, "ties")
