@@ -88,9 +88,9 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
   auto tile_at = [&](int T) { return order.at(T); };
 
   const __amdgpu_buffer_rsrc_t g_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)p.grad, 0, (int)(uint32_t)((int64_t)p.S * p.grad_ld * 2), 0x00020000);
+      (void*)p.grad, 0, wg_span(p.S, p.grad_ld, p.N, 2), 0x00020000);
   const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)p.x, 0, (int)(uint32_t)((int64_t)(p.S / p.top_k) * p.x_ld * 2), 0x00020000);
+      (void*)p.x, 0, wg_span(p.S / p.top_k, p.x_ld, p.K, 2), 0x00020000);
   const __amdgpu_buffer_rsrc_t sorted_rsrc = __builtin_amdgcn_make_buffer_rsrc(
       (void*)p.sorted, 0, (int)(uint32_t)((int64_t)p.max_blocks * kWgBM * 4), 0x00020000);
   const uint32_t lds_base = (uint32_t)(uintptr_t)(wg_lds_u8_t*)&lds[0][0];

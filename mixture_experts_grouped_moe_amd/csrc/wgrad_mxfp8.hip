@@ -86,18 +86,14 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   wg_block_ranges<kMxThreads>(p, s_start);
   const WgSplitOrder order(p, s_start);
 
-  // The buffers end with their last row's last element (a view's last row
-  // may end with its allocation); PAD slots (s = S) lie past them.
+  // (PAD slots, s = S, lie past the buffers)
   const int64_t T = p.S / p.top_k;
-  auto span = [](int64_t rows, int64_t ld, int64_t width, int bytes) {
-    return (int)(uint32_t)(rows > 0 ? ((rows - 1) * ld + width) * bytes : 0);
-  };
   const __amdgpu_buffer_rsrc_t g_rsrc =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.grad, 0, span(p.S, p.grad_ld, p.N, 2), 0x00020000);
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.grad, 0, wg_span(p.S, p.grad_ld, p.N, 2), 0x00020000);
   const __amdgpu_buffer_rsrc_t x_rsrc =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, span(T, p.x_ld, p.K, 1), 0x00020000);
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, wg_span(T, p.x_ld, p.K, 1), 0x00020000);
   const __amdgpu_buffer_rsrc_t s_rsrc =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.xs, 0, span(T, p.xs_ld, p.K / 32, 1), 0x00020000);
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.xs, 0, wg_span(T, p.xs_ld, p.K / 32, 1), 0x00020000);
   const uint32_t g_lds = (uint32_t)(uintptr_t)(wg_lds_u8_t*)&lds_g[0][0];
   const uint32_t x_lds = (uint32_t)(uintptr_t)(wg_lds_u8_t*)&lds_x[0][0];
   const uint32_t c_lds = (uint32_t)(uintptr_t)(wg_lds_u8_t*)&lds_c[0][0];

@@ -80,6 +80,12 @@ __device__ __forceinline__ bf16x8_t wg_operand(const wg_lds_u8_t* part, int c0, 
   return r;
 }
 
+// Bytes of a buffer of rows: up to its last row's last element, since a view's
+// last row may end with its allocation.
+__device__ __forceinline__ int wg_span(int64_t rows, int64_t ld, int64_t width, int bytes) {
+  return (int)(uint32_t)(rows > 0 ? ((rows - 1) * ld + width) * bytes : 0);
+}
+
 // A tile of dW and its expert's block range.
 struct WgTile {
   int e, n0, k0, b0, b1;

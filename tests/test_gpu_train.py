@@ -482,6 +482,21 @@ def test_wgrad_mxfp8_strides_at_the_end_of_an_allocation():
     _check_wgrad(xw[:, 32:], sw[:, 5:], gw[:, 8:], ids, E)
 
 
+def test_wgrad_strides_at_the_end_of_an_allocation():
+    """The bf16 entry point: a tile wider than the rows reads nothing past the last one."""
+    moe = _moe()
+    T, k, E, N, K = 50, 2, 3, 64, 96
+    xq, xs, grad, ids = _wgrad_case(T, k, E, N, K, 6)
+    x = torch.from_numpy(oquant.mx_dequantize_e4m3(xq.cpu().numpy(), xs.cpu().numpy())).to(torch.bfloat16)
+    xw = torch.zeros((T, K + 512), dtype=torch.bfloat16, device="cuda")
+    gw = torch.zeros((T * k, N + 512), dtype=torch.bfloat16, device="cuda")
+    xw[:, 512:], gw[:, 512:] = x.cuda(), grad
+    routing = moe.moe_align(ids, E, moe.moe_wgrad_block_m())
+    dw = moe.moe_wgrad(xw[:, 512:], gw[:, 512:], routing, T, k, E)
+    assert torch.equal(dw, moe.moe_wgrad(x.cuda(), grad, routing, T, k, E))
+    _check_wgrad(xq, xs, grad, ids, E)
+
+
 def test_wgrad_mxfp8_scale_edges():
     T, k, E, N, K = 40, 1, 2, 32, 64
     xq, xs, grad, ids = _wgrad_case(T, k, E, N, K, 7)
