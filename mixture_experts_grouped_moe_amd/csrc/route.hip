@@ -20,7 +20,7 @@
 // Backward: the same layout. The probabilities are not kept by the forward
 // pass but recomputed from the logits, which the gradient would otherwise
 // replace by a read of the same size. The chosen experts' terms go through a
-// row of LDS that is zero otherwise, so adding them costs one scattered write
+// row of LDS that is zero otherwise, so adding them costs one scattered add
 // and one read however many there are.
 //
 // Statistics: each lane adds its rows' probabilities into registers, a
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RoutePara
   using V = RtVec<T>;
   constexpr int RPW = 64 / LPR;
   constexpr int WIDTH = LPR * VPL + 32;  // (rows a bank group apart)
-  __shared__ float s_u[kRtWaves][RPW][WIDTH];
+  __shared__ __attribute__((aligned(16))) float s_u[kRtWaves][RPW][WIDTH];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int l = lane % LPR, group = lane / LPR;
   float* su = s_u[wave][group];
@@ -449,17 +449,20 @@ __global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RoutePara
     }
 #pragma unroll
     for (int jj = 0; jj < NJ; ++jj)
-      if (id[jj] >= 0) su[id[jj]] = v[jj];
+      if (id[jj] >= 0) atomicAdd(&su[id[jj]], v[jj]);  // (added: a caller's ids may name an expert twice)
     __builtin_amdgcn_wave_barrier();
     T* out = static_cast<T*>(p.dlogits) + t * p.dld;
 #pragma unroll
     for (int c = 0; c < VPL / V::N; ++c) {
       const int e = (c * LPR + l) * V::N;
       typename V::vec o;
+      f32x4_t u[V::N / 4];
+#pragma unroll
+      for (int i = 0; i < V::N / 4; ++i) u[i] = *reinterpret_cast<const f32x4_t*>(su + e + 4 * i);
 #pragma unroll
       for (int i = 0; i < V::N; ++i) {
         const int at = c * V::N + i;
-        float d = x[at] * inv * (cost[at] + common) + su[e + i];
+        float d = x[at] * inv * (cost[at] + common) + u[i / 4][i % 4];
         if (SIGMOID) d *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[at] * 1.44269504f));  // 1 - sigmoid(z)
         d = on ? d : 0.0f;
         if (e + V::N <= p.E)
@@ -477,7 +480,7 @@ __global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RoutePara
   }
 }
 
-// Rows that one workgroup takes at a time (rt_layout, 16 and 32 logits a lane).
+// Rows that one workgroup takes at a time (rt_layout, rt_layout_deep).
 static int rt_rows(int E) { return kRtWaves * (E <= 128 ? 8 : E <= 256 ? 4 : E <= 512 ? 2 : 1); }
 static int rt_rows_deep(int E) { return kRtWaves * (E <= 256 ? 8 : E <= 512 ? 4 : 2); }
 
@@ -504,9 +507,9 @@ int64_t route_workspace_bytes(int64_t T, int32_t E) {
 template <int N>
 using rt_c = std::integral_constant<int, N>;
 
-// f(type, LPR, VPL) for the row layout of E experts: VPL at most 16, or 32.
+// f(type, LPR, VPL) for the row layout of E experts, VPL at most 16.
 template <class F>
-static void rt_layout(int E, bool bf16, bool deep, F&& f) {
+static void rt_layout(int E, bool bf16, F&& f) {
   auto by_type = [&](auto lpr, auto vpl) {
     if (bf16)
       f(uint16_t{}, lpr, vpl);
@@ -517,18 +520,28 @@ static void rt_layout(int E, bool bf16, bool deep, F&& f) {
     by_type(rt_c<8>{}, rt_c<8>{});
   else if (E <= 128)
     by_type(rt_c<8>{}, rt_c<16>{});
-  else if (deep && E <= 256)
-    by_type(rt_c<8>{}, rt_c<32>{});
-  else if (deep && E <= 512)
-    by_type(rt_c<16>{}, rt_c<32>{});
-  else if (deep)
-    by_type(rt_c<32>{}, rt_c<32>{});
   else if (E <= 256)
     by_type(rt_c<16>{}, rt_c<16>{});
   else if (E <= 512)
     by_type(rt_c<32>{}, rt_c<16>{});
   else
     by_type(rt_c<64>{}, rt_c<16>{});
+}
+// With 32 logits a lane (E > 128).
+template <class F>
+static void rt_layout_deep(int E, bool bf16, F&& f) {
+  auto by_type = [&](auto lpr) {
+    if (bf16)
+      f(uint16_t{}, lpr, rt_c<32>{});
+    else
+      f(float{}, lpr, rt_c<32>{});
+  };
+  if (E <= 256)
+    by_type(rt_c<8>{});
+  else if (E <= 512)
+    by_type(rt_c<16>{});
+  else
+    by_type(rt_c<32>{});
 }
 
 hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t stream) {
@@ -574,7 +587,7 @@ hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t s
     else
       by_type(rt_c<16>{});
   } else {
-    rt_layout(p.E, bf16, deep, [&](auto t, auto lpr, auto vpl) {
+    auto go = [&](auto t, auto lpr, auto vpl) {
       by_score([&](auto sig) {
         using T = decltype(t);
         constexpr int R = decltype(lpr)::value, N = decltype(vpl)::value;
@@ -586,7 +599,11 @@ hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t s
         else
           launch(route_kernel<T, R, N, 16, S>);
       });
-    });
+    };
+    if (deep)
+      rt_layout_deep(p.E, bf16, go);
+    else
+      rt_layout(p.E, bf16, go);
   }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || !p.stats) return err;
@@ -598,7 +615,7 @@ hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t s
 hipError_t launch_route_backward(const RouteParams& p, bool bf16, hipStream_t stream) {
   const uint32_t grid = rt_grid(p.T, rt_rows(p.E));
   if (grid == 0) return hipSuccess;
-  rt_layout(p.E, bf16, false, [&](auto t, auto lpr, auto vpl) {
+  rt_layout(p.E, bf16, [&](auto t, auto lpr, auto vpl) {
     using T = decltype(t);
     constexpr int R = decltype(lpr)::value, N = decltype(vpl)::value;
     auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kRtThreads), 0, stream, p); };

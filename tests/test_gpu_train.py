@@ -262,6 +262,19 @@ def test_route_backward_skips_ids_out_of_range():
     check_route_backward(z, 3, fwd)
 
 
+@pytest.mark.parametrize("E,k", [(20, 3), (300, 40)])
+def test_route_backward_adds_an_expert_named_twice(E, k):
+    z = logits(6, E, 13)
+    fwd = list(check_route(z, k))
+    ids = fwd[0].clone()
+    ids[1] = ids[1, 0]              # one expert in every place
+    ids[2, 1] = ids[2, 2]
+    ids[4, k - 1] = ids[4, 0]
+    fwd[0] = ids
+    for score, renorm in (("softmax", False), ("softmax", True), ("sigmoid", False)):
+        check_route_backward(z, k, fwd, score, renorm)
+
+
 def test_route_repeats_bit_for_bit_on_any_stream():
     moe = _moe()
     z = logits(3000, 256, 12)
