@@ -68,7 +68,8 @@ typedef enum {
  * graphs replayed side by side) each need their own.
  * Requirements: 1 <= num_experts <= 1024; 1 <= top_k <= min(num_experts, 64);
  * logits_ld >= num_experts; num_tokens * top_k <= 2^31 - 2^16 (as moe_align);
- * finite scale; pointers aligned to their elements. */
+ * finite scale; pointers aligned to their elements; outputs and workspace must
+ * not overlap each other or the inputs. */
 moe_status moe_route(const void* logits, int32_t logits_dtype, int64_t logits_ld, const uint8_t* token_mask,
                      int64_t num_tokens, int32_t num_experts, int32_t top_k, int32_t score, int32_t renormalize,
                      float scale, int32_t* topk_ids, float* topk_w, int32_t stats, int32_t* counts,
@@ -89,7 +90,8 @@ int64_t moe_route_workspace_bytes(int64_t num_tokens, int32_t num_experts);
  * da[e] * (1 - sigmoid(z_e)) for sigmoid scores.
  * Every row of dlogits is written (in logits' type, rounded once); a token
  * whose first id is negative gets zeros and its logits are not read. Ids
- * outside [0, E) past the first contribute nothing.
+ * outside [0, E) past the first contribute nothing; an expert named twice gets
+ * both terms.
  * dtopk_w (device) fp32 [T][top_k]; entries at ids of -1 are ignored. dlosses
  * (device) fp32 [2] or NULL (no losses; counts and num_routed may then be
  * NULL). dlogits must not overlap the inputs. Requirements as for moe_route;
@@ -106,7 +108,8 @@ moe_status moe_route_backward(const void* logits, int32_t logits_dtype, int64_t 
  * in fp32. The other slots' rows of C (which the grouped GEMM leaves as they
  * were) and weights are not read; a token without a routed slot gets zeros.
  * topk_ids (device) int32 [T][top_k]; everything else as for moe_combine,
- * whose bits this gives when every slot is routed. */
+ * whose bits this gives when every slot is routed; y must not overlap the
+ * inputs. */
 moe_status moe_combine_routed(const void* c, int64_t c_ld, const float* topk_w, const int32_t* topk_ids,
                               int64_t num_tokens, int32_t top_k, int32_t num_experts, int64_t n, void* y,
                               int64_t y_ld, moe_stream_t stream);
@@ -119,8 +122,8 @@ moe_status moe_combine_routed(const void* c, int64_t c_ld, const float* topk_w, 
  * An unrouted slot gets a dC row of zeros and dtopk_w 0; its row of C is not
  * read. dy (device) bf16 [T][n]; c, dc (device) bf16 [T*top_k][n]; topk_w,
  * dtopk_w (device) fp32 [T][top_k]. Every row and weight is written. dc and
- * dtopk_w must not overlap the inputs or each other (checked for dc against
- * dy and c). num_experts is read with topk_ids only.
+ * dtopk_w must not overlap the inputs or each other. num_experts is read with
+ * topk_ids only.
  * n % 8 == 0; dy_ld, c_ld, dc_ld >= n and multiples of 8; dy, c, dc 16-byte
  * aligned. No workspace. */
 moe_status moe_combine_backward(const void* dy, int64_t dy_ld, const void* c, int64_t c_ld, const float* topk_w,
@@ -165,7 +168,8 @@ moe_status moe_act_mxfp8_backward(int32_t act, const void* q, int64_t q_ld, cons
  * in fp32, xhat exact in bf16 (values below bf16's subnormal range round to
  * zero). xq (device) uint8 E4M3 [T][K], row stride xq_ld bytes, a multiple of
  * 16, 16-byte aligned; xs (device) uint8 E8M0 [T][K/32], row stride xs_ld
- * bytes >= K / 32. Everything else as for moe_wgrad. No workspace. */
+ * bytes >= K / 32. dw must not overlap the inputs. Everything else as for
+ * moe_wgrad. No workspace. */
 moe_status moe_wgrad_mxfp8(const void* xq, int64_t xq_ld, const uint8_t* xs, int64_t xs_ld, const void* grad,
                            int64_t grad_ld, const int32_t* sorted_token_ids, const int32_t* expert_ids,
                            const int32_t* num_tokens_post_pad, int64_t num_tokens, int32_t top_k,

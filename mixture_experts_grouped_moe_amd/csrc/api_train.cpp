@@ -4,6 +4,7 @@
 
 #include <climits>
 #include <cmath>
+#include <initializer_list>
 
 #include "moe_train.h"
 
@@ -20,17 +21,40 @@ using moe::ok;
 
 constexpr int32_t kRouteMaxTopK = 64;
 constexpr int64_t kBufMax = (int64_t)0x80000000;
-constexpr int64_t kMaxLd = (int64_t)1 << 40;  // row strides and row counts below it: byte offsets fit 64 bits
+constexpr int64_t kMaxElements = (int64_t)1 << 60;  // rows * stride at most: byte offsets fit 64 bits
 
-// [a, a + a_bytes) and [b, b + b_bytes) share a byte.
-bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a_bytes > 0 && b_bytes > 0 && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+// `bytes` bytes at p.
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+
+// `rows` rows of `width` elements, up to the last one's end.
+Range span(const void* p, int64_t rows, int64_t ld, int64_t width, int64_t bytes) {
+  return {p, rows > 0 ? ((rows - 1) * ld + width) * bytes : 0};
 }
 
-// Bytes from the first element of `rows` rows to the last one's end.
-int64_t span(int64_t rows, int64_t ld, int64_t width, int64_t bytes) {
-  return rows > 0 ? ((rows - 1) * ld + width) * bytes : 0;
+// One of `outs` shares a byte with another of them or with one of `ins`.
+// (Null and empty ranges share none.)
+bool clash(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  const auto share = [](const Range& a, const Range& b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x != 0 && y != 0 && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes &&
+           y < x + (uintptr_t)a.bytes;
+  };
+  for (const Range* a = outs.begin(); a != outs.end(); ++a) {
+    for (const Range* b = a + 1; b != outs.end(); ++b)
+      if (share(*a, *b)) return true;
+    for (const Range& b : ins)
+      if (share(*a, b)) return true;
+  }
+  return false;
+}
+
+// A row stride that does not cover `width`, is no multiple of `multiple`, or
+// takes `rows` rows past kMaxElements.
+bool bad_ld(int64_t ld, int64_t width, int64_t multiple, int64_t rows) {
+  return ld < width || ld % multiple != 0 || ld > kMaxElements / (rows > 1 ? rows : 1);
 }
 
 bool misaligned(const void* p, uintptr_t to) { return (uintptr_t)p % to != 0; }
@@ -49,7 +73,7 @@ moe_status check_route(const void* logits, int32_t dtype, int64_t ld, int64_t T,
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID)
     return fail(MOE_ERR_INVALID_ARGUMENT, "unknown score %d", score);
   if (!std::isfinite(scale)) return fail(MOE_ERR_INVALID_ARGUMENT, "scale is not finite");
-  if (ld < E || ld >= kMaxLd) return fail(MOE_ERR_INVALID_ARGUMENT, "logits_ld must be >= num_experts");
+  if (bad_ld(ld, E, 1, T)) return fail(MOE_ERR_INVALID_ARGUMENT, "logits_ld must be >= num_experts");
   if (T > 0 && (logits == nullptr || ids == nullptr)) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (misaligned(logits, dtype == MOE_FP32 ? 4 : 2) || misaligned(ids, 4))
     return fail(MOE_ERR_INVALID_ARGUMENT, "logits and topk_ids must be aligned to their elements");
@@ -66,8 +90,6 @@ moe_status check_combine(int64_t T, int32_t k, int64_t n) {
   return MOE_OK;
 }
 
-bool bad_ld8(int64_t ld, int64_t width) { return ld < width || ld % 8 != 0 || ld >= kMaxLd; }
-
 // What both activation entry points check alike; `out` is the width of h.
 moe_status check_act(int32_t act, int64_t rows, int64_t n, const void* q, int64_t q_ld, const uint8_t* scales,
                      int64_t scales_ld, int64_t* out) {
@@ -78,9 +100,9 @@ moe_status check_act(int32_t act, int64_t rows, int64_t n, const void* q, int64_
   const int64_t unit = swiglu ? 64 : 32;
   if (n < unit || n % unit != 0 || n >= INT32_MAX)
     return fail(MOE_ERR_INVALID_ARGUMENT, "n must be a positive multiple of %lld", (long long)unit);
-  if (q_ld < n || q_ld % 16 != 0 || q_ld >= kMaxLd)
+  if (bad_ld(q_ld, n, 16, rows))
     return fail(MOE_ERR_INVALID_ARGUMENT, "q_ld must be >= n and a multiple of 16");
-  if (scales_ld < n / 32 || scales_ld >= kMaxLd) return fail(MOE_ERR_INVALID_ARGUMENT, "scales_ld must be >= n / 32");
+  if (bad_ld(scales_ld, n / 32, 1, rows)) return fail(MOE_ERR_INVALID_ARGUMENT, "scales_ld must be >= n / 32");
   if (rows > 0 && (q == nullptr || scales == nullptr)) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
   *out = swiglu ? n / 2 : n;
   return MOE_OK;
@@ -116,6 +138,11 @@ moe_status moe_route(const void* logits, int32_t logits_dtype, int64_t logits_ld
                   (long long)need);
     if (misaligned(workspace, 8)) return fail(MOE_ERR_INVALID_ARGUMENT, "workspace must be 8-byte aligned");
   }
+  const int64_t T = num_tokens, E = num_experts, slots = T * top_k, on = stats ? 1 : 0;
+  if (clash({{topk_ids, slots * 4}, {topk_w, slots * 4}, {counts, on * E * 4}, {num_routed, on * 4},
+             {prob_sum, on * E * 4}, {losses, on * 8}, {workspace, on * moe_route_workspace_bytes(T, num_experts)}},
+            {span(logits, T, logits_ld, E, logits_dtype == MOE_FP32 ? 4 : 2), {token_mask, T}}))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "the outputs overlap each other, the workspace or an input");
   st = check_device();
   if (st != MOE_OK) return st;
   moe::RouteParams p{};
@@ -147,7 +174,7 @@ moe_status moe_route_backward(const void* logits, int32_t logits_dtype, int64_t 
   moe_status st =
       check_route(logits, logits_dtype, logits_ld, num_tokens, num_experts, top_k, score, scale, topk_ids);
   if (st != MOE_OK) return st;
-  if (dlogits_ld < num_experts || dlogits_ld >= kMaxLd)
+  if (bad_ld(dlogits_ld, num_experts, 1, num_tokens))
     return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits_ld must be >= num_experts");
   if (num_tokens > 0 && (dtopk_w == nullptr || dlogits == nullptr))
     return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
@@ -157,13 +184,10 @@ moe_status moe_route_backward(const void* logits, int32_t logits_dtype, int64_t 
   if (misaligned(dtopk_w, 4) || misaligned(counts, 4) || misaligned(num_routed, 4) || misaligned(dlosses, 4) ||
       misaligned(dlogits, (uintptr_t)es))
     return fail(MOE_ERR_INVALID_ARGUMENT, "pointers must be aligned to their elements");
-  const int64_t out_bytes = span(num_tokens, dlogits_ld, num_experts, es);
-  const int64_t slots = num_tokens * top_k;
-  if (overlap(dlogits, out_bytes, logits, span(num_tokens, logits_ld, num_experts, es)) ||
-      overlap(dlogits, out_bytes, topk_ids, slots * 4) || overlap(dlogits, out_bytes, dtopk_w, slots * 4) ||
-      (dlosses != nullptr &&
-       (overlap(dlogits, out_bytes, counts, (int64_t)num_experts * 4) || overlap(dlogits, out_bytes, num_routed, 4) ||
-        overlap(dlogits, out_bytes, dlosses, 8))))
+  const int64_t T = num_tokens, E = num_experts, slots = T * top_k, on = dlosses != nullptr ? 1 : 0;
+  if (clash({span(dlogits, T, dlogits_ld, E, es)},
+            {span(logits, T, logits_ld, E, es), {topk_ids, slots * 4}, {dtopk_w, slots * 4}, {counts, on * E * 4},
+             {num_routed, on * 4}, {dlosses, 8}}))
     return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits overlaps an input");
   st = check_device();
   if (st != MOE_OK) return st;
@@ -193,14 +217,15 @@ moe_status moe_combine_routed(const void* c, int64_t c_ld, const float* topk_w, 
   moe_status st = check_combine(num_tokens, top_k, n);
   if (st != MOE_OK) return st;
   if (num_experts < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "num_experts < 1");
-  if (bad_ld8(c_ld, n) || bad_ld8(y_ld, n))
+  const int64_t S = num_tokens * top_k;
+  if (bad_ld(c_ld, n, 8, S) || bad_ld(y_ld, n, 8, num_tokens))
     return fail(MOE_ERR_INVALID_ARGUMENT, "c_ld and y_ld must be >= n and multiples of 8");
   if (num_tokens > 0 && (c == nullptr || topk_w == nullptr || topk_ids == nullptr || y == nullptr))
     return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (misaligned(c, 16) || misaligned(y, 16) || misaligned(topk_w, 4) || misaligned(topk_ids, 4))
     return fail(MOE_ERR_INVALID_ARGUMENT, "c and y must be 16-byte aligned, topk_w and topk_ids 4-byte");
-  if (num_tokens * (n / 8) >= (int64_t)INT32_MAX * 128)
-    return fail(MOE_ERR_UNSUPPORTED, "problem too large for one launch");
+  if (clash({span(y, num_tokens, y_ld, n, 2)}, {span(c, S, c_ld, n, 2), {topk_w, S * 4}, {topk_ids, S * 4}}))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "y overlaps an input");
   st = check_device();
   if (st != MOE_OK) return st;
   return hip_status(moe::launch_combine_routed(static_cast<const uint16_t*>(c), c_ld, topk_w, topk_ids, num_tokens,
@@ -215,17 +240,17 @@ moe_status moe_combine_backward(const void* dy, int64_t dy_ld, const void* c, in
   moe_status st = check_combine(num_tokens, top_k, n);
   if (st != MOE_OK) return st;
   if (topk_ids != nullptr && num_experts < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "num_experts < 1");
-  if (bad_ld8(dy_ld, n) || bad_ld8(c_ld, n) || bad_ld8(dc_ld, n))
+  const int64_t S = num_tokens * top_k;
+  if (bad_ld(dy_ld, n, 8, num_tokens) || bad_ld(c_ld, n, 8, S) || bad_ld(dc_ld, n, 8, S))
     return fail(MOE_ERR_INVALID_ARGUMENT, "dy_ld, c_ld and dc_ld must be >= n and multiples of 8");
   if (num_tokens > 0 && (dy == nullptr || c == nullptr || topk_w == nullptr || dc == nullptr || dtopk_w == nullptr))
     return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (misaligned(dy, 16) || misaligned(c, 16) || misaligned(dc, 16) || misaligned(topk_w, 4) ||
       misaligned(topk_ids, 4) || misaligned(dtopk_w, 4))
     return fail(MOE_ERR_INVALID_ARGUMENT, "dy, c and dc must be 16-byte aligned, the others 4-byte");
-  const int64_t S = num_tokens * top_k;
-  const int64_t dc_bytes = span(S, dc_ld, n, 2);
-  if (overlap(dc, dc_bytes, c, span(S, c_ld, n, 2)) || overlap(dc, dc_bytes, dy, span(num_tokens, dy_ld, n, 2)))
-    return fail(MOE_ERR_INVALID_ARGUMENT, "dc overlaps c or dy");
+  if (clash({span(dc, S, dc_ld, n, 2), {dtopk_w, S * 4}},
+            {span(c, S, c_ld, n, 2), span(dy, num_tokens, dy_ld, n, 2), {topk_w, S * 4}, {topk_ids, S * 4}}))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dc and dtopk_w must not overlap each other or an input");
   st = check_device();
   if (st != MOE_OK) return st;
   return hip_status(
@@ -240,15 +265,13 @@ moe_status moe_act_mxfp8(int32_t act, const void* pre, int64_t pre_ld, int64_t r
   int64_t out = 0;
   moe_status st = check_act(act, rows, n, q, q_ld, scales, scales_ld, &out);
   if (st != MOE_OK) return st;
-  if (bad_ld8(pre_ld, n) || bad_ld8(h_ld, out))
+  if (bad_ld(pre_ld, n, 8, rows) || bad_ld(h_ld, out, 8, rows))
     return fail(MOE_ERR_INVALID_ARGUMENT, "pre_ld and h_ld must cover a row and be multiples of 8");
   if (rows > 0 && (pre == nullptr || h == nullptr)) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (misaligned(pre, 16) || misaligned(h, 16) || misaligned(q, 16))
     return fail(MOE_ERR_INVALID_ARGUMENT, "pre, h and q must be 16-byte aligned");
-  const int64_t pre_b = span(rows, pre_ld, n, 2), h_b = span(rows, h_ld, out, 2), q_b = span(rows, q_ld, n, 1),
-                s_b = span(rows, scales_ld, n / 32, 1);
-  if (overlap(pre, pre_b, h, h_b) || overlap(pre, pre_b, q, q_b) || overlap(pre, pre_b, scales, s_b) ||
-      overlap(h, h_b, q, q_b) || overlap(h, h_b, scales, s_b) || overlap(q, q_b, scales, s_b))
+  if (clash({span(h, rows, h_ld, out, 2), span(q, rows, q_ld, n, 1), span(scales, rows, scales_ld, n / 32, 1)},
+            {span(pre, rows, pre_ld, n, 2)}))
     return fail(MOE_ERR_INVALID_ARGUMENT, "pre, h, q and scales must not overlap");
   st = check_device();
   if (st != MOE_OK) return st;
@@ -272,16 +295,13 @@ moe_status moe_act_mxfp8_backward(int32_t act, const void* q, int64_t q_ld, cons
   int64_t out = 0;
   moe_status st = check_act(act, rows, n, q, q_ld, scales, scales_ld, &out);
   if (st != MOE_OK) return st;
-  if (bad_ld8(dh_ld, out) || bad_ld8(dpre_ld, n) || (h != nullptr && bad_ld8(h_ld, out)))
+  if (bad_ld(dh_ld, out, 8, rows) || bad_ld(dpre_ld, n, 8, rows) || (h != nullptr && bad_ld(h_ld, out, 8, rows)))
     return fail(MOE_ERR_INVALID_ARGUMENT, "dh_ld, dpre_ld and h_ld must cover a row and be multiples of 8");
   if (rows > 0 && (dh == nullptr || dpre == nullptr)) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (misaligned(dh, 16) || misaligned(dpre, 16) || misaligned(h, 16) || misaligned(q, 16))
     return fail(MOE_ERR_INVALID_ARGUMENT, "q, dh, dpre and h must be 16-byte aligned");
-  const int64_t q_b = span(rows, q_ld, n, 1), s_b = span(rows, scales_ld, n / 32, 1), dh_b = span(rows, dh_ld, out, 2),
-                dpre_b = span(rows, dpre_ld, n, 2), h_b = h != nullptr ? span(rows, h_ld, out, 2) : 0;
-  if (overlap(dpre, dpre_b, q, q_b) || overlap(dpre, dpre_b, scales, s_b) || overlap(dpre, dpre_b, dh, dh_b) ||
-      overlap(dpre, dpre_b, h, h_b) || overlap(h, h_b, q, q_b) || overlap(h, h_b, scales, s_b) ||
-      overlap(h, h_b, dh, dh_b))
+  if (clash({span(dpre, rows, dpre_ld, n, 2), span(h, rows, h_ld, out, 2)},
+            {span(q, rows, q_ld, n, 1), span(scales, rows, scales_ld, n / 32, 1), span(dh, rows, dh_ld, out, 2)}))
     return fail(MOE_ERR_INVALID_ARGUMENT, "dpre and h must not overlap each other or the inputs");
   st = check_device();
   if (st != MOE_OK) return st;
@@ -313,7 +333,8 @@ moe_status moe_wgrad_mxfp8(const void* xq, int64_t xq_ld, const uint8_t* xs, int
     return fail(MOE_ERR_UNSUPPORTED, "num_experts %d > %d", num_experts, kAlignMaxExperts);
   if (n < 32 || n % 32 != 0 || k < 32 || k % 32 != 0 || n >= INT32_MAX || k >= INT32_MAX)
     return fail(MOE_ERR_INVALID_ARGUMENT, "n and k must be positive multiples of 32");
-  if (xq_ld < k || xq_ld % 16 != 0 || xq_ld >= kBufMax || bad_ld8(grad_ld, n) || grad_ld >= kBufMax)
+  if (xq_ld < k || xq_ld % 16 != 0 || xq_ld >= kBufMax || grad_ld < n || grad_ld % 8 != 0 ||
+      grad_ld >= kBufMax)
     return fail(MOE_ERR_INVALID_ARGUMENT, "xq_ld / grad_ld must cover a row and be multiples of 16 / 8");
   if (xs_ld < k / 32 || xs_ld >= kBufMax) return fail(MOE_ERR_INVALID_ARGUMENT, "xs_ld must be >= k / 32");
   if (block_m != moe::wgrad_block_m())
@@ -338,6 +359,10 @@ moe_status moe_wgrad_mxfp8(const void* xq, int64_t xq_ld, const uint8_t* xs, int
   if (num_tokens * xq_ld >= kBufMax || num_tokens * xs_ld >= kBufMax || S * grad_ld * 2 >= kBufMax ||
       n * k * 4 >= kBufMax)
     return fail(MOE_ERR_UNSUPPORTED, "xq, xs, grad or one expert's dW spans 2 GB or more");
+  if (clash({{dw, num_experts * n * k * 4}},
+            {span(xq, num_tokens, xq_ld, k, 1), span(xs, num_tokens, xs_ld, k / 32, 1), span(grad, S, grad_ld, n, 2),
+             {sorted_token_ids, max_blocks * block_m * 4}, {expert_ids, max_blocks * 4}}))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dw overlaps an input");
   (void)num_tokens_post_pad;
   moe_status st = check_device();
   if (st != MOE_OK) return st;

@@ -69,8 +69,14 @@ __device__ __forceinline__ void rt_write_partial(const RouteParams& p, const flo
   }
 }
 
+// Waves per SIMD that the registers leave room for: 32 logits a lane or lists
+// of 16 double keys take more than 128 (4096 x 256 fp32 top 16: 5.4 us, with
+// 10 registers in scratch memory at four waves 6.1).
+template <class T, int VPL, int L>
+constexpr int kRtOccupancy = VPL > 16 || sizeof(typename RtVec<T>::key::type) * L > 64 ? 2 : 4;
+
 template <class T, int LPR, int VPL, int L, bool SIGMOID>
-__global__ __launch_bounds__(kRtThreads, VPL > 16 ? 2 : 4) void route_kernel(RouteParams p) {
+__global__ __launch_bounds__(kRtThreads, (kRtOccupancy<T, VPL, L>)) void route_kernel(RouteParams p) {
   using V = RtVec<T>;
   using K = typename V::key;
   constexpr int RPW = 64 / LPR;        // rows of a wave

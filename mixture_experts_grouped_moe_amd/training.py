@@ -81,8 +81,8 @@ def _on_stream(f):
     def call(*args, stream=None, **kw):
         if stream is None and _one_device():
             return f(*args, **kw)
-        first = args[0] if args else next(iter(kw.values()), None)
-        on_gpu = isinstance(first, torch.Tensor) and first.is_cuda
+        first = next((a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor)), None)
+        on_gpu = first is not None and first.is_cuda
         if stream is None:
             if not on_gpu or first.get_device() == torch.cuda.current_device():
                 return f(*args, **kw)

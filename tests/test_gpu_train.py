@@ -347,6 +347,34 @@ def test_combine_backward_strides_and_rows_behind():
     assert (wide == 7.0).all()
 
 
+def test_combine_over_more_than_one_launch():
+    """More slots than one launch takes (2^20), and more output pieces (2^26)."""
+    moe = _moe()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T, k, N, E = 349527, 3, 8, 5
+    assert T * k > 1 << 20
+    dy = torch.randn((T, N), generator=g, device="cuda").to(torch.bfloat16)
+    c = torch.randn((T * k, N), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.rand((T, k), generator=g, device="cuda")
+    ids = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    on = (ids >= 0)
+    dc, dw = moe.moe_combine_backward(dy, c, w, ids, E)
+    ref = torch.where(on[..., None], w[..., None] * dy.float()[:, None, :], 0.0).to(torch.bfloat16)
+    assert torch.equal(dc, ref.view(T * k, N))
+    terms = torch.where(on[..., None], dy.double()[:, None, :] * c.double().view(T, k, N), 0.0)
+    assert ((dw.double() - terms.sum(-1)).abs() <= N * U * terms.abs().sum(-1)).all()
+    del dc, dw, ref, terms, dy, c
+    T, N = (1 << 23) + 5, 64
+    c = torch.randint(-32768, 32767, (T, N), generator=g, device="cuda", dtype=torch.int16).clamp_(-9000, 9000)
+    c = (c.view(torch.int16) & 0x3FFF).view(torch.bfloat16)     # any finite bits below 2
+    w = torch.rand((T, 1), generator=g, device="cuda")
+    ids = torch.randint(-1, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    y = moe.moe_combine_routed(c, w, ids, E)
+    for part in (slice(0, 4096), slice(T // 2, T // 2 + 4096), slice(T - 4096, T)):
+        want = torch.where(ids[part] >= 0, w[part] * c[part].float(), 0.0).to(torch.bfloat16)
+        assert torch.equal(y[part], want)
+
+
 def test_combine_no_tokens():
     moe = _moe()
     e = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")

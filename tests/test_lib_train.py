@@ -203,6 +203,44 @@ def test_wgrad_mxfp8_rejects(no_device):
     assert _wgrad(n=1 << 15, K=1 << 15, xld=1 << 15, xsld=1 << 10, gld=1 << 15) == UNSUPPORTED
 
 
+def _far(n):
+    return [(i + 1) << 32 for i in range(n)]  # pointers far apart
+
+
+def _overlaps(call, outputs, inputs):
+    """Every output over every other one and over every input is refused; the call as such is not."""
+    names = outputs + inputs
+    ptr = dict(zip(names, _far(len(names))))
+    assert call(**ptr) not in (INVALID, UNSUPPORTED), L.moe_last_error()   # (no device here)
+    for i, a in enumerate(outputs):
+        for b in outputs[i + 1:] + inputs:
+            assert call(**{**ptr, a: ptr[b]}) == INVALID, (a, b)
+            assert b"overlap" in L.moe_last_error()
+
+
+def test_overlaps_are_rejected(no_device):
+    _overlaps(_route, ["ids", "w", "counts", "n", "p", "loss", "ws"], ["z", "mask"])
+    _overlaps(_route_bwd, ["out"], ["z", "ids", "dw", "counts", "n", "dl"])
+    _overlaps(_combine, ["y"], ["c", "w", "ids"])
+    _overlaps(_combine_bwd, ["dc", "dw"], ["dy", "c", "w", "ids"])
+    _overlaps(_act, ["h", "q", "s"], ["pre"])
+    _overlaps(_act_bwd, ["dp", "h"], ["q", "s", "dh"])
+    _overlaps(_wgrad, ["dw"], ["xq", "xs", "g", "s", "e"])
+    # what a call leaves out overlaps nothing
+    z, ids, w = _far(3)
+    assert _route(z=z, ids=ids, w=w, stats=0, counts=z, n=z, p=z, loss=z, ws=z) not in (INVALID, UNSUPPORTED)
+    assert _act_bwd(q=z, s=z + 4096, dh=ids, dp=w, h=None, hld=0) not in (INVALID, UNSUPPORTED)
+
+
+def test_strides_past_64_bits_are_rejected(no_device):
+    big = 1 << 40
+    for call, sizes in ((_route, dict(T=1 << 29, ld=big)), (_route_bwd, dict(T=1 << 29, old=big)),
+                        (_combine, dict(T=1 << 29, cld=big)), (_combine_bwd, dict(T=1 << 29, dcld=big)),
+                        (_act, dict(R=1 << 30, pld=big)), (_act_bwd, dict(R=1 << 30, dpld=big))):
+        assert call(**sizes) == INVALID
+        assert b"_ld" in L.moe_last_error()
+
+
 def test_binding_rejects_before_the_library():
     z = torch.zeros(4, 8)
     ids, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
