@@ -105,7 +105,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   //      every step costs the same number of loads.
   const uint32_t g_col0 = (uint32_t)wg_swz(lane / 32, lane % 32) * 16;      // rows 0, 1 of the wave's four
   const uint32_t g_col1 = (uint32_t)wg_swz(2 + lane / 32, lane % 32) * 16;  // rows 2, 3
-  const uint32_t c_col = (uint32_t)(lane % 16) * 16, s_col = (uint32_t)(lane % 16) / 2;
+  const uint32_t c_col = (uint32_t)(lane % 16) * 16, s_col = (uint32_t)(lane % 8);
   const uint32_t g_row = (uint32_t)(p.grad_ld * 2), x_row = (uint32_t)p.x_ld, s_row = (uint32_t)p.xs_ld;
   const uint32_t m32 = lane & 32 ? ~0u : 0u, m16 = lane & 16 ? ~0u : 0u;
   // a where the mask is set, else b
@@ -173,27 +173,26 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   };
 
   // ---- decoding: this wave's pieces of a unit's codes into its rows of x.
-  //      Lanes 8..15 of a row store their second piece first: the 16 pieces
-  //      that one write serves at a time then lie on distinct banks.
-  u32x4_t raw_c;
-  uint32_t raw_s;
-  const uint32_t c_src = c_dst + (uint32_t)lane * 16, s_src = s_dst + (uint32_t)lane * 4;
+  //      Lane l takes 8 codes of either half of row l / 16, so that 16 lanes'
+  //      pieces of a write are contiguous.
+  u32x2_t raw_c[2];
+  uint32_t raw_s[2];
+  const uint32_t c_src = c_dst + (uint32_t)(lane / 16 * 256 + lane % 16 * 8),
+                 s_src = s_dst + (uint32_t)(lane / 16 * 64 + lane % 16 / 4 * 4);
   auto read_raw = [&](int slot) {
-    raw_c = *(const mx_lds<u32x4_t>*)(c_src + (uint32_t)(slot * kMxCodeB));
-    raw_s = *(const mx_lds<uint32_t>*)(s_src + (uint32_t)(slot * kMxScaleB));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      raw_c[i] = *(const mx_lds<u32x2_t>*)(c_src + (uint32_t)(slot * kMxCodeB + i * 128));
+      raw_s[i] = *(const mx_lds<uint32_t>*)(s_src + (uint32_t)(slot * kMxScaleB + i * 16));
+    }
   };
-  const int dm = wave * 4 + lane / 16, du = 2 * (lane % 16);
-  const int dsw = (lane / 8) & 1;
-  const uint32_t m8 = dsw ? ~0u : 0u;
-  const uint32_t d_at0 = x_lds + (uint32_t)(dm * kMxRowB + wg_swz(dm, du + dsw) * 16),
-                 d_at1 = x_lds + (uint32_t)(dm * kMxRowB + wg_swz(dm, du + 1 - dsw) * 16);
+  const int dm = wave * 4 + lane / 16;
+  const uint32_t d_at = x_lds + (uint32_t)(dm * kMxRowB + wg_swz(dm, lane % 16) * 16);  // (+ 16 pieces keep the swizzle)
   auto decode = [&](int slot) {
-    const float scale = e8m0_as_scale(raw_s);
-    // (selected by bit logic, one operation a dword)
-    const uint32_t c0 = pick(m8, raw_c[2], raw_c[0]), c1 = pick(m8, raw_c[3], raw_c[1]);
-    const uint32_t c2 = pick(m8, raw_c[0], raw_c[2]), c3 = pick(m8, raw_c[1], raw_c[3]);
-    *(mx_lds<bf16x8_t>*)(d_at0 + (uint32_t)(slot * kWgXUnitB)) = dequant_e4m3x8(c0, c1, scale);
-    *(mx_lds<bf16x8_t>*)(d_at1 + (uint32_t)(slot * kWgXUnitB)) = dequant_e4m3x8(c2, c3, scale);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *(mx_lds<bf16x8_t>*)(d_at + (uint32_t)(slot * kWgXUnitB + i * 256)) =
+          dequant_e4m3x8(raw_c[i][0], raw_c[i][1], e8m0_as_scale(raw_s[i]));
   };
 
   // ---- computation: wave (wn, wk) of 4 x 2 computes dW rows n0 + wn*64 ..
