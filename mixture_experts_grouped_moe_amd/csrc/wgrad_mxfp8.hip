@@ -107,11 +107,11 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   const uint32_t g_col1 = (uint32_t)wg_swz(2 + lane / 32, lane % 32) * 16;  // rows 2, 3
   const uint32_t c_col = (uint32_t)(lane % 16) * 16, s_col = (uint32_t)(lane % 8);
   const uint32_t g_row = (uint32_t)(p.grad_ld * 2), x_row = (uint32_t)p.x_ld, s_row = (uint32_t)p.xs_ld;
-  const uint32_t m32 = lane & 32 ? ~0u : 0u, m16 = lane & 16 ? ~0u : 0u;
-  // a where the mask is set, else b
-  auto pick = [](uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); };
-  const bool whole = p.top_k == 1;
-  const int div_shift = whole ? 0 : p.topk_shift - 32;
+  // masks of the lanes whose row of the wave's four is at least 1, 2, 3
+  const uint32_t from[4] = {~0u, lane >= 16 ? ~0u : 0u, lane >= 32 ? ~0u : 0u, lane >= 48 ? ~0u : 0u};
+  // s / top_k without a branch: the multiply-high for top_k > 1, s for 1
+  const uint32_t div_mul = p.top_k == 1 ? 0 : p.topk_magic, div_one = p.top_k == 1 ? ~0u : 0u;
+  const int div_shift = p.top_k == 1 ? 0 : p.topk_shift - 32;
 
   int ld_it = 0, ld_u = 0, ld_n = 0;
   WgTile ld{};
@@ -148,26 +148,40 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
     if (ld_live && ld_u >= ld_n) ld_tile();
   };
   // Byte offsets of the lane's pieces of a unit: its two grad loads', its
-  // codes' (16 lanes a row) and its scale's. A PAD slot (s = S) lands at or
-  // past the end of every buffer; past the last tile the ids are 0 and the
-  // bases put every lane past them.
-  struct Offs {
-    uint32_t g0, g1, c, s;
+  // codes' (16 lanes a row) and its scale's. The slots are scalars, so the
+  // products are formed on the scalar unit and a lane adds up the differences
+  // between rows as far as its own: two full-rate operations for each of the
+  // wave's rows. A PAD slot (s = S) lands at or past the end of every buffer;
+  // past the last tile the ids are 0 and the bases put every lane past them.
+  struct Codes {
+    uint32_t c, s, row;  // row: the last one added, a scalar
   };
-  auto offsets = [&](const wg_i32x4_t& id) {
-    const uint32_t i0 = (uint32_t)id[0], i1 = (uint32_t)id[1], i2 = (uint32_t)id[2], i3 = (uint32_t)id[3];
-    const uint32_t a = pick(m32, i1, i0), b = pick(m32, i3, i2);
-    const uint32_t sl = pick(m32, pick(m16, i3, i2), pick(m16, i1, i0));
-    const uint32_t row = whole ? sl : __umulhi(sl, p.topk_magic) >> div_shift;
-    return Offs{a * g_row + (g_base + g_col0), b * g_row + (g_base + g_col1), row * x_row + (x_base + c_col),
-                row * s_row + (s_base + s_col)};
+  auto codes_row = [&](Codes& o, const wg_i32x4_t& id, int q) {  // q = 0 .. 3 in turn
+    const uint32_t sl = (uint32_t)id[q];
+    const uint32_t row = (__umulhi(sl, div_mul) | (sl & div_one)) >> div_shift;
+    if (q == 0) {
+      o.c = c_col + (row * x_row + x_base);
+      o.s = s_col + (row * s_row + s_base);
+    } else {
+      const uint32_t d = row - o.row;
+      o.c += (d * x_row) & from[q];
+      o.s += (d * s_row) & from[q];
+    }
+    o.row = row;
+    asm volatile("" : "+v"(o.c), "+v"(o.s));  // formed here, not where it is used
+  };
+  auto grad_offset = [&](const wg_i32x4_t& id, int half) {
+    const uint32_t a = (uint32_t)id[2 * half], b = (uint32_t)id[2 * half + 1];
+    uint32_t off = (half ? g_col1 : g_col0) + (a * g_row + g_base) + (((b - a) * g_row) & from[2]);
+    asm volatile("" : "+v"(off));
+    return off;
   };
   const uint32_t g_dst = g_lds + (uint32_t)(wave * 2048), c_dst = c_lds + (uint32_t)(wave * 1024),
                  s_dst = s_lds + (uint32_t)(wave * 256);
   auto dma_grads = [&](int slot, int half, uint32_t off) {
     wg_dma16(g_rsrc, off, g_dst + (uint32_t)(slot * kWgGUnitB + half * 1024));
   };
-  auto dma_codes = [&](int slot, const Offs& o) {
+  auto dma_codes = [&](int slot, const Codes& o) {
     wg_dma16(x_rsrc, o.c, c_dst + (uint32_t)(slot * kMxCodeB));
     wg_dma_byte(s_rsrc, o.s, s_dst + (uint32_t)(slot * kMxScaleB));
   };
@@ -254,7 +268,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
     mx_lds<float>* scr = (mx_lds<float>*)&lds_x[x_slot][wave * 2048];
     const int row0 = t.n0 + wn * 64, rows = p.N - row0;  // rows of this wave's part that exist
     const int k = t.k0 + wk * 128 + 4 * (lane % 16);
-    const uint32_t row_b = (uint32_t)p.K * 4;
+    const int row_b = p.K * 4;  // (one expert's dW spans less than 2 GB)
     const uint32_t base = (uint32_t)(((int64_t)(row0 + lane / 16) * p.K + k) * 4);  // (below 2^31 where it is used)
 #pragma unroll
     for (int pass = 0; pass < 16; ++pass) {
@@ -270,9 +284,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
         const f32x4_t v =
             *(const mx_lds<f32x4_t>*)&scr[lr * 64 + ((4 * (lane % 16)) ^ (32 * rd))];
         const int r = i * 32 + 8 * q + 4 * rd;
-        const uint32_t off =
-            (r + lane / 16 < rows && k + jh * 64 < p.K) ? base + (uint32_t)r * row_b + (uint32_t)(jh * 256) : kWgOOB;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(wg_i32x4_t, v), dw_rsrc, off, 0, kWgStoreNT);
+        const uint32_t off = (r + lane / 16 < rows && k + jh * 64 < p.K) ? base : kWgOOB;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(wg_i32x4_t, v), dw_rsrc, off,
+                                               r * row_b + jh * 256, kWgStoreNT);
       }
     }
   };
@@ -290,23 +304,30 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
 
   // ---- prologue: codes of unit 0, then grads of units 0 .. 2 with codes of
   //      1 .. 3; unit 0 decoded
+  Codes codes;
+  uint32_t g0, g1;
+  auto load_codes = [&](int slot, const wg_i32x4_t& id) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) codes_row(codes, id, q);
+    dma_codes(slot, codes);
+  };
+  auto load_grads = [&](int slot, const wg_i32x4_t& id) {
+    dma_grads(slot, 0, grad_offset(id, 0));
+    dma_grads(slot, 1, grad_offset(id, 1));
+  };
   ld_tile();
   ld_ids(ids_e, ids_o);
-  Offs oe = offsets(ids_e), oo = offsets(ids_o);
-  dma_codes(0, oe);
-  dma_grads(0, 0, oe.g0);
-  dma_grads(0, 1, oe.g1);
-  dma_codes(1, oo);
-  dma_grads(1, 0, oo.g0);
-  dma_grads(1, 1, oo.g1);
+  load_codes(0, ids_e);
+  load_grads(0, ids_e);
+  load_codes(1, ids_o);
+  load_grads(1, ids_o);
   ld_next();
   ld_ids(ids_e, ids_o);
-  oe = offsets(ids_e);
-  oo = offsets(ids_o);
-  dma_codes(2, oe);
-  dma_grads(2, 0, oe.g0);
-  dma_grads(2, 1, oe.g1);
-  dma_codes(3, oo);
+  load_codes(2, ids_e);
+  load_grads(2, ids_e);
+  load_codes(3, ids_o);
+  g0 = grad_offset(ids_o, 0);
+  g1 = grad_offset(ids_o, 1);
   ld_next();
   ld_ids(ids_e, ids_o);
   mx_wait<3 * kMxLoads>();
@@ -356,8 +377,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
     ++since;
   };
   // the products of unit u - 1's second half with unit `unit`'s first operand
-  // reads and the grad loads into g_slot; raw codes from c_slot
-  auto first_half = [&](int unit, int g_slot, uint32_t g0, uint32_t g1, int c_slot) {
+  // reads and the grad loads into g_slot (offsets g0, g1); raw codes from
+  // c_slot; the offsets of the codes of slots `id`
+  auto first_half = [&](int unit, int g_slot, int c_slot, const wg_i32x4_t& id) {
     read_a(even, 0, unit, 0);
     read_b(even, 0, unit, 0);
     mul(odd, 0, 0);
@@ -367,6 +389,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
     fence();
     read_b(even, 1, unit, 0);
     read_b(even, 2, unit, 0);
+    codes_row(codes, id, 0);
     mul(odd, 0, 2);
     fence();
     dma_grads(g_slot, 1, g1);
@@ -374,29 +397,33 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
     fence();
     read_b(even, 3, unit, 0);
     read_a(even, 1, unit, 0);
+    codes_row(codes, id, 1);
     mul(odd, 1, 0);
     fence();
     read_raw(c_slot);
+    codes_row(codes, id, 2);
     mul(odd, 1, 1);
+    fence();
+    codes_row(codes, id, 3);
     mul(odd, 1, 2);
     mul(odd, 1, 3);
     fence();
   };
-  // the products of its first half, with the loads of a later unit's codes
-  // into c_slot (unit 0 forms the offsets of the later pair), the decoding of
-  // the next unit into x_slot and the operand reads of its second half
-  auto second_half = [&](int unit, int c_slot, int x_slot) {
+  // the products of its first half, with the loads of the codes of `id` into
+  // c_slot and the offsets of its grads, the decoding of the next unit into
+  // x_slot and the operand reads of its second half
+  auto second_half = [&](int unit, int c_slot, int x_slot, const wg_i32x4_t& id) {
     mul(even, 0, 0);
-    if (unit == 0) oe = offsets(ids_e);
+    dma_codes(c_slot, codes);
     mul(even, 0, 1);
     fence();
-    dma_codes(c_slot, unit == 0 ? oe : oo);
+    g0 = grad_offset(id, 0);
     mul(even, 0, 2);
-    if (unit == 0) oo = offsets(ids_o);
     fence();
     decode(x_slot);
     mul(even, 0, 3);
     fence();
+    g1 = grad_offset(id, 1);
     // the next ids here: no LDS result is waited for before the barrier's own
     // wait (scalar loads return out of order, so a wait for LDS with one in
     // flight waits for all)
@@ -422,7 +449,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   done.e = -1;
   for (bool go = next_tile(); go;) {
     wait_step();
-    first_half(0, (ring ^ 2) + 1, oo.g0, oo.g1, ring + 1);
+    first_half(0, (ring ^ 2) + 1, ring + 1, ids_e);
     if (uu == 0) {
       if (done.e >= 0) {
         store_tile(done, 1);
@@ -431,10 +458,10 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
       clear();
       fence();
     }
-    second_half(0, ring, 1);
+    second_half(0, ring, 1, ids_e);
     wait_step();
-    first_half(1, ring, oe.g0, oe.g1, ring ^ 2);
-    second_half(1, ring + 1, 0);
+    first_half(1, ring, ring ^ 2, ids_o);
+    second_half(1, ring + 1, 0, ids_o);
     ring ^= 2;
     const uint32_t to = ring ? 2 * kWgGUnitB : 0u - 2 * kWgGUnitB;
     a_addr[0] += to;
