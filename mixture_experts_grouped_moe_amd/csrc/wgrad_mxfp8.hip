@@ -26,8 +26,14 @@
 //    between MFMAs in program order. A wave issues in order and both waves of
 //    a SIMD leave a barrier together, so what stands before or after a run of
 //    MFMAs adds to them: with the loader and the reads in front of the
-//    products the same pipeline ran at 2.6 ms on E = 64, N = 2048, K = 7168
-//    over 65536 slots, its matrix pipe busy 35% of the time.
+//    products, and every XCD taking whole experts, the same pipeline ran at
+//    2.6 ms on E = 64, N = 2048, K = 7168 over 65536 slots.
+//
+// Those sizes now take 2.02 to 2.06 ms, 0.94 PFLOP/s: the matrix pipe is busy 48% of
+// the cycles, at a clock that the chip's power holds at 1.95 GHz (2.4 where
+// the data are zeros). Changes that save cycles alone no longer save time:
+// starting each XCD at an expert of its own took 1.4% fewer cycles and ran as
+// long. A library's dense product of the same size, bf16 out, takes 1.90 ms.
 #include "common.h"
 #include "params.h"
 #include "wgrad_util.h"
@@ -43,6 +49,10 @@ constexpr int kMxCodeB = kWgUM * kWgTK;     // 8 KB: a unit's codes
 constexpr int kMxScaleB = kMxThreads * 4;   // 2 KB: one scale dword per lane
 constexpr int kMxLoads = 4;   // DMA instructions per wave per unit: 2 grads, codes, scales
 constexpr int kMxStores = 32; // 16-byte stores per lane per tile
+// N tiles per group of the tile order: neighbouring tiles write long stretches
+// of the same rows of dW and read the same codes (on the sizes above 2.02 ms,
+// against 2.06 with 1, 2.03 with 3, 2.07 with 4 and 2.08 with 8).
+constexpr int kMxGroupN = 2;
 constexpr int kMxRowB = kWgTN * 2;
 static_assert(kMxRowB == kWgTK * 2, "rows of both operands have one length");
 
@@ -84,7 +94,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   const int l32 = lane % 32, h = lane / 32;
 
   wg_block_ranges<kMxThreads>(p, s_start);
-  const WgSplitOrder order(p, s_start);
+  const WgSplitOrder order(p, s_start, kMxGroupN);
 
   // (PAD slots, s = S, lie past the buffers)
   const int64_t T = p.S / p.top_k;
@@ -108,16 +118,15 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   const uint32_t c_col = (uint32_t)(lane % 16) * 16, s_col = (uint32_t)(lane % 8);
   const uint32_t g_row = (uint32_t)(p.grad_ld * 2), x_row = (uint32_t)p.x_ld, s_row = (uint32_t)p.xs_ld;
   // masks of the lanes whose row of the wave's four is at least 1, 2, 3
-  const uint32_t from[4] = {~0u, lane >= 16 ? ~0u : 0u, lane >= 32 ? ~0u : 0u, lane >= 48 ? ~0u : 0u};
-  // s / top_k without a branch: the multiply-high for top_k > 1, s for 1
-  const uint32_t div_mul = p.top_k == 1 ? 0 : p.topk_magic, div_one = p.top_k == 1 ? ~0u : 0u;
-  const int div_shift = p.top_k == 1 ? 0 : p.topk_shift - 32;
+  uint32_t from[4] = {~0u, lane >= 16 ? ~0u : 0u, lane >= 32 ? ~0u : 0u, lane >= 48 ? ~0u : 0u};
+  asm volatile("" : "+v"(from[1]), "+v"(from[2]), "+v"(from[3]));  // kept as masks: one AND each
+  const int div_shift = p.topk_shift - 31;  // s / top_k = (2 s m) >> (32 + div_shift), top_k = 1 included
 
   int ld_it = 0, ld_u = 0, ld_n = 0;
   WgTile ld{};
   bool ld_live = true;
   wg_i32x4_t ids_e, ids_o;  // the wave's slots of the pair two ahead of the computation's
-  uint32_t g_base = 0, x_base = 0, s_base = 0;
+  uint32_t g_at0 = 0, g_at1 = 0, c_at = 0, s_at = 0;  // the lane's offsets in the tile's columns
   auto ld_tile = [&]() {  // the next tile with slots, from ld_it on
     for (;; ++ld_it) {
       const int at = order.index(ld_it);
@@ -129,9 +138,10 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
     }
     ++ld_it;
     ld_u = 0;
-    g_base = ld_live ? (uint32_t)ld.n0 * 2 : kWgOOB;
-    x_base = ld_live ? (uint32_t)ld.k0 : kWgOOB;
-    s_base = ld_live ? (uint32_t)ld.k0 / 32 : kWgOOB;
+    g_at0 = g_col0 + (ld_live ? (uint32_t)ld.n0 * 2 : kWgOOB);
+    g_at1 = g_col1 + (ld_live ? (uint32_t)ld.n0 * 2 : kWgOOB);
+    c_at = c_col + (ld_live ? (uint32_t)ld.k0 : kWgOOB);
+    s_at = s_col + (ld_live ? (uint32_t)ld.k0 / 32 : kWgOOB);
   };
   // the pair's ids, by scalar loads that the compiler tracks
   auto ld_ids = [&](wg_i32x4_t& e, wg_i32x4_t& o) {
@@ -148,31 +158,31 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
     if (ld_live && ld_u >= ld_n) ld_tile();
   };
   // Byte offsets of the lane's pieces of a unit: its two grad loads', its
-  // codes' (16 lanes a row) and its scale's. The slots are scalars, so the
-  // products are formed on the scalar unit and a lane adds up the differences
-  // between rows as far as its own: two full-rate operations for each of the
-  // wave's rows. A PAD slot (s = S) lands at or past the end of every buffer;
-  // past the last tile the ids are 0 and the bases put every lane past them.
+  // codes' (16 lanes a row) and its scale's. The slots are scalars; a lane's
+  // own is the first plus the differences up to its row, and the grads'
+  // products are formed on the scalar unit. A PAD slot (s = S) lands at or
+  // past the end of every buffer; past the last tile the ids are 0 and the
+  // bases put every lane past them.
   struct Codes {
-    uint32_t c, s, row;  // row: the last one added, a scalar
+    uint32_t c, s, row;
   };
-  auto codes_row = [&](Codes& o, const wg_i32x4_t& id, int q) {  // q = 0 .. 3 in turn
-    const uint32_t sl = (uint32_t)id[q];
-    const uint32_t row = (__umulhi(sl, div_mul) | (sl & div_one)) >> div_shift;
-    if (q == 0) {
-      o.c = c_col + (row * x_row + x_base);
-      o.s = s_col + (row * s_row + s_base);
-    } else {
-      const uint32_t d = row - o.row;
-      o.c += (d * x_row) & from[q];
-      o.s += (d * s_row) & from[q];
-    }
-    o.row = row;
-    asm volatile("" : "+v"(o.c), "+v"(o.s));  // formed here, not where it is used
+  auto codes_slot = [&](Codes& o, const wg_i32x4_t& id) {  // twice the lane's slot, in `row`
+    const uint32_t i0 = (uint32_t)id[0], i1 = (uint32_t)id[1], i2 = (uint32_t)id[2], i3 = (uint32_t)id[3];
+    o.row = (i0 + ((i1 - i0) & from[1]) + ((i2 - i1) & from[2]) + ((i3 - i2) & from[3])) << 1;
+    asm volatile("" : "+v"(o.row));  // formed here, not where it is used (as the others below)
+  };
+  auto codes_row = [&](Codes& o) {
+    o.row = __umulhi(o.row, p.topk_magic) >> div_shift;
+    asm volatile("" : "+v"(o.row));
+  };
+  auto codes_offset = [&](Codes& o) {
+    o.c = o.row * x_row + c_at;
+    o.s = o.row * s_row + s_at;
+    asm volatile("" : "+v"(o.c), "+v"(o.s));
   };
   auto grad_offset = [&](const wg_i32x4_t& id, int half) {
     const uint32_t a = (uint32_t)id[2 * half], b = (uint32_t)id[2 * half + 1];
-    uint32_t off = (half ? g_col1 : g_col0) + (a * g_row + g_base) + (((b - a) * g_row) & from[2]);
+    uint32_t off = (half ? g_at1 : g_at0) + a * g_row + (((b - a) * g_row) & from[2]);
     asm volatile("" : "+v"(off));
     return off;
   };
@@ -193,20 +203,21 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   uint32_t raw_s[2];
   const uint32_t c_src = c_dst + (uint32_t)(lane / 16 * 256 + lane % 16 * 8),
                  s_src = s_dst + (uint32_t)(lane / 16 * 64 + lane % 16 / 4 * 4);
-  auto read_raw = [&](int slot) {
+  // codes at c_rd[next] and scales at s_rd[next], `unit` slots on; [0] is the
+  // ring slot of the current pair, [1] that of the next
+  uint32_t c_rd[2] = {c_src, c_src + 2 * kMxCodeB}, s_rd[2] = {s_src, s_src + 2 * kMxScaleB};
+  auto read_raw = [&](int next, int unit) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      raw_c[i] = *(const mx_lds<u32x2_t>*)(c_src + (uint32_t)(slot * kMxCodeB + i * 128));
-      raw_s[i] = *(const mx_lds<uint32_t>*)(s_src + (uint32_t)(slot * kMxScaleB + i * 16));
+      raw_c[i] = *(const mx_lds<u32x2_t>*)(c_rd[next] + (uint32_t)(unit * kMxCodeB + i * 128));
+      raw_s[i] = *(const mx_lds<uint32_t>*)(s_rd[next] + (uint32_t)(unit * kMxScaleB + i * 16));
     }
   };
   const int dm = wave * 4 + lane / 16;
   const uint32_t d_at = x_lds + (uint32_t)(dm * kMxRowB + wg_swz(dm, lane % 16) * 16);  // (+ 16 pieces keep the swizzle)
-  auto decode = [&](int slot) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *(mx_lds<bf16x8_t>*)(d_at + (uint32_t)(slot * kWgXUnitB + i * 256)) =
-          dequant_e4m3x8(raw_c[i][0], raw_c[i][1], e8m0_as_scale(raw_s[i]));
+  auto decode = [&](int slot, int i) {
+    *(mx_lds<bf16x8_t>*)(d_at + (uint32_t)(slot * kWgXUnitB + i * 256)) =
+        dequant_e4m3x8(raw_c[i][0], raw_c[i][1], __uint_as_float(raw_s[i] << 23));
   };
 
   // ---- computation: wave (wn, wk) of 4 x 2 computes dW rows n0 + wn*64 ..
@@ -307,8 +318,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   Codes codes;
   uint32_t g0, g1;
   auto load_codes = [&](int slot, const wg_i32x4_t& id) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) codes_row(codes, id, q);
+    codes_slot(codes, id);
+    codes_row(codes);
+    codes_offset(codes);
     dma_codes(slot, codes);
   };
   auto load_grads = [&](int slot, const wg_i32x4_t& id) {
@@ -331,8 +343,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   ld_next();
   ld_ids(ids_e, ids_o);
   mx_wait<3 * kMxLoads>();
-  read_raw(0);
-  decode(0);
+  read_raw(0, 0);
+  decode(0, 0);
+  decode(0, 1);
 
   // ---- step u, for the units of the workgroup's tiles in order. At its
   //      barrier: every wave's grads of u and codes of u + 1 have landed (the
@@ -376,54 +389,67 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
       mx_wait_barrier<2 * kMxLoads>();
     ++since;
   };
-  // the products of unit u - 1's second half with unit `unit`'s first operand
-  // reads and the grad loads into g_slot (offsets g0, g1); raw codes from
-  // c_slot; the offsets of the codes of slots `id`
-  auto first_half = [&](int unit, int g_slot, int c_slot, const wg_i32x4_t& id) {
+  // What a wave issues beside the products is spread over the gaps between
+  // them, about ten operations each: with two waves on a SIMD, a gap lasts two
+  // products.
+  //
+  // The products of unit u - 1's second half, with the first operand reads of
+  // unit u (`unit` of its pair), the grad loads into g_slot (offsets g0, g1),
+  // the raw codes of unit u + 1 and the offsets of the codes of slots `id`.
+  auto first_half = [&](int unit, int g_slot, const wg_i32x4_t& id) {
+    mul(odd, 0, 0);
     read_a(even, 0, unit, 0);
     read_b(even, 0, unit, 0);
-    mul(odd, 0, 0);
-    fence();
     dma_grads(g_slot, 0, g0);
-    mul(odd, 0, 1);
     fence();
+    mul(odd, 0, 1);
+    codes_slot(codes, id);
+    fence();
+    mul(odd, 0, 2);
     read_b(even, 1, unit, 0);
     read_b(even, 2, unit, 0);
-    codes_row(codes, id, 0);
-    mul(odd, 0, 2);
-    fence();
     dma_grads(g_slot, 1, g1);
-    mul(odd, 0, 3);
     fence();
+    mul(odd, 0, 3);
+    codes_row(codes);
+    fence();
+    mul(odd, 1, 0);
     read_b(even, 3, unit, 0);
     read_a(even, 1, unit, 0);
-    codes_row(codes, id, 1);
-    mul(odd, 1, 0);
+    read_raw(unit, 1 - unit);
     fence();
-    read_raw(c_slot);
-    codes_row(codes, id, 2);
     mul(odd, 1, 1);
+    codes_offset(codes);
     fence();
-    codes_row(codes, id, 3);
     mul(odd, 1, 2);
+    fence();
     mul(odd, 1, 3);
     fence();
   };
-  // the products of its first half, with the loads of the codes of `id` into
-  // c_slot and the offsets of its grads, the decoding of the next unit into
-  // x_slot and the operand reads of its second half
+  // The products of its first half, with the code loads (of slots `id`) into
+  // c_slot and the offsets of their grads, the decoding of the next unit into
+  // x_slot and the operand reads of the second half.
   auto second_half = [&](int unit, int c_slot, int x_slot, const wg_i32x4_t& id) {
     mul(even, 0, 0);
     dma_codes(c_slot, codes);
+    fence();
     mul(even, 0, 1);
+    decode(x_slot, 0);
     fence();
-    g0 = grad_offset(id, 0);
     mul(even, 0, 2);
+    decode(x_slot, 1);
     fence();
-    decode(x_slot);
     mul(even, 0, 3);
+    read_a(odd, 0, unit, 1);
+    read_b(odd, 0, unit, 1);
+    g0 = grad_offset(id, 0);
     fence();
+    mul(even, 1, 0);
+    read_b(odd, 1, unit, 1);
+    read_b(odd, 2, unit, 1);
     g1 = grad_offset(id, 1);
+    fence();
+    mul(even, 1, 1);
     // the next ids here: no LDS result is waited for before the barrier's own
     // wait (scalar loads return out of order, so a wait for LDS with one in
     // flight waits for all)
@@ -432,16 +458,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
       ld_ids(ids_e, ids_o);
       fence();
     }
-    read_a(odd, 0, unit, 1);
-    read_b(odd, 0, unit, 1);
-    mul(even, 1, 0);
-    fence();
-    read_b(odd, 1, unit, 1);
-    read_b(odd, 2, unit, 1);
-    mul(even, 1, 1);
-    fence();
     read_b(odd, 3, unit, 1);
     read_a(odd, 1, unit, 1);
+    fence();
     mul(even, 1, 2);
     mul(even, 1, 3);
     fence();
@@ -449,7 +468,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
   done.e = -1;
   for (bool go = next_tile(); go;) {
     wait_step();
-    first_half(0, (ring ^ 2) + 1, ring + 1, ids_e);
+    first_half(0, (ring ^ 2) + 1, ids_e);
     if (uu == 0) {
       if (done.e >= 0) {
         store_tile(done, 1);
@@ -460,12 +479,15 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
     }
     second_half(0, ring, 1, ids_e);
     wait_step();
-    first_half(1, ring, ring ^ 2, ids_o);
+    first_half(1, ring, ids_o);
     second_half(1, ring + 1, 0, ids_o);
     ring ^= 2;
-    const uint32_t to = ring ? 2 * kWgGUnitB : 0u - 2 * kWgGUnitB;
+    const int to = ring ? 2 * kWgGUnitB : -2 * kWgGUnitB;
+    static_assert(kWgGUnitB == 2 * kMxCodeB && kWgGUnitB == 8 * kMxScaleB, "one step for the three rings");
     a_addr[0] += to;
     a_addr[1] += to;
+    c_rd[0] += to / 2, c_rd[1] -= to / 2;
+    s_rd[0] += to / 8, s_rd[1] -= to / 8;
     uu += 2;
     if (uu == nu) {
       done = t;

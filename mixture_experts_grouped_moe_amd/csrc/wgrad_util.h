@@ -111,16 +111,17 @@ __device__ __forceinline__ void wg_block_ranges(const WgradParams& p, int32_t* s
   __syncthreads();
 }
 
-// Tile order: expert-major; within an expert, groups of kWgGroupN N tiles
-// walked N-fastest then K, so any kWgGroupN x (64 / kWgGroupN) consecutive
+// Tile order: expert-major; within an expert, groups of group_n N tiles
+// walked N-fastest then K, so any group_n x (64 / group_n) consecutive
 // tiles share a few grad and x slices. XCD x (= hardware id % 8) owns the
 // x-th eighth of the sequence, and its G/8 workgroups take consecutive
 // tiles of it round by round (G = gridDim.x).
 struct WgOrder {
   const WgradParams& p;
   const int32_t* s_start;
-  int per_e, total, G, xcd, local, chunk;
-  __device__ __forceinline__ WgOrder(const WgradParams& p_, const int32_t* s) : p(p_), s_start(s) {
+  int per_e, total, G, xcd, local, chunk, group_n;
+  __device__ __forceinline__ WgOrder(const WgradParams& p_, const int32_t* s, int group = kWgGroupN)
+      : p(p_), s_start(s), group_n(group) {
     per_e = p.tiles_n * p.tiles_k;
     total = p.E * per_e;  // below 2^31 (checked by the host API)
     G = gridDim.x;
@@ -138,9 +139,9 @@ struct WgOrder {
     WgTile t;
     t.e = T / per_e;
     const int r = T % per_e;
-    const int in_group = kWgGroupN * p.tiles_k;
-    const int first_n = (r / in_group) * kWgGroupN;
-    const int gsize = min(p.tiles_n - first_n, kWgGroupN);
+    const int in_group = group_n * p.tiles_k;
+    const int first_n = (r / in_group) * group_n;
+    const int gsize = min(p.tiles_n - first_n, group_n);
     t.n0 = (first_n + (r % in_group) % gsize) * kWgTN;
     t.k0 = ((r % in_group) / gsize) * kWgTK;
     t.b0 = __builtin_amdgcn_readfirstlane(s_start[t.e]);
@@ -160,7 +161,8 @@ struct WgSplitOrder {
   WgOrder base;
   int per_e, step, xcd, local;
   int total;  // tiles of this XCD
-  __device__ __forceinline__ WgSplitOrder(const WgradParams& p, const int32_t* s_start) : base(p, s_start) {
+  __device__ __forceinline__ WgSplitOrder(const WgradParams& p, const int32_t* s_start, int group)
+      : base(p, s_start, group) {
     per_e = base.per_e;
     step = base.G / 8;
     xcd = base.xcd;
