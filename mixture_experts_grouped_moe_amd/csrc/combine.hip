@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(
 // waves, whose slots are the same token's, find its dy in the cache. (One
 // workgroup per token, which reads dy once, took as long for many tokens and
 // longer for few: 9.8 us against 5.5 at 333 tokens of 4 slots, width 2880.)
-// 8192 tokens of 8 slots, width 7168, an eighth of them padding: 351 us, 5.7 TB/s.
+// 8192 tokens of 8 slots, width 7168, an eighth of them padding: 351 us, 5.6 TB/s.
 constexpr int kCombineBwdUnroll = 4;
 
 __global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(
