@@ -376,6 +376,33 @@ __global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RoutePara
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int l = lane % LPR, group = lane / LPR;
   float* su = s_u[wave][group];
+  // A row's loads, before what does not need them and without a branch between
+  // them: one that waits for another costs its latency. (So the logits also of
+  // a row routed nowhere, and clamped places.)
+  float z[VPL], dwj[NJ];
+  int idj[NJ], first;
+  const auto load = [&](int64_t t) {
+    const int64_t s0 = min(t, p.T - 1) * p.k;
+    first = p.ids[s0];
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj) {
+      const int64_t s = s0 + min(jj * LPR + l, p.k - 1);
+      idj[jj] = p.ids[s];
+      dwj[jj] = p.dw[s];
+    }
+    rt_load_row<T, LPR, VPL>(static_cast<const T*>(p.logits) + t * p.ld, p.E, l, t < p.T, z);
+  };
+  const int64_t step = (int64_t)gridDim.x * kRtWaves * RPW;
+  int64_t t0 = ((int64_t)blockIdx.x * kRtWaves + wave) * RPW;
+  int32_t count[VPL];
+  if (p.dlosses != nullptr) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = ((i / V::N) * LPR + l) * V::N + i % V::N;
+      count[i] = p.counts[min(e, p.E - 1)];
+    }
+  }
+  load(t0 + group);
   float cost[VPL], zcoef = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -389,29 +416,24 @@ __global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RoutePara
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = ((i / V::N) * LPR + l) * V::N + i % V::N;
-      if (e < p.E) cost[i] = f * (float)p.counts[e];
+      cost[i] = e < p.E ? f * (float)count[i] : 0.0f;
     }
     if (!SIGMOID) zcoef = 2.0f * p.dlosses[1] / n;
   }
-  const int64_t step = (int64_t)gridDim.x * kRtWaves * RPW;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kRtWaves + wave) * RPW; t0 < p.T; t0 += step) {
+  for (; t0 < p.T; t0 += step) {
     const int64_t t = t0 + group;
-    const bool on = t < p.T && p.ids[t * p.k] >= 0;
+    const bool on = t < p.T && first >= 0;
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-    float z[VPL];
-    rt_load_row<T, LPR, VPL>(row, p.E, l, on, z);
     // the chosen experts in places l, l + LPR, ..
     int id[NJ];
     float g[NJ], zj[NJ];
     float top = rt_neg_inf();
 #pragma unroll
     for (int jj = 0; jj < NJ; ++jj) {
-      const int j = jj * LPR + l;
-      id[jj] = on && j < p.k ? p.ids[t * p.k + j] : -1;
-      const bool ok = (uint32_t)id[jj] < (uint32_t)p.E;
-      id[jj] = ok ? id[jj] : -1;
+      const bool ok = on && jj * LPR + l < p.k && (uint32_t)idj[jj] < (uint32_t)p.E;
+      id[jj] = ok ? idj[jj] : -1;
       zj[jj] = ok ? V::one(row + id[jj]) : rt_neg_inf();
-      g[jj] = ok ? p.scale * p.dw[t * p.k + j] : 0.0f;
+      g[jj] = ok ? p.scale * dwj[jj] : 0.0f;
       top = fmaxf(top, zj[jj]);
     }
     float m = rt_neg_inf();
@@ -484,6 +506,7 @@ __global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RoutePara
     for (int jj = 0; jj < NJ; ++jj)
       if (id[jj] >= 0) su[id[jj]] = 0.0f;
     __builtin_amdgcn_wave_barrier();
+    load(t + step);
   }
 }
 

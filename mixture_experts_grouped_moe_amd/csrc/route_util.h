@@ -214,27 +214,36 @@ __device__ __forceinline__ void rt_load_row(const T* row, int E, int l, bool on,
     }
     return;
   }
+  // No branch per piece: a load behind a branch waits for the one before it.
+  // A lane whose piece lies past E, or is partial, reads the row's first
+  // instead (none if E < N, where all are partial).
 #pragma unroll
   for (int i = 0; i < VPL; ++i) z[i] = rt_neg_inf();
   if (!on) return;
-#pragma unroll
-  for (int c = 0; c < VPL / V::N; ++c) {
-    const int e = (c * LPR + l) * V::N;
-    if (e + V::N <= E) {
-      const typename V::vec v = *reinterpret_cast<const typename V::vec*>(row + e);
-#pragma unroll
-      for (int i = 0; i < V::N; ++i) z[c * V::N + i] = V::get(v, i);
-    }
-  }
-  if (E % V::N != 0) {  // the last, partial piece
+  if (E >= V::N) {
+    typename V::vec v[VPL / V::N];
 #pragma unroll
     for (int c = 0; c < VPL / V::N; ++c) {
       const int e = (c * LPR + l) * V::N;
-      if (e < E && e + V::N > E)
-#pragma unroll
-        for (int i = 0; i < V::N - 1; ++i)
-          if (e + i < E) z[c * V::N + i] = V::one(row + e + i);
+      v[c] = *reinterpret_cast<const typename V::vec*>(row + (e + V::N <= E ? e : 0));
     }
+#pragma unroll
+    for (int c = 0; c < VPL / V::N; ++c)
+#pragma unroll
+      for (int i = 0; i < V::N; ++i)
+        z[c * V::N + i] = (c * LPR + l) * V::N + V::N <= E ? V::get(v[c], i) : rt_neg_inf();
+  }
+  if (E % V::N != 0) {  // the last, partial piece: of lane (E / N) % LPR
+    if (E / V::N % LPR != l) return;
+    const int last = E / V::N * V::N;
+    float x[V::N - 1];
+#pragma unroll
+    for (int i = 0; i < V::N - 1; ++i) x[i] = V::one(row + min(last + i, E - 1));
+#pragma unroll
+    for (int c = 0; c < VPL / V::N; ++c)
+#pragma unroll
+      for (int i = 0; i < V::N - 1; ++i)
+        if (last == (c * LPR + l) * V::N && last + i < E) z[c * V::N + i] = x[i];
   }
 }
 
