@@ -89,7 +89,7 @@ int64_t moe_route_workspace_bytes(int64_t num_tokens, int32_t num_experts);
  * (the lse term for softmax scores only), dlogits[t][e] = da[e] for softmax,
  * da[e] * (1 - sigmoid(z_e)) for sigmoid scores.
  * Every row of dlogits is written (in logits' type, rounded once); a token
- * whose first id is negative gets zeros and its logits are not read. Ids
+ * whose first id is negative gets zeros, whatever its logits hold. Ids
  * outside [0, E) past the first contribute nothing; an expert named twice gets
  * both terms.
  * dtopk_w (device) fp32 [T][top_k]; entries at ids of -1 are ignored. dlosses

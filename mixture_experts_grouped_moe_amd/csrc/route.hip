@@ -22,7 +22,7 @@
 // replace by a read of the same size. The chosen experts' terms go through a
 // row of LDS that is zero otherwise, so adding them costs one scattered add
 // and one read however many there are. 65536 x 256 fp32, an eighth of the rows
-// padding: 30 us, 4.3 TB/s.
+// padding: 27 us, 5.1 TB/s.
 //
 // Statistics: each lane adds its rows' probabilities into registers, a
 // workgroup adds its lanes' and writes one partial row, and a second launch
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(kRtFinThreads) void route_finish_kernel(RouteParams
 
 // NJ: places of a row per lane (top_k <= NJ * LPR).
 template <class T, int LPR, int VPL, int NJ, bool SIGMOID>
-__global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RouteParams p) {
+__global__ __launch_bounds__(kRtThreads, NJ > 4 ? 2 : 4) void route_backward_kernel(RouteParams p) {
   using V = RtVec<T>;
   constexpr int RPW = 64 / LPR;
   constexpr int WIDTH = LPR * VPL + 32;  // (rows a bank group apart)
@@ -510,9 +510,10 @@ __global__ __launch_bounds__(kRtThreads, 4) void route_backward_kernel(RoutePara
   }
 }
 
-// Rows that one workgroup takes at a time (rt_layout, rt_layout_deep).
+// Rows that one workgroup takes at a time (rt_layout, and with 32 and 8 logits a lane).
 static int rt_rows(int E) { return kRtWaves * (E <= 128 ? 8 : E <= 256 ? 4 : E <= 512 ? 2 : 1); }
 static int rt_rows_deep(int E) { return kRtWaves * (E <= 256 ? 8 : E <= 512 ? 4 : 2); }
+static int rt_rows_spread(int E) { return kRtWaves * (E <= 128 ? 4 : E <= 256 ? 2 : 1); }
 
 static uint32_t rt_grid(int64_t T, int rows, int most = kRtMaxGrid) {
   const int64_t want = (T + rows - 1) / rows;
@@ -533,6 +534,13 @@ static bool rt_deep(int64_t T, int E) { return E > 128 && T >= (int64_t)kRtMaxGr
 int64_t route_workspace_bytes(int64_t T, int32_t E) {
   return 64 * 8 + 8 + (int64_t)rt_grid(T, kRtWaves) * ((int64_t)E + 1) * 8;
 }
+
+// Backward pass of 65 to 512 experts: with 8 logits a lane a wave has half the
+// rows and half the instructions, which bound it while every wave takes its
+// rows once. It pays up to one workgroup per CU of the usual 256 (with the
+// losses: 4096 x 256 fp32 6.6 -> 5.3 us, bf16 8.9 -> 6.2; 8192 x 256 7.7
+// either way; 65536 x 512 49 -> 55).
+static bool rt_spread(int64_t T, int E) { return E > 64 && E <= 512 && T <= (int64_t)256 * rt_rows_spread(E); }
 
 template <int N>
 using rt_c = std::integral_constant<int, N>;
@@ -556,6 +564,22 @@ static void rt_layout(int E, bool bf16, F&& f) {
     by_type(rt_c<32>{}, rt_c<16>{});
   else
     by_type(rt_c<64>{}, rt_c<16>{});
+}
+// With 8 logits a lane (64 < E <= 512).
+template <class F>
+static void rt_layout_spread(int E, bool bf16, F&& f) {
+  auto by_type = [&](auto lpr) {
+    if (bf16)
+      f(uint16_t{}, lpr, rt_c<8>{});
+    else
+      f(float{}, lpr, rt_c<8>{});
+  };
+  if (E <= 128)
+    by_type(rt_c<16>{});
+  else if (E <= 256)
+    by_type(rt_c<32>{});
+  else
+    by_type(rt_c<64>{});
 }
 // With 32 logits a lane (E > 128).
 template <class F>
@@ -643,9 +667,10 @@ hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t s
 }
 
 hipError_t launch_route_backward(const RouteParams& p, bool bf16, hipStream_t stream) {
-  const uint32_t grid = rt_grid(p.T, rt_rows(p.E));
+  const bool spread = rt_spread(p.T, p.E);
+  const uint32_t grid = rt_grid(p.T, spread ? rt_rows_spread(p.E) : rt_rows(p.E));
   if (grid == 0) return hipSuccess;
-  rt_layout(p.E, bf16, [&](auto t, auto lpr, auto vpl) {
+  auto go = [&](auto t, auto lpr, auto vpl) {
     using T = decltype(t);
     constexpr int R = decltype(lpr)::value, N = decltype(vpl)::value;
     auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kRtThreads), 0, stream, p); };
@@ -662,7 +687,11 @@ hipError_t launch_route_backward(const RouteParams& p, bool bf16, hipStream_t st
       by_score(rt_c<2>{});
     else
       by_score(rt_c<64 / R>{});
-  });
+  };
+  if (spread)
+    rt_layout_spread(p.E, bf16, go);
+  else
+    rt_layout(p.E, bf16, go);
   return hipGetLastError();
 }
 

@@ -197,8 +197,9 @@ struct RtVec<uint16_t> {
   typedef uint16_t vec __attribute__((ext_vector_type(8), aligned(2)));
   __device__ static float get(vec v, int i) { return bf16_bits_to_f32(v[i]); }
   __device__ static float one(const uint16_t* p) { return bf16_bits_to_f32(*p); }
-  __device__ static void put(vec& v, int i, float x) { v[i] = (uint16_t)f32_to_bf16_bits(x); }
-  __device__ static void put(uint16_t* p, float x) { *p = (uint16_t)f32_to_bf16_bits(x); }
+  __device__ static uint16_t bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }  // nearest even
+  __device__ static void put(vec& v, int i, float x) { v[i] = bits(x); }
+  __device__ static void put(uint16_t* p, float x) { *p = bits(x); }
 };
 
 // A row's logits, VPL per lane; -inf past E and where !on.

@@ -160,6 +160,21 @@ def test_route_long_batches(T, E, k, score, dtype):
     check_route(z, k, score, False)
 
 
+# up to 256 workgroups' rows a lane takes 8 logits of a row, past them 16
+@pytest.mark.parametrize("T,E,k,score", [(8193, 100, 4, "softmax"), (8192, 128, 20, "sigmoid"),
+                                         (4100, 160, 6, "sigmoid"), (4096, 256, 33, "softmax"),
+                                         (2049, 500, 10, "softmax"), (2048, 512, 64, "sigmoid"),
+                                         (9000, 72, 10, "softmax"), (5000, 255, 17, "softmax")])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_route_gradient_of_long_batches(T, E, k, score, dtype):
+    z = logits(T, E, T + E + 1, dtype)
+    z[T - 1, 1:] = float("-inf")
+    mask = (torch.rand(T, generator=synth.gen(T + E, "mask")) < 0.9).cuda()
+    for renorm in (True, False):
+        fwd = check_route(z, k, score, renorm, 0.5, mask)
+        check_route_backward(z, k, fwd, score, renorm, 0.5)
+
+
 def test_route_ties_take_the_lowest_expert():
     # logits of few distinct values, both zeros among them
     g = synth.gen(5, "ties")
