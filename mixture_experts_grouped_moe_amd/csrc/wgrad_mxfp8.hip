@@ -29,7 +29,7 @@
 //    products, and every XCD taking whole experts, the same pipeline ran at
 //    2.6 ms on E = 64, N = 2048, K = 7168 over 65536 slots.
 //
-// Those sizes now take 2.02 to 2.06 ms, 0.94 PFLOP/s: the matrix pipe is busy 48% of
+// Those sizes now take 2.02 to 2.16 ms from card to card, 0.9 PFLOP/s: the matrix pipe is busy 48% of
 // the cycles, at a clock that the chip's power holds at 1.95 GHz (2.4 where
 // the data are zeros). Changes that save cycles alone no longer save time:
 // starting each XCD at an expert of its own took 1.4% fewer cycles and ran as

@@ -135,6 +135,15 @@ def _flat(t, name, dtype, shape):
         raise ValueError(f"{name} must be a contiguous {list(shape)}, got {list(t.shape)}")
 
 
+def _table(t, name, dtype):
+    """Checks a contiguous 2-d device tensor; its shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or t.dim() != 2:
+        _need(t, name, dtype, 2)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape
+
+
 def _logits(t):
     """(T, E, row stride) of the router's logits."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _LOGITS:
@@ -216,8 +225,9 @@ def moe_route_backward(logits, topk_ids, dtopk_w, score="softmax", renormalize=T
     logits, topk_ids, score, renormalize and scale as in the forward pass;
     the experts chosen there are held constant."""
     T, E, ld = _logits(logits)
-    k = _mat(topk_ids, "topk_ids", torch.int32)[1]
-    _flat(topk_ids, "topk_ids", torch.int32, (T, k))
+    rows, k = _table(topk_ids, "topk_ids", torch.int32)
+    if rows != T:
+        raise ValueError(f"topk_ids must be [{T}, {k}], got {[rows, k]}")
     _flat(dtopk_w, "dtopk_w", torch.float32, (T, k))
     losses = (None,) * 3
     if dlosses is not None:
@@ -244,8 +254,7 @@ def moe_combine_routed(c, topk_w, topk_ids, num_experts, out=None):
     """moe_combine over the slots whose id lies in [0, num_experts): y[t] =
     sum_j topk_w[t, j] * c[t * top_k + j] (fp32, bf16 out). The other slots'
     rows of c, which the grouped GEMM leaves as they were, are not read."""
-    T, k, _ = _mat(topk_ids, "topk_ids", torch.int32)
-    _flat(topk_ids, "topk_ids", torch.int32, (T, k))
+    T, k = _table(topk_ids, "topk_ids", torch.int32)
     _flat(topk_w, "topk_w", torch.float32, (T, k))
     rows, N, cld = _mat(c, "c", torch.bfloat16)
     if rows < T * k:
@@ -269,10 +278,10 @@ def moe_combine_backward(dy, c, topk_w, topk_ids=None, num_experts=None, out=Non
     [T, top_k]; with topk_ids (int32 [T, top_k]) and num_experts, slots routed
     nowhere get zeros and their rows of c are not read. Returns (dC, dtopk_w);
     `out` may give both (not overlapping the inputs)."""
-    T, k, _ = _mat(topk_w, "topk_w", torch.float32)
-    _flat(topk_w, "topk_w", torch.float32, (T, k))
-    N = _mat(dy, "dy", torch.bfloat16)[1]
-    dyld = _mat(dy, "dy", torch.bfloat16, T, N)[2]
+    T, k = _table(topk_w, "topk_w", torch.float32)
+    rows, N, dyld = _mat(dy, "dy", torch.bfloat16)
+    if rows < T:
+        raise ValueError(f"dy must hold {T} rows, got {rows}")
     cld = _mat(c, "c", torch.bfloat16, T * k, N)[2]
     ids_p, E = None, 0
     if topk_ids is not None:
@@ -353,11 +362,11 @@ def moe_wgrad_mxfp8(xq, xs, grad, routing, num_tokens, top_k, num_experts, out=N
     [T, K], xs: uint8 E8M0 [T, K / 32] (moe_quantize_mxfp8); grad, routing and
     out as for moe_wgrad."""
     T, k, E = int(num_tokens), int(top_k), int(num_experts)
-    K = _mat(xq, "xq", torch.uint8)[1]
-    N = _mat(grad, "grad", torch.bfloat16)[1]
-    xld = _mat(xq, "xq", torch.uint8, T, K)[2]
+    rows, K, xld = _mat(xq, "xq", torch.uint8)
+    slots, N, gld = _mat(grad, "grad", torch.bfloat16)
+    if rows < T or slots < T * k:
+        raise ValueError(f"xq must hold {T} rows and grad {T * k}, got {rows} and {slots}")
     sld = _mat(xs, "xs", torch.uint8, T, K // 32)[2]
-    gld = _mat(grad, "grad", torch.bfloat16, T * k, N)[2]
     sorted_ids, expert_ids, post_pad = routing
     for t, name in zip(routing, ("sorted_token_ids", "expert_ids", "num_tokens_post_pad")):
         _need(t, name, torch.int32, 1)

@@ -693,3 +693,43 @@ def test_training_step_captured_and_replayed():
         torch.cuda.synchronize()
         for n in ref:
             assert torch.equal(out[n], ref[n]) and torch.equal(eager[n], ref[n]), (i, n)
+
+
+@pytest.mark.parametrize("T", [1, 7])
+def test_router_feeds_the_decode_layer(T):
+    """A decode step from logits, captured: new logits at every replay."""
+    moe = _moe()
+    E, k, K, N = 16, 3, 64, 96
+    g = synth.gen(41, "decode")
+    x = torch.randn((T, K), generator=g).to(torch.bfloat16).cuda()
+    w = (torch.randn((E, N, K), generator=g) / 8).to(torch.bfloat16).cuda()
+    mask = torch.ones(T, dtype=torch.bool, device="cuda")
+    mask[T // 2] = T == 1              # one padded row, but for the single token
+    z = torch.empty((T, E), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        ids, tw = moe.moe_route(z, k, renormalize=False, mask=mask)
+        return ids, tw, moe.moe_decode_layer(x, ids, tw, w, "bf16", epilogue="relu2")
+
+    def unfused(ids, tw):
+        routing = moe.moe_align(ids, E, moe.moe_gemm_block_m("bf16", T))
+        c = moe.moe_grouped_gemm(x, w, "bf16", routing, T, k, E, k, epilogue="relu2")
+        return moe.moe_combine_routed(c, tw, ids, E)
+
+    z.copy_(logits(T, E, 1, "bf16"))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = step()
+    for i in range(4):
+        z.copy_(logits(T, E, 50 + i, "bf16"))
+        ids, tw, y = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(ids.cpu().numpy(), otrain.route(f64(z), k, "softmax", False, 1.0, mask.cpu().numpy())[0])
+        assert torch.equal(out[0], ids) and torch.equal(out[1], tw) and torch.equal(out[2], y)
+        assert torch.equal(y, unfused(ids, tw)) and (y[~mask] == 0).all() and (y[mask] != 0).any()
