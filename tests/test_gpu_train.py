@@ -695,6 +695,54 @@ def test_training_step_captured_and_replayed():
             assert torch.equal(out[n], ref[n]) and torch.equal(eager[n], ref[n]), (i, n)
 
 
+def _far_rows(rows, width, dtype):
+    """A [rows, width] view whose rows lie 2^32 + 64 bytes apart."""
+    es = torch.empty((), dtype=dtype).element_size()
+    ld = ((1 << 32) + 64) // es
+    return torch.empty((rows - 1) * ld + width, dtype=dtype, device="cuda").as_strided((rows, width), (ld, 1))
+
+
+def test_rows_more_than_32_bits_apart():
+    moe = _moe()
+    g = synth.gen(43, "far")
+    R, k, E, N = 4, 2, 32, 128
+    pre = torch.randn((R, N), generator=g).to(torch.bfloat16).cuda()
+    dh = torch.randn((R, N // 2), generator=g).to(torch.bfloat16).cuda()
+    z = logits(R, E, 44)
+    c = torch.randn((R, N), generator=g).to(torch.bfloat16).cuda()
+    dy = torch.randn((R // k, N), generator=g).to(torch.bfloat16).cuda()
+
+    def far(t):
+        return _far_rows(*t.shape, t.dtype).copy_(t)
+
+    def like(t):
+        return _far_rows(*t.shape, t.dtype)
+
+    h, q, s = moe.moe_act_mxfp8(pre, "swiglu")
+    got = moe.moe_act_mxfp8(far(pre), "swiglu", out=(like(h), like(q), like(s)))
+    assert all(torch.equal(a, b) for a, b in zip(got, (h, q, s)))
+    ref = moe.moe_act_mxfp8_backward(q, s, dh, "swiglu")
+    got = moe.moe_act_mxfp8_backward(got[1], got[2], far(dh), "swiglu", out=tuple(like(t) for t in ref))
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    del got
+    ids, w = moe.moe_route(z, k)
+    zf = far(z)
+    got = moe.moe_route(zf, k)
+    assert torch.equal(got[0], ids) and torch.equal(got[1], w)
+    ref = moe.moe_route_backward(z, ids, w)
+    assert torch.equal(moe.moe_route_backward(zf, ids, w, out=like(ref)), ref)
+    del zf
+    ids, w = ids[:R // k].contiguous(), w[:R // k].contiguous()
+    cf, dyf = far(c), far(dy)
+    ref = moe.moe_combine_routed(c, w, ids, E)
+    assert torch.equal(moe.moe_combine_routed(cf, w, ids, E, out=like(ref)), ref)
+    dc, dw = moe.moe_combine_backward(dy, c, w, ids, E)
+    got = moe.moe_combine_backward(dyf, cf, w, ids, E, out=(like(dc), torch.empty_like(dw)))
+    assert torch.equal(got[0], dc) and torch.equal(got[1], dw)
+    # and ld larger than a row alone says nothing of one row
+    assert torch.equal(moe.moe_route(_far_rows(1, E, torch.float32).copy_(z[:1]), k)[0], moe.moe_route(z[:1], k)[0])
+
+
 @pytest.mark.parametrize("T", [1, 7])
 def test_router_feeds_the_decode_layer(T):
     """A decode step from logits, captured: new logits at every replay."""
