@@ -519,6 +519,9 @@ static uint32_t rt_grid(int64_t T, int rows, int most = kRtMaxGrid) {
   const int64_t want = (T + rows - 1) / rows;
   return (uint32_t)(want < most ? want : most);
 }
+// Workgroups that write a partial row of the statistics: without tokens one
+// still does, so that the statistics of nothing are written.
+static uint32_t rt_partials(uint32_t grid) { return grid > 0 ? grid : 1; }
 
 // Forward pass above 128 experts: 32 logits a lane instead of 16 sorts more
 // in a lane and merges less between lanes, a quarter fewer instructions, but
@@ -530,9 +533,9 @@ static bool rt_deep(int64_t T, int E) { return E > 128 && T >= (int64_t)kRtMaxGr
 
 // Workspace for either forward kernel: the finishing kernel's 64 partial
 // products (8 bytes each) and ticket, the partial probability sums and
-// counts [grid][E], z sums and tokens [grid].
+// counts [rows][E], z sums and tokens [rows].
 int64_t route_workspace_bytes(int64_t T, int32_t E) {
-  return 64 * 8 + 8 + (int64_t)rt_grid(T, kRtWaves) * ((int64_t)E + 1) * 8;
+  return 64 * 8 + 8 + (int64_t)rt_partials(rt_grid(T, kRtWaves)) * ((int64_t)E + 1) * 8;
 }
 
 // Backward pass of 65 to 512 experts: with 8 logits a lane a wave has half the
@@ -601,10 +604,11 @@ static void rt_layout_deep(int E, bool bf16, F&& f) {
 hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t stream) {
   const bool wide = p.k > kRtListMax;
   const bool deep = !wide && rt_deep(p.T, p.E);
-  const uint32_t grid = wide   ? rt_grid(p.T, kRtWaves)
-                        : deep ? rt_grid(p.T, rt_rows_deep(p.E), kRtMaxGrid / 2)  // (registers: half the waves)
-                               : rt_grid(p.T, rt_rows(p.E));
+  uint32_t grid = wide   ? rt_grid(p.T, kRtWaves)
+                  : deep ? rt_grid(p.T, rt_rows_deep(p.E), kRtMaxGrid / 2)  // (registers: half the waves)
+                         : rt_grid(p.T, rt_rows(p.E));
   if (p.stats) {
+    grid = rt_partials(grid);
     p.part_b = static_cast<double*>(workspace);
     p.ticket = reinterpret_cast<int32_t*>(p.part_b + 64);
     p.part_p = reinterpret_cast<float*>(p.ticket + 2);
@@ -612,11 +616,9 @@ hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t s
     p.part_z = reinterpret_cast<float*>(p.part_c + (int64_t)grid * p.E);
     p.part_n = reinterpret_cast<int32_t*>(p.part_z + grid);
   }
-  // (no tokens: one workgroup without a row still writes the empty statistics)
-  const uint32_t blocks = grid > 0 ? grid : (p.stats ? 1 : 0);
-  if (blocks == 0) return hipSuccess;
+  if (grid == 0) return hipSuccess;
   auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kRtThreads), 0, stream, p);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kRtThreads), 0, stream, p);
   };
   auto by_score = [&](auto with) {
     if (p.sigmoid)
@@ -662,7 +664,7 @@ hipError_t launch_route(RouteParams p, bool bf16, void* workspace, hipStream_t s
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || !p.stats) return err;
   hipLaunchKernelGGL(route_finish_kernel, dim3((p.E + kRtFinExperts - 1) / kRtFinExperts), dim3(kRtFinThreads), 0,
-                     stream, p, (int)blocks);
+                     stream, p, (int)grid);
   return hipGetLastError();
 }
 

@@ -781,3 +781,18 @@ def test_router_feeds_the_decode_layer(T):
         assert np.array_equal(ids.cpu().numpy(), otrain.route(f64(z), k, "softmax", False, 1.0, mask.cpu().numpy())[0])
         assert torch.equal(out[0], ids) and torch.equal(out[1], tw) and torch.equal(out[2], y)
         assert torch.equal(y, unfused(ids, tw)) and (y[~mask] == 0).all() and (y[mask] != 0).any()
+
+
+@pytest.mark.parametrize("T", [0, 1, 3, 65, 5000])
+@pytest.mark.parametrize("E,k", [(1, 1), (40, 3), (256, 8), (1024, 5), (1024, 40)])
+def test_route_stays_inside_its_workspace(T, E, k):
+    """A workspace of exactly the stated size, and outputs of their own, inside a guarded buffer."""
+    moe = _moe()
+    need = moe.moe_route_workspace_bytes(T, E)
+    size, guard = -(-need // 8) * 8, 16384
+    buf = torch.full((guard + size + guard,), 0xAB, dtype=torch.uint8, device="cuda")
+    z = logits(T, E, T + E)
+    got = check_route(z, k, workspace=buf[guard:guard + need])
+    assert (buf[:guard] == 0xAB).all() and (buf[guard + need:] == 0xAB).all()
+    if T == 0:
+        assert all((t == 0).all() for t in got[2:])

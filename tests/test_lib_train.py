@@ -266,3 +266,10 @@ def test_binding_rejects_before_the_library():
         moe.moe_act_mxfp8_backward(u8, u8[:, :2], x[:, :32], "swiglu")
     with pytest.raises(ValueError):
         moe.moe_wgrad_mxfp8(u8, u8[:, :2], x, (ids[0], ids[0], ids[0]), 4, 1, 4)
+
+
+def test_route_workspace_of_no_tokens_holds_a_row():
+    # without tokens one workgroup still writes its (empty) partial row
+    for E in (1, 8, 40, 127, 256, 1024):
+        assert moe.moe_route_workspace_bytes(0, E) == moe.moe_route_workspace_bytes(1, E)
+        assert moe.moe_route_workspace_bytes(0, E) >= 520 + 8 * (E + 1)
