@@ -6,6 +6,9 @@
  * over MXFP8 rows. The conventions of moe.h hold for every entry point here
  * (caller-owned device memory, host validation before any launch, nothing
  * allocated or synchronized, MOE_* status codes, slot s = t * top_k + j).
+ * Ranges "overlap" when they share a byte: matrices may be columns of one
+ * buffer, and an array may lie in a gap between rows. Only matrices whose row
+ * strides differ in bytes must lie apart, from their first byte to their last.
  *
  * One step of a layer, forward:
  *   moe_route -> moe_align -> moe_grouped_gemm (no epilogue) -> moe_act_mxfp8

@@ -796,3 +796,61 @@ def test_route_stays_inside_its_workspace(T, E, k):
     assert (buf[:guard] == 0xAB).all() and (buf[guard + need:] == 0xAB).all()
     if T == 0:
         assert all((t == 0).all() for t in got[2:])
+
+
+@pytest.mark.parametrize("activation", ["swiglu", "relu2"])
+def test_act_in_columns_of_one_buffer(activation):
+    """Input and outputs interleaved row by row, no byte shared."""
+    moe, R, N = _moe(), 37, 192
+    H = N // 2 if activation == "swiglu" else N
+    g = synth.gen(51, "columns")
+    pre = torch.randn((R, N), generator=g).to(torch.bfloat16).cuda()
+    dh = torch.randn((R, H), generator=g).to(torch.bfloat16).cuda()
+    ref = moe.moe_act_mxfp8(pre, activation)
+    want = moe.moe_act_mxfp8_backward(ref[1], ref[2], dh, activation)
+
+    def columns(*widths):
+        """uint8 columns of these widths, each starting on 16 bytes, and the buffer."""
+        at, cuts = 0, []
+        for w in widths:
+            cuts.append((at, at + w))
+            at += -(-w // 16) * 16
+        buf = torch.full((R, at + 16), 0xA5, dtype=torch.uint8, device="cuda")
+        return [buf[:, a:b] for a, b in cuts], buf, cuts
+
+    (p, h, q, s), buf, cuts = columns(2 * N, 2 * H, N, N // 32)
+    p.view(torch.bfloat16).copy_(pre)
+    got = moe.moe_act_mxfp8(p.view(torch.bfloat16), activation, out=(h.view(torch.bfloat16), q, s))
+    assert all(torch.equal(a, b) for a, b in zip(got, ref)) and torch.equal(p.view(torch.bfloat16), pre)
+    for a, b in cuts:
+        buf[:, a:b] = 0xA5
+    assert (buf == 0xA5).all()
+    (q, s, d, dp, h), buf, cuts = columns(N, N // 32, 2 * H, 2 * N, 2 * H)
+    q.copy_(ref[1]), s.copy_(ref[2]), d.view(torch.bfloat16).copy_(dh)
+    got = moe.moe_act_mxfp8_backward(q, s, d.view(torch.bfloat16), activation,
+                                     out=(dp.view(torch.bfloat16), h.view(torch.bfloat16)))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(q, ref[1]) and torch.equal(s, ref[2]) and torch.equal(d.view(torch.bfloat16), dh)
+    for a, b in cuts:
+        buf[:, a:b] = 0xA5
+    assert (buf == 0xA5).all()
+
+
+def test_gradients_beside_their_inputs():
+    """dlogits beside logits, dC beside C: columns of one buffer."""
+    moe = _moe()
+    for dtype, E in (("fp32", 70), ("bf16", 70), ("fp32", 256)):
+        both = torch.cat([logits(50, E, 52, dtype)] * 2, 1)
+        z, keep = both[:, :E], both[:, :E].clone()
+        fwd = check_route(z, 6)
+        check_route_backward(z, 6, fwd, out=both[:, E:])
+        check_route_backward(both[:, :E].contiguous(), 6, fwd)
+        assert torch.equal(z, keep)
+    T, k, N = 9, 3, 136
+    dy, c, w, ids = _combine_case(T, k, N, 5, 53)
+    both = torch.cat([c, c], 1)
+    dw = torch.empty((T, k), device="cuda")
+    ref = moe.moe_combine_backward(dy, c, w, ids, 5)
+    moe.moe_combine_backward(dy, both[:, :N], w, ids, 5, out=(both[:, N:], dw))
+    assert torch.equal(both[:, N:], ref[0]) and torch.equal(dw, ref[1])
+    assert torch.equal(both[:, :N].contiguous().view(torch.int16), c.view(torch.int16))

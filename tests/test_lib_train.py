@@ -273,3 +273,58 @@ def test_route_workspace_of_no_tokens_holds_a_row():
     for E in (1, 8, 40, 127, 256, 1024):
         assert moe.moe_route_workspace_bytes(0, E) == moe.moe_route_workspace_bytes(1, E)
         assert moe.moe_route_workspace_bytes(0, E) >= 520 + 8 * (E + 1)
+
+
+def _refused(status):
+    return status in (INVALID, UNSUPPORTED)
+
+
+def _swapped(call, a, b, **kw):
+    """Whether the call is refused with the two pointers as given and exchanged (alike)."""
+    first, second = _refused(call(**kw)), _refused(call(**{**kw, a: kw[b], b: kw[a]}))
+    assert first == second
+    return first
+
+
+def test_rows_that_interleave_without_sharing_a_byte_are_accepted(no_device):
+    far, base = 1 << 40, 1 << 33
+    # codes and scales side by side in rows of 144 bytes, h beside pre, all in one buffer
+    assert not _refused(_act(q=base, qld=144, s=base + 128, sld=144))
+    assert not _refused(_act(pre=base, pld=256, h=base + 256, hld=256, q=far, s=2 * far))
+    assert _refused(_act(pre=base, pld=256, h=base + 240, hld=256, q=far, s=2 * far))    # 16 bytes of pre's row
+    assert _refused(_act(pre=base, pld=256, h=base + 400, hld=256, q=far, s=2 * far))    # the next row of pre
+    # rows of 528 bytes: pre [0, 256), h [256, 384), codes [384, 512), scales [512, 516)
+    row = dict(pld=264, hld=264, qld=528, sld=528)
+    assert not _refused(_act(pre=base, h=base + 256, q=base + 384, s=base + 512, **row))
+    assert not _refused(_act(pre=base, h=base + 256, q=base + 384, s=base + 524, **row))
+    assert _refused(_act(pre=base, h=base + 256, q=base + 384, s=base + 511, **row))
+    assert _refused(_act(pre=base, h=base + 256, q=base + 384, s=base + 525, **row))     # over pre's next row
+    assert _refused(_act(pre=base + 528 * 4, h=base + 256, q=base + 384, s=base + 525, **row))   # its first row
+    assert not _refused(_act(pre=base + 528 * 5, h=base + 256, q=base + 384, s=base + 525, **row))
+    # dpre beside h; one row after the other matrix's last
+    for kw in (dict(dp=base, dpld=192, h=base + 256, hld=192), dict(dp=base, dpld=192, h=base + 3 * 384 + 256, hld=64)):
+        assert not _refused(_act_bwd(q=far, s=2 * far, dh=3 * far, **kw))
+    assert _refused(_act_bwd(q=far, s=2 * far, dh=3 * far, dp=base, dpld=192, h=base + 3 * 384 + 240, hld=64))
+    # dlogits beside logits, the other way round too
+    assert not _swapped(_route_bwd, "z", "out", z=base, ld=16, out=base + 32, old=16)
+    assert _swapped(_route_bwd, "z", "out", z=base, ld=16, out=base + 28, old=16)
+    assert _swapped(_route_bwd, "z", "out", z=base, ld=15, out=base + 32, old=15)
+    # a block that lies in one gap of the rows, and one that reaches the next row
+    assert not _refused(_combine_bwd(dc=base, dcld=128, dw=base + 128, dy=far, c=2 * far, w=3 * far, ids=4 * far))
+    assert not _refused(_combine_bwd(dc=base, dcld=128, dw=base + 224, dy=far, c=2 * far, w=3 * far, ids=4 * far))
+    assert _refused(_combine_bwd(dc=base, dcld=128, dw=base + 228, dy=far, c=2 * far, w=3 * far, ids=4 * far))
+    assert _refused(_combine_bwd(dc=base, dcld=128, dw=base - 28, dy=far, c=2 * far, w=3 * far, ids=4 * far))
+    # rows of unequal strides have to lie apart
+    assert _refused(_combine_bwd(dc=base, dcld=128, c=base + 128, cld=256, dy=far, dw=2 * far, w=3 * far, ids=4 * far))
+
+
+def test_overlap_rule_is_that_of_the_bytes(no_device):
+    """The dlogits / logits check against the set of bytes, at every offset around each other."""
+    T, E, base = 3, 2, 1 << 33
+    for ld in (2, 3, 5):
+        rows = {base + 4 * (t * ld + e) for t in range(T) for e in range(E)}
+        for off in range(-4 * ld, 4 * ld + 1):
+            mine = {base + 4 * (off + t * ld + e) for t in range(T) for e in range(E)}
+            st = _route_bwd(z=base, ld=ld, T=T, E=E, k=1, out=base + 4 * off, old=ld, ids=1 << 40, dw=1 << 41,
+                            counts=1 << 42, n=1 << 43, dl=1 << 44)
+            assert _refused(st) == bool(rows & mine), (ld, off)
