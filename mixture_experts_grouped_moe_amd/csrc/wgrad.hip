@@ -68,6 +68,7 @@ constexpr int kWgThreads = kWgWaves * 64;
 constexpr int kWgGLoads = kWgGUnitB / 1024 / kWgWaves;  // DMA instructions per wave per unit: 2 grad
 constexpr int kWgXLoads = kWgXUnitB / 1024 / kWgWaves;  //   + 2 x (2 rows each)
 constexpr int kWgStores = 8 * 4;             // 16-byte stores per lane per tile
+constexpr int kWgWaitLds = 0xC07F;           // s_waitcnt lgkmcnt(0), no wait for vector memory
 constexpr int kWgPerCU = 1;                  // resident workgroups per CU
 static_assert(kWgGLoads == 2 && kWgXLoads == 2, "each wave loads the same 4 slot rows of both parts");
 
@@ -91,8 +92,6 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
       (void*)p.grad, 0, wg_span(p.S, p.grad_ld, p.N, 2), 0x00020000);
   const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
       (void*)p.x, 0, wg_span(p.S / p.top_k, p.x_ld, p.K, 2), 0x00020000);
-  const __amdgpu_buffer_rsrc_t sorted_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)p.sorted, 0, (int)(uint32_t)((int64_t)p.max_blocks * kWgBM * 4), 0x00020000);
   const uint32_t lds_base = (uint32_t)(uintptr_t)(wg_lds_u8_t*)&lds[0][0];
   const uint32_t g_row = (uint32_t)(p.grad_ld * 2), x_row = (uint32_t)(p.x_ld * 2);
 
@@ -131,9 +130,10 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
     a = wg_i32x4_t{0, 0, 0, 0};
     b = a;
     if (ld_live) {
-      const uint32_t off = (uint32_t)((ld.b0 * kWgBM + ld_u * kWgUM + wave * 4) * 4);
-      a = wg_scalar_ids4(sorted_rsrc, off);
-      b = wg_scalar_ids4(sorted_rsrc, off + kWgUM * 4);
+      const wg_const<int32_t>* at =
+          (const wg_const<int32_t>*)p.sorted + (int64_t)ld.b0 * kWgBM + ld_u * kWgUM + wave * 4;
+      a = wg_scalar_ids4(at);
+      b = wg_scalar_ids4(at + kWgUM);
     }
   };
   ld_skip_empty();
@@ -173,7 +173,6 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
     if (ld_live) {
       ld_u += 2;
       ld_skip_empty();
-      ld_ids_pair(ids, ids_b);  // complete by the next wait
     }
   };
 
@@ -181,7 +180,7 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
   // columns k0 + wk*128 .. + 127
   const int wn = wave / 2, wk = wave % 2;
   f32x16_t acc[2][4];  // [n sub-tile][k sub-tile]
-  auto contract = [&](int stage) {
+  auto contract = [&](int stage, bool next_ids) {
     const wg_lds_u8_t* gt = (const wg_lds_u8_t*)&lds[stage][0];
     const wg_lds_u8_t* xt = gt + kWgGUnitB;
     // every operand of the unit first (their LDS latency overlaps), then the MFMAs
@@ -195,12 +194,22 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
       for (int j = 0; j < 4; ++j) bfr[ks][j] = wg_operand<kWgXRowB>(xt, wk * 128 + j * 32, ks * 16, lane);
     }
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    for (int ks = 0; ks < KS; ++ks) {
+      if (ks == KS - 1 && next_ids) {
+        // the next pair's ids here: the last LDS results are awaited first, since
+        // scalar loads return out of order and a wait for LDS with one in flight
+        // waits for all, and the products that follow cover the load
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(kWgWaitLds);
+        ld_ids_pair(ids, ids_b);
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[ks][i], bfr[ks][j], acc[i][j], 0, 0, 0);
+    }
   };
 
   // ---- computation, a pair of units (one routing block) per barrier:
@@ -210,6 +219,7 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
   //      guarantees all waves finished the previous pair, whose two stages
   //      the loads issued next overwrite.
   issue_pair(0);
+  ld_ids_pair(ids, ids_b);
   int st = 0;  // first stage of the next pair computed
   bool stored = false;
   for (int it = 0; tile_index(it) < total; ++it) {
@@ -229,8 +239,8 @@ __global__ __launch_bounds__(kWgThreads, kWgPerCU) void wgrad_kernel(WgradParams
         wg_wait_barrier<0>(ids, ids_b);
       }
       issue_pair(st ^ 2);  // the pair computed last, now free
-      contract(st);
-      contract(st + 1);
+      contract(st, false);
+      contract(st + 1, true);
       st ^= 2;
     }
     // store the tile through LDS: the first stage of the pair computed last

@@ -65,8 +65,6 @@ __device__ __forceinline__ void wg_dma_byte(__amdgpu_buffer_rsrc_t rsrc, uint32_
 
 template <class T>
 using mx_lds = __attribute__((address_space(3))) T;
-template <class T>
-using mx_const = __attribute__((address_space(4))) T;
 
 // Wait until at most N of this wave's vector-memory operations are in flight
 // and its LDS operations are done, then barrier; without the barrier.
@@ -148,9 +146,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void wgrad_mxfp8_kernel(WgradParams 
     e = wg_i32x4_t{0, 0, 0, 0};
     o = e;
     if (ld_live) {
-      const mx_const<int32_t>* at = (const mx_const<int32_t>*)p.sorted + (int64_t)ld.b0 * kWgBM + ld_u * kWgUM + wave * 4;
-      e = *(const mx_const<wg_i32x4_t>*)at;
-      o = *(const mx_const<wg_i32x4_t>*)(at + kWgUM);
+      const wg_const<int32_t>* at = (const wg_const<int32_t>*)p.sorted + (int64_t)ld.b0 * kWgBM + ld_u * kWgUM + wave * 4;
+      e = wg_scalar_ids4(at);
+      o = wg_scalar_ids4(at + kWgUM);
     }
   };
   auto ld_next = [&]() {

@@ -39,19 +39,19 @@ __device__ __forceinline__ void wg_dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t v
 
 typedef __attribute__((__vector_size__(4 * sizeof(int)))) int wg_i32x4_t;
 
-// 4 consecutive int32 at byte `off` of buffer `rsrc` through the scalar
-// cache (a read). Asynchronous: the result must not be used before an
-// lgkmcnt(0) wait that lists it (wg_wait_barrier).
-__device__ __forceinline__ wg_i32x4_t wg_scalar_ids4(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
-  wg_i32x4_t v;
-  asm volatile("s_buffer_load_dwordx4 %0, %1, %2"
-               : "=s"(v) : "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(off)));
-  return v;
+template <class T>
+using wg_const = __attribute__((address_space(4))) T;
+
+// 4 consecutive slot ids through the scalar cache (a read). The load is the
+// compiler's, which waits for it where the ids are used: one issued by inline
+// asm may have its registers copied or reused before it lands.
+__device__ __forceinline__ wg_i32x4_t wg_scalar_ids4(const wg_const<int32_t>* at) {
+  return *(const wg_const<wg_i32x4_t>*)at;
 }
 
 // Wait until at most N of this wave's vector-memory operations are in
 // flight and every LDS and scalar-memory operation is done, then barrier;
-// `a` and `b` (prefetched scalar loads) are final from here on.
+// `a` and `b` (ids loaded ahead) are loaded before it.
 template <int N>
 __device__ __forceinline__ void wg_wait_barrier(wg_i32x4_t& a, wg_i32x4_t& b) {
   static_assert(N >= 0 && N < 64, "vmcnt range");
