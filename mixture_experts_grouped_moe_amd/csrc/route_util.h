@@ -251,13 +251,13 @@ __device__ __forceinline__ void rt_load_row(const T* row, int E, int l, bool on,
 // The unnormalised probability of logit z in a row whose largest is m (at
 // most 1, and not below about 1/2 for the largest itself):
 //   softmax: exp(z - m)
-//   sigmoid: sigmoid(z), relative to exp(m) in a row whose logits all lie
-//     far below 0, where sigmoid(z) = exp(z) / (1 + exp(z)) would underflow
+//   sigmoid: sigmoid(z) = exp(z) / (1 + exp(z)), relative to exp(m) where m is
+//     below 0, so that small shares underflow with the share, not with the
+//     score (the exponential's results below 2^-126 are 0)
 // rt_base(m) is the part of m that the row's scores are relative to.
 template <bool SIGMOID>
 __device__ __forceinline__ float rt_base(float m) {
-  if (SIGMOID) return m < -60.0f && m != rt_neg_inf() ? m : 0.0f;
-  return m == rt_neg_inf() ? 0.0f : m;
+  return m == rt_neg_inf() ? 0.0f : SIGMOID ? fminf(m, 0.0f) : m;
 }
 template <bool SIGMOID>
 __device__ __forceinline__ float rt_score(float z, float base) {

@@ -854,3 +854,21 @@ def test_gradients_beside_their_inputs():
     moe.moe_combine_backward(dy, both[:, :N], w, ids, 5, out=(both[:, N:], dw))
     assert torch.equal(both[:, N:], ref[0]) and torch.equal(dw, ref[1])
     assert torch.equal(both[:, :N].contiguous().view(torch.int16), c.view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("top", [-20.0, -59.0, -61.0])
+@pytest.mark.parametrize("E,k", [(70, 6), (300, 20)])
+def test_route_sigmoid_scores_far_below_one(dtype, top, E, k):
+    """Logits spread over 70 below a largest one that lies far below 0: their shares reach down to
+    e^-70, the scores themselves past the smallest float."""
+    g = synth.gen(61, "low")
+    z = top - 70 * torch.rand((40, E), generator=g)
+    z[:, 3] = top
+    z[::2, 5] = top - 29.5
+    z[1, k - 1:] = float("-inf")
+    z = (z.to(torch.bfloat16) if dtype == "bf16" else z).cuda()
+    for renorm in (True, False):
+        fwd = check_route(z, k, "sigmoid", renorm)
+        check_route_backward(z, k, fwd, "sigmoid", renorm)
+    check_route_backward(z, k, check_route(z, k, "softmax", False), "softmax", False)
