@@ -58,8 +58,10 @@ typedef enum {
  *   losses[1]   = (1/n) sum_t (log sum_e exp z[t][e])^2 for softmax scores, 0
  *                 for sigmoid scores;  both 0 when n = 0.
  * A NaN logit, or +inf with softmax scores, makes its token's q NaN, which
- * reaches prob_sum, the losses and its weights (renormalized weights of a
- * token with NaN logits are those of its other experts).
+ * reaches prob_sum, the losses and, for softmax scores without
+ * renormalization, all its weights. The other weights depend on the chosen
+ * experts' logits alone, which are never NaN; a chosen +inf makes renormalized
+ * softmax weights NaN.
  *
  * logits (device) MOE_FP32 or MOE_BF16 [T][E], row stride logits_ld elements;
  * token_mask (device) uint8 [T] or NULL; topk_ids (device) int32 [T][top_k];

@@ -872,3 +872,30 @@ def test_route_sigmoid_scores_far_below_one(dtype, top, E, k):
         fwd = check_route(z, k, "sigmoid", renorm)
         check_route_backward(z, k, fwd, "sigmoid", renorm)
     check_route_backward(z, k, check_route(z, k, "softmax", False), "softmax", False)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("k", [5, 20])
+def test_route_weights_beside_non_finite_logits(dtype, k):
+    """Which weights a NaN or an infinite logit reaches, as moe_train.h states it."""
+    moe = _moe()
+    clean = logits(6, 50, 62, dtype)
+    z = clean.clone()
+    z[2, 3] = float("nan")
+    z[4, 7] = float("inf")
+    rest = clean.clone()
+    rest[2, 3] = float("-inf")                         # the row without its NaN expert
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            ids, w = moe.moe_route(z, k, score=score, renormalize=renorm)
+            want = moe.moe_route(rest, k, score=score, renormalize=renorm)
+            assert torch.equal(ids[:4], want[0][:4]) and int(ids[4, 0]) == 7
+            assert torch.equal(w[[0, 1, 3, 5]], want[1][[0, 1, 3, 5]])
+            if score == "softmax" and not renorm:
+                assert torch.isnan(w[2]).all()
+            else:
+                assert torch.equal(w[2], want[1][2])
+            if score == "softmax":
+                assert torch.isnan(w[4]).all()
+            else:
+                assert torch.isfinite(w[4]).all() and (renorm or w[4, 0] == 1.0)
