@@ -899,3 +899,32 @@ def test_route_weights_beside_non_finite_logits(dtype, k):
                 assert torch.isnan(w[4]).all()
             else:
                 assert torch.isfinite(w[4]).all() and (renorm or w[4, 0] == 1.0)
+
+
+def test_training_step_reads_nothing_that_it_did_not_write(monkeypatch):
+    """Every output, workspace and intermediate of the step starts as one repeated byte (0xFF: NaN in
+    bf16, fp32, E4M3 and E8M0); the results have the same bits whatever it is."""
+    moe, d = _moe(), _step_case()
+    plain, filled = {n: getattr(torch, n) for n in ("empty", "empty_strided")}, []
+    byte = [0]
+
+    def filling(name):
+        def make(*args, **kw):
+            t = plain[name](*args, **kw)
+            if t.is_cuda:
+                t.view(torch.uint8).fill_(byte[0])
+                filled.append(t.numel())
+            return t
+        return make
+
+    for name in plain:
+        monkeypatch.setattr(torch, name, filling(name))
+    runs = []
+    for byte[0] in (0xFF, 0x00, 0x47):
+        del filled[:]
+        runs.append({n: t.clone() for n, t in _step(moe, d).items()})
+        assert len(filled) > 20
+    for n, t in runs[0].items():
+        assert not t.is_floating_point() or torch.isfinite(t).all(), n
+        for r in runs[1:]:
+            assert torch.equal(r[n], t), n
