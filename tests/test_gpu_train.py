@@ -928,3 +928,36 @@ def test_training_step_reads_nothing_that_it_did_not_write(monkeypatch):
         assert not t.is_floating_point() or torch.isfinite(t).all(), n
         for r in runs[1:]:
             assert torch.equal(r[n], t), n
+
+
+def test_training_step_replayed_on_new_inputs():
+    """Captured once, replayed on other logits, activations, gradients, padding and loss weights:
+    every replay against an eager step on the same inputs."""
+    moe, d = _moe(), _step_case()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(moe, d)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = _step(moe, d)
+    seen = []
+    for i in range(5):
+        g = synth.gen(70 + i, "replay")
+        for name in ("x", "logits", "dy"):
+            d[name].copy_(torch.randn(d[name].shape, generator=g).to(d[name].dtype))
+        d["logits"][:, i] += 2.0                       # another favourite expert each time
+        d["mask"].copy_(torch.rand(len(d["mask"]), generator=g) < (0.0 if i == 3 else 0.8))   # once all padding
+        d["dlosses"].copy_(torch.rand(2, generator=g))
+        for t in out.values():
+            t.fill_(-3)
+        eager = {n: t.clone() for n, t in _step(moe, d).items()}
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, t in eager.items():
+            assert torch.equal(out[n], t), (i, n)
+        assert torch.isfinite(out["dw1"]).all() and (i != 3 or (out["dw1"] == 0).all())
+        seen.append(eager["losses"])
+    assert len({tuple(l.tolist()) for l in seen}) == 5
