@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kActThreads) void act_backward_kernel(ActParams p) 
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       h[j] = relu2_f32(g[j]);
-      g[j] = g[j] > 0.0f ? 2.0f * g[j] * dh[j] : 0.0f;
+      g[j] = g[j] > 0.0f ? 2.0f * (g[j] * dh[j]) : 0.0f;  // (2 g may overflow where the product does not)
     }
   }
   *reinterpret_cast<u32x4_t*>(dpre) = act_pack(g);

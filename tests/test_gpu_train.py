@@ -961,3 +961,48 @@ def test_training_step_replayed_on_new_inputs():
         assert torch.isfinite(out["dw1"]).all() and (i != 3 or (out["dw1"] == 0).all())
         seen.append(eager["losses"])
     assert len({tuple(l.tolist()) for l in seen}) == 5
+
+
+def _every_code():
+    """Row t: the 256 E4M3 codes under scale byte t, and their values (float64; NaN under byte 0xFF)."""
+    q = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
+    s = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 8)
+    v = oquant.mx_dequantize_e4m3(q.numpy(), s.numpy())
+    v[255] = np.nan
+    return q.cuda(), s.cuda(), v
+
+
+def _bf16(v):
+    with np.errstate(over="ignore"):
+        return torch.from_numpy(v).to(torch.bfloat16).double().numpy()
+
+
+@pytest.mark.parametrize("p", [0, 60, -60])
+def test_wgrad_mxfp8_decodes_every_code_under_every_scale(p):
+    """One slot an expert: dW is grad times the decoded row, exact (bf16's subnormals and the
+    infinities past its range with it)."""
+    moe, N = _moe(), 32
+    q, s, v = _every_code()
+    ids = torch.arange(256, dtype=torch.int32)[:, None].cuda()
+    grad = torch.full((256, N), 2.0 ** p).to(torch.bfloat16).cuda()
+    routing = moe.moe_align(ids, 256, moe.moe_wgrad_block_m())
+    dw = moe.moe_wgrad_mxfp8(q, s, grad, routing, 256, 1, 256)
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = (_bf16(v) * 2.0 ** p).astype(np.float32)
+    for n in (0, N - 1):
+        got = dw[:, n].cpu().numpy()
+        assert np.array_equal(got, want, equal_nan=True)
+
+
+@pytest.mark.parametrize("p", [0, 50, -50])
+def test_act_relu2_gradient_of_every_code_under_every_scale(p):
+    """Scales up to 2^119, the largest that a finite bf16 has: the gradient is finite wherever its value is."""
+    moe = _moe()
+    q, s, v = (t[:247] for t in _every_code())
+    dh = torch.full((247, 256), 2.0 ** p).to(torch.bfloat16).cuda()
+    d, h = moe.moe_act_mxfp8_backward(q, s, dh, "relu2")
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore", invalid="ignore"):
+        assert np.array_equal(f64(d), _bf16(np.where(v > 0, 2 * v * 2.0 ** p, 0.0)))     # (NaN codes give 0)
+        assert np.array_equal(f64(h), _bf16(np.where(v > 0, v * v, 0.0)))    # 8 significant bits: exact
