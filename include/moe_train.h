@@ -139,7 +139,8 @@ moe_status moe_combine_backward(const void* dy, int64_t dy_ld, const void* c, in
  * The expert activation with an 8-bit checkpoint of its input. For every row
  * r < rows of pre (the first GEMM's output, bf16, width n):
  *   h[r] = bf16( act(pre[r]) ), act MOE_EPILOGUE_SWIGLU (width n / 2) or
- *          MOE_EPILOGUE_RELU2 (width n), as in moe_grouped_gemm
+ *          MOE_EPILOGUE_RELU2 (width n), the formulas of moe_grouped_gemm's
+ *          epilogues (SwiGLU not bit for bit: that one divides)
  *   q[r], scales[r] = moe_quantize_mxfp8 of pre[r]
  * so a training step keeps n (1 + 1/32) bytes a row for the backward pass in
  * place of 2n for pre and more for h. Rows are independent; rows that no slot

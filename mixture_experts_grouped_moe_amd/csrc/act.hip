@@ -54,6 +54,8 @@ __device__ __forceinline__ void act_decode(const u32x2_t q, uint32_t byte, float
     f[4 * w + 3] = b[1];
   }
 }
+// (the hardware's exponential and reciprocal, 1 ulp each: far below the bf16
+// that h and dpre are rounded to)
 __device__ __forceinline__ float act_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 // floor(i / d) for i < 2^31 by a multiply-high (see wgrad.hip's launch).

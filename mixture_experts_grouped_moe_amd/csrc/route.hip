@@ -11,18 +11,24 @@
 // carry the expert's index below the logit (route_util.h), so ties need no
 // extra step and ordering a pair takes two instructions. Taking the maximum k
 // times over one row per wave cost 335 us on 65536 x 256 fp32 logits with
-// top 8 and statistics; this takes 26 us (23 and the finishing launch), where
-// the logits' bytes alone take 14 us at the rate of a large copy. What bounds
-// it is instructions: about 130 a row, two thirds of the kernel's time at one
-// per SIMD and 4 cycles. Loading a row ahead of its use changed nothing.
-// Wider top_k (up to 64): k rounds of a wave's maximum, one row per wave.
+// top 8 and statistics; this takes 30 us on logits that no cache holds (25 and
+// the finishing launch; 27 where the 256 MB cache holds them), where the
+// logits' bytes take 13 us at the rate of a large copy. Instructions, about
+// 130 a row, take half of the kernel's cycles at one per SIMD and 4 cycles;
+// the same logits in bf16, half the bytes, take 27 us. What the other half
+// waits for is not taken apart. Loading a row ahead of its use changed nothing.
+// Wider top_k (up to 64): k rounds of a wave's maximum, one row per wave. On
+// 65536 x 512 fp32 the merging kernel takes 53 us at top 16, this one 241 at
+// top 17, 423 at top 32 and 812 at top 64.
 //
 // Backward: the same layout. The probabilities are not kept by the forward
 // pass but recomputed from the logits, which the gradient would otherwise
 // replace by a read of the same size. The chosen experts' terms go through a
 // row of LDS that is zero otherwise, so adding them costs one scattered add
 // and one read however many there are. 65536 x 256 fp32, an eighth of the rows
-// padding: 27 us, 5.1 TB/s.
+// padding: 29 us (sigmoid 30.5) from logits and into gradients that no cache
+// holds, 4.7 TB/s; 27.5 (30) where the 256 MB cache holds some. In bf16 25 us:
+// bound by instructions.
 //
 // Statistics: each lane adds its rows' probabilities into registers, a
 // workgroup adds its lanes' and writes one partial row, and a second launch
@@ -71,8 +77,8 @@ __device__ __forceinline__ void rt_write_partial(const RouteParams& p, const flo
 }
 
 // Waves per SIMD that the registers leave room for: 32 logits a lane or lists
-// of 16 double keys take more than 128 (4096 x 256 fp32 top 16: 5.4 us, with
-// 10 registers in scratch memory at four waves 6.1).
+// of 16 double keys take more than 128 (4096 x 256 fp32 top 16: 6.4 us, with
+// registers in scratch memory at four waves 8.7).
 template <class T, int VPL, int L>
 constexpr int kRtOccupancy = VPL > 16 || sizeof(typename RtVec<T>::key::type) * L > 64 ? 2 : 4;
 
@@ -525,10 +531,10 @@ static uint32_t rt_partials(uint32_t grid) { return grid > 0 ? grid : 1; }
 
 // Forward pass above 128 experts: 32 logits a lane instead of 16 sorts more
 // in a lane and merges less between lanes, a quarter fewer instructions, but
-// has fewer waves. It pays from where 16 a lane fill their largest grid
-// (statistics included; fp32, 256 experts top 8: 65536 tokens 29.7 -> 26.6 us,
-// 16384 16.8 -> 14.6, 4096 10.6 -> 12.6; 1024 experts: 65536 tokens
-// 112 -> 87 us, 4096 20.0 -> 16.3, 512 11.3 -> 12.5).
+// has fewer waves. It pays from where 16 a lane fill their largest grid (both
+// kernels, statistics included, on logits that no cache holds; fp32 top 8, 256
+// experts: 65536 tokens 34 -> 31 us, 16384 17.6 -> 16.2, 4096 11.6 -> 13.9;
+// 1024 experts: 65536 tokens 130 -> 96 us, 4096 20.4 -> 17.7, 512 12.2 -> 13.3).
 static bool rt_deep(int64_t T, int E) { return E > 128 && T >= (int64_t)kRtMaxGrid * rt_rows(E); }
 
 // Workspace for either forward kernel: the finishing kernel's 64 partial
@@ -541,8 +547,8 @@ int64_t route_workspace_bytes(int64_t T, int32_t E) {
 // Backward pass of 65 to 512 experts: with 8 logits a lane a wave has half the
 // rows and half the instructions, which bound it while every wave takes its
 // rows once. It pays up to one workgroup per CU of the usual 256 (with the
-// losses: 4096 x 256 fp32 6.6 -> 5.3 us, bf16 8.9 -> 6.2; 8192 x 256 7.7
-// either way; 65536 x 512 49 -> 55).
+// losses: 4096 x 256 fp32 7.2 -> 5.7 us, bf16 9.3 -> 7.0; 8192 x 256 7.9 and
+// 8.1; 65536 x 512 52 -> 56).
 static bool rt_spread(int64_t T, int E) { return E > 64 && E <= 512 && T <= (int64_t)256 * rt_rows_spread(E); }
 
 template <int N>

@@ -8,6 +8,8 @@
 namespace moe {
 
 __device__ __forceinline__ float rt_neg_inf() { return -__builtin_huge_valf(); }
+// The hardware's one-instruction exponential and logarithm (base 2, 1 ulp); the
+// argument's rounding adds |x| 2^-24 of the result, as a - m itself has.
 __device__ __forceinline__ float rt_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }  // x <= 0
 __device__ __forceinline__ float rt_log(float x) { return __builtin_amdgcn_logf(x) * 0.69314718f; }  // log2 -> log
 

@@ -49,7 +49,10 @@
 //    slices stay in its L2.
 //  * Every expert's block range comes from one pass over expert_ids (sorted
 //    by expert, sentinels last) into an LDS table at the start; slot ids are
-//    read with scalar loads one unit ahead of their use and turned into row
+//    read with scalar loads between the products of the pair before their use
+//    (loads that the compiler tracks, placed where it waits for nothing else:
+//    as fast as inline asm, whose registers it may copy before they are
+//    loaded) and turned into row
 //    offsets on the scalar unit (the token row s / top_k by a multiply-high),
 //    so a load costs each lane only a select and an add. PAD slots and the
 //    look-ahead past the last tile read zeros through the buffer bounds;
