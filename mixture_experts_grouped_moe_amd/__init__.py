@@ -655,8 +655,10 @@ def moe_relu2_layer(x, topk_ids, topk_w, w1, w2, b1=None, b2=None, num_tokens=No
     return moe_combine(c2, topk_w, k, num_tokens=T, stream=stream)
 
 
-# the training entry points (moe_train.h) bind to the library loaded above
-from . import training  # noqa: E402
+# the training (moe_train.h) and block entry points (moe_block.h) bind to the
+# library loaded above
+from . import training, block  # noqa: E402
 from .training import *  # noqa: E402,F401,F403
+from .block import *  # noqa: E402,F401,F403
 
-__all__ += training.__all__
+__all__ += training.__all__ + block.__all__

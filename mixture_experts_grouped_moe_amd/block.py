@@ -1,0 +1,221 @@
+"""Python binding of libmoe's block entry points (include/moe_block.h): what
+stands around an expert layer.
+
+The same manner as the rest of the package. A block whose expert GEMMs read
+MXFP8 activations, with dropout of the layer's output:
+
+    y, r, q, s = moe_rmsnorm(x, weight, residual, p=p, rng=rng, quant="mxfp8")
+    ... y to the router, q and s to moe_grouped_gemm(a_scale=s), r the next block's residual ...
+
+    dx, dres, dweight = moe_rmsnorm_backward(dy, r, weight, dsum=dr, p=p, rng=rng)
+"""
+
+import ctypes
+
+import torch
+
+from . import _check, _need, lib, MOE_BF16, MOE_FP32
+from .training import _flat, _mat, _new, _on_stream, _same_device, _stream
+
+__all__ = [
+    "moe_dropout", "moe_rmsnorm", "moe_rmsnorm_backward", "moe_rmsnorm_backward_workspace_bytes",
+    "MOE_QUANT_NONE", "MOE_QUANT_MXFP8", "MOE_QUANT_PER_TOKEN",
+]
+
+MOE_QUANT_NONE, MOE_QUANT_MXFP8, MOE_QUANT_PER_TOKEN = 0, 1, 2
+_QUANTS = {None: MOE_QUANT_NONE, "none": MOE_QUANT_NONE, "mxfp8": MOE_QUANT_MXFP8, "per_token": MOE_QUANT_PER_TOKEN}
+_WIDE = {torch.float32: MOE_FP32, torch.bfloat16: MOE_BF16}
+
+_i64, _i32, _vp, _f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
+
+
+class MoeRmsnormArgs(ctypes.Structure):
+    """ctypes mirror of moe_rmsnorm_args (include/moe_block.h)."""
+    _fields_ = [
+        ("rows", _i64), ("n", _i64), ("x", _vp), ("x_ld", _i64), ("p", _f32), ("rng", _vp),
+        ("residual", _vp), ("residual_ld", _i64), ("residual_dtype", _i32), ("sum", _vp), ("sum_ld", _i64),
+        ("weight", _vp), ("weight_dtype", _i32), ("eps", _f32), ("y", _vp), ("y_ld", _i64),
+        ("quant", _i32), ("q", _vp), ("q_ld", _i64), ("scales", _vp), ("scales_ld", _i64),
+    ]
+
+
+class MoeRmsnormBackwardArgs(ctypes.Structure):
+    """ctypes mirror of moe_rmsnorm_backward_args (include/moe_block.h)."""
+    _fields_ = [
+        ("rows", _i64), ("n", _i64), ("dy", _vp), ("dy_ld", _i64), ("dsum", _vp), ("dsum_ld", _i64),
+        ("sum", _vp), ("sum_ld", _i64), ("sum_dtype", _i32), ("weight", _vp), ("weight_dtype", _i32), ("eps", _f32),
+        ("p", _f32), ("rng", _vp), ("dresidual", _vp), ("dresidual_ld", _i64), ("dx", _vp), ("dx_ld", _i64),
+        ("dweight", _vp), ("workspace", _vp), ("workspace_bytes", _i64),
+    ]
+
+
+def _bind():
+    sig = {
+        "moe_dropout": (_i32, [_vp, _i64, _i64, _i64, _f32, _vp, _vp, _i64, _vp]),
+        "moe_rmsnorm": (_i32, [ctypes.POINTER(MoeRmsnormArgs), _vp]),
+        "moe_rmsnorm_backward": (_i32, [ctypes.POINTER(MoeRmsnormBackwardArgs), _vp]),
+        "moe_rmsnorm_backward_workspace_bytes": (_i64, [_i64, _i64]),
+    }
+    for name, (res, args) in sig.items():
+        fn = getattr(lib, name)
+        fn.restype = res
+        fn.argtypes = args
+
+
+_bind()
+
+
+def _rng(rng):
+    """The address of a dropout's {seed, offset}; None without one."""
+    if rng is None:
+        return None
+    _flat(rng, "rng", torch.int64, (2,))
+    return rng.data_ptr()
+
+
+def _wide(t, name):
+    """The library's dtype of a matrix of the residual stream, or of the norm's weight."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _WIDE:
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+    return _WIDE[t.dtype]
+
+
+@_on_stream
+def moe_dropout(x, p, rng, out=None):
+    """x / (1 - p) where kept and 0 elsewhere, bf16 [T, n] (rows may be strided).
+
+    p in [0, 1], in steps of 2^-16; rng: int64 [2] on the device, {seed,
+    offset} of the counter-based generator. The mask is a function of rng and
+    of the element's place, so the gradient is the same call on the gradient.
+    `out` may be x."""
+    T, n, ld = _mat(x, "x", torch.bfloat16)
+    if out is None:
+        out, old = _new(x, T, n, torch.bfloat16), n
+    else:
+        old = _mat(out, "out", torch.bfloat16, T, n)[2]
+    rng_p = _rng(rng)
+    _same_device(x, rng, out)
+    _check(lib.moe_dropout(x.data_ptr(), ld, T, n, p, rng_p, out.data_ptr(), old, _stream(x)))
+    return out
+
+
+@_on_stream
+def moe_rmsnorm(x, weight, residual=None, eps=1e-6, p=0.0, rng=None, quant=None, keep_y=True, keep_sum=True, out=None):
+    """The root-mean-square norm of residual + drop(x), times weight.
+
+    x: bf16 [T, n]; weight: bf16 or fp32 [n]; residual: bf16 or fp32 [T, n];
+    p, rng: dropout of x as in moe_dropout; quant: "mxfp8" (n % 32 == 0; what
+    moe_grouped_gemm takes as MXFP8 activations) or "per_token" (what
+    moe_grouped_gemm_per_token takes).
+
+    Returns (y, sum, q, scales): y bf16 [T, n] (None with keep_y=False); sum =
+    residual + drop(x) in the residual's dtype (None with keep_sum=False, or
+    where it would be x); q uint8 E4M3 codes [T, n] with scales uint8 E8M0
+    [T, n / 32] or fp32 [T] (None without quant). `out` may give the four, None
+    for what is not wanted; its sum may be residual."""
+    T, n, xld = _mat(x, "x", torch.bfloat16)
+    kind, wd = _QUANTS[quant], _wide(weight, "weight")
+    _flat(weight, "weight", weight.dtype, (n,))
+    rd, rld, res_p = MOE_BF16, 0, None
+    if residual is not None:
+        rd = _wide(residual, "residual")
+        rld, res_p = _mat(residual, "residual", residual.dtype, T, n)[2], residual.data_ptr()
+        if residual.shape[0] != T:
+            raise ValueError(f"residual must be [{T}, {n}], got {list(residual.shape)}")
+    y = v = q = s = None
+    yld = vld = qld = sld = 0
+    if out is None:
+        if keep_y:
+            y, yld = _new(x, T, n, torch.bfloat16), n
+        if keep_sum and (residual is not None or p > 0):
+            v, vld = _new(x, T, n, torch.bfloat16 if residual is None else residual.dtype), n
+        if kind:
+            q, qld = _new(x, T, n, torch.uint8), n
+            if kind == MOE_QUANT_MXFP8:
+                s, sld = _new(x, T, n // 32, torch.uint8), n // 32
+            else:
+                s = torch.empty(T, dtype=torch.float32, device=x.device)
+    else:
+        y, v, q, s = out
+        if (q is None) != (kind == 0) or (s is None) != (kind == 0):
+            raise ValueError("out must give q and scales with a quant, and only then")
+        if y is not None:
+            yld = _mat(y, "y", torch.bfloat16, T, n)[2]
+        if v is not None:
+            if residual is None:
+                rd = _wide(v, "sum")
+            vld = _mat(v, "sum", v.dtype if residual is None else residual.dtype, T, n)[2]
+        if kind:
+            qld = _mat(q, "q", torch.uint8, T, n)[2]
+            if kind == MOE_QUANT_MXFP8:
+                sld = _mat(s, "scales", torch.uint8, T, n // 32)[2]
+            else:
+                _flat(s, "scales", torch.float32, (T,))
+    rng_p = _rng(rng)
+    _same_device(x, weight, residual, rng, y, v, q, s)
+    _check(lib.moe_rmsnorm(ctypes.byref(MoeRmsnormArgs(
+        T, n, x.data_ptr(), xld, p, rng_p, res_p, rld, rd, v.data_ptr() if v is not None else None, vld,
+        weight.data_ptr(), wd, eps, y.data_ptr() if y is not None else None, yld, kind,
+        q.data_ptr() if kind else None, qld, s.data_ptr() if kind else None, sld)), _stream(x)))
+    return y, v, q, s
+
+
+def moe_rmsnorm_backward_workspace_bytes(rows, n):
+    """Bytes of the workspace that moe_rmsnorm_backward takes for dweight."""
+    return int(lib.moe_rmsnorm_backward_workspace_bytes(int(rows), int(n)))
+
+
+@_on_stream
+def moe_rmsnorm_backward(dy, sum, weight, dsum=None, eps=1e-6, p=0.0, rng=None, keep_dweight=True, out=None,
+                         workspace=None):
+    """Gradient of moe_rmsnorm from the sum that it returned (x itself where it
+    returned none).
+
+    dy: bf16 [T, n], y's gradient; dsum: sum's gradient, in sum's dtype; weight,
+    eps, p, rng as in the forward pass. Returns (dx bf16, dresidual in sum's
+    dtype, dweight fp32 [n] or None); without dropout, and for a bf16 sum, dx
+    and dresidual are one tensor. `out` may give the three, None for what is
+    not wanted (its dresidual may be dsum); `workspace` a uint8 tensor of
+    moe_rmsnorm_backward_workspace_bytes (calls that may run at the same time
+    need one each)."""
+    T, n, gld = _mat(dy, "dy", torch.bfloat16)
+    sd, wd = _wide(sum, "sum"), _wide(weight, "weight")
+    vld = _mat(sum, "sum", sum.dtype, T, n)[2]
+    if sum.shape[0] != T:
+        raise ValueError(f"sum must be [{T}, {n}], got {list(sum.shape)}")
+    _flat(weight, "weight", weight.dtype, (n,))
+    dsld = _mat(dsum, "dsum", sum.dtype, T, n)[2] if dsum is not None else 0
+    dx = dres = dw = None
+    dxld = drld = 0
+    if out is None:
+        dx, dxld = _new(dy, T, n, torch.bfloat16), n
+        same = p == 0 and sd == MOE_BF16
+        if not same:
+            dres, drld = _new(dy, T, n, sum.dtype), n
+        if keep_dweight:
+            dw = torch.empty(n, dtype=torch.float32, device=dy.device)
+        result = dx, dx if same else dres, dw
+    else:
+        dx, dres, dw = result = tuple(out)
+        if dx is not None:
+            dxld = _mat(dx, "dx", torch.bfloat16, T, n)[2]
+        if dres is not None:
+            drld = _mat(dres, "dresidual", sum.dtype, T, n)[2]
+        if dw is not None:
+            _flat(dw, "dweight", torch.float32, (n,))
+    ws_p, ws_n = None, 0
+    if dw is not None:
+        if workspace is None:
+            workspace = torch.empty(max(moe_rmsnorm_backward_workspace_bytes(T, n), 0), dtype=torch.uint8,
+                                    device=dy.device)
+        else:
+            _need(workspace, "workspace", torch.uint8, 1)
+        ws_p, ws_n = workspace.data_ptr(), workspace.numel()
+    rng_p = _rng(rng)
+    _same_device(dy, sum, weight, dsum, rng, dx, dres, dw, workspace)
+    _check(lib.moe_rmsnorm_backward(ctypes.byref(MoeRmsnormBackwardArgs(
+        T, n, dy.data_ptr(), gld, dsum.data_ptr() if dsum is not None else None, dsld, sum.data_ptr(), vld, sd,
+        weight.data_ptr(), wd, eps, p, rng_p, dres.data_ptr() if dres is not None else None, drld,
+        dx.data_ptr() if dx is not None else None, dxld, dw.data_ptr() if dw is not None else None, ws_p, ws_n)),
+        _stream(dy)))
+    return result

@@ -119,6 +119,34 @@ struct ActParams {
   int32_t shift;
 };
 
+// The norm and its gradient (norm.hip). Strides in elements.
+struct NormParams {
+  int64_t rows;
+  int64_t row0;    // the launch's first row
+  int32_t pieces;  // of 8 columns, in a row
+  float eps, inv_n;
+  const uint16_t* x;  // backward: dy
+  int64_t x_ld;
+  const void* res;  // backward: dsum
+  int64_t res_ld;
+  const void* v;  // backward: the stored sum
+  int64_t v_ld;
+  void* sum;  // backward: dresidual
+  int64_t sum_ld;
+  bool wide;  // residual, sum and their gradients are fp32
+  const void* w;
+  bool w_wide;
+  uint16_t* y;  // backward: dx
+  int64_t y_ld;
+  int32_t quant;
+  uint8_t* q;
+  int64_t q_ld;
+  void* scales;
+  int64_t scales_ld;
+  float* dw;
+  float* partial;
+};
+
 hipError_t launch_align(const int32_t* ids, int32_t S, int32_t E, int32_t B, int32_t* sorted_ids,
                         int32_t* expert_ids, int32_t* post_pad, int32_t max_blocks, hipStream_t stream);
 hipError_t launch_block_map(const int32_t* group_sizes, int32_t E, int32_t B, int32_t rows, int32_t* expert_ids,
@@ -151,6 +179,12 @@ hipError_t launch_pack(const uint8_t* w, int64_t w_stride_e, int64_t w_ld, const
                        uint8_t* w_out, uint8_t* ws_out, hipStream_t stream);
 hipError_t launch_quant_mxfp8(const uint16_t* x, int64_t x_ld, int64_t rows, int64_t k, uint8_t* q, int64_t q_ld,
                               uint8_t* s, int64_t s_ld, hipStream_t stream);
+struct Dropout;
+hipError_t launch_dropout(const uint16_t* x, int64_t x_ld, int64_t rows, int64_t n, float p, const uint64_t* rng,
+                          uint16_t* y, int64_t y_ld, hipStream_t stream);
+hipError_t launch_norm(const NormParams& p, const Dropout& d, hipStream_t stream);
+hipError_t launch_norm_backward(const NormParams& p, const Dropout& d, hipStream_t stream);
+int64_t norm_backward_workspace_bytes(int64_t rows, int64_t n);
 int gemm_block_m_large();
 int gemm_block_m_f8();
 int gemm_block_m_decode();

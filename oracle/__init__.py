@@ -41,8 +41,12 @@ other than itself:
     train.combine_routed / combine_backward  pinned (gemm.combine, linearity)
     train.act_mxfp8 / act_backward  pinned  (quant and gemm's parts, central differences, closed forms)
     train.wgrad_mxfp8_expert pinned (wgrad.wgrad_expert on the decoded rows)
+    block.philox4x32        pinned  (the authors' known answers)
+    block.dropout           pinned  (bit order by hand, share of kept elements, closed forms)
+    block.rmsnorm / rmsnorm_backward  pinned (closed forms, scale invariance, central differences)
+    block.quantize_per_token  pinned (torch's float8_e4m3fn cast)
 """
 
-from . import formats, bucket, align, gemm, wgrad, layer, layout, quant, train  # noqa: F401
+from . import formats, bucket, align, gemm, wgrad, layer, layout, quant, train, block  # noqa: F401
 
-__all__ = ["formats", "bucket", "align", "gemm", "wgrad", "layer", "layout", "quant", "train"]
+__all__ = ["formats", "bucket", "align", "gemm", "wgrad", "layer", "layout", "quant", "train", "block"]

@@ -1,0 +1,158 @@
+"""CPU tests of the block half of the C ABI (include/moe_block.h): it exports
+what the header declares, and every argument check rejects bad calls before
+anything reaches a GPU (all calls here are invalid on purpose)."""
+
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+moe = pytest.importorskip("mixture_experts_grouped_moe_amd")
+L = moe.lib
+
+INVALID, UNSUPPORTED = 1, 2
+P = 1 << 32  # never dereferenced: every call below is rejected first
+BF16, FP32 = moe.MOE_BF16, moe.MOE_FP32
+
+
+@pytest.fixture
+def no_device():
+    if torch.cuda.is_available():
+        pytest.skip("argument-rejection tests run on hosts without a GPU")
+
+
+def _header():
+    return re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "moe_block.h")).read(), flags=re.S)
+
+
+def test_exports_every_declared_symbol():
+    for name in sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", _header()))):
+        assert hasattr(L, name), name
+        assert name in moe.__all__ and callable(getattr(moe, name))
+
+
+def test_struct_mirrors(tmp_path):
+    """Field names, offsets and sizes of the ctypes mirrors are those of the header's structs."""
+    structs = {m[1]: re.findall(r"(\w+);", m[0]) for m in re.findall(r"typedef struct \{(.*?)\} (\w+);", _header(), re.S)}
+    mirrors = {"moe_" + re.sub(r"(?<!^)([A-Z])", r"_\1", n[3:]).lower().lstrip("_"): c for n, c in vars(moe.block).items()
+               if isinstance(c, type) and issubclass(c, ctypes.Structure)}
+    assert set(structs) == set(mirrors)
+    lines = [f'printf("%s %zu %zu\\n", "{s}.{f}", offsetof({s}, {f}), sizeof((({s}*)0)->{f}));'
+             for s, fields in structs.items() for f in fields]
+    src = tmp_path / "o.c"
+    src.write_text('#include <stdio.h>\n#include "moe_block.h"\nint main(void) {' + "\n".join(lines) + "return 0; }")
+    subprocess.run(["gcc", "-std=c99", f"-I{ROOT}/include", str(src), "-o", str(tmp_path / "o")], check=True)
+    said = subprocess.run([str(tmp_path / "o")], check=True, capture_output=True, text=True).stdout.split("\n")
+    want = [f"{s}.{n} {getattr(mirrors[s], n).offset} {getattr(mirrors[s], n).size}" for s in structs
+            for n, _ in mirrors[s]._fields_]
+    assert [l for l in said if l] == want
+
+
+def refused(st):
+    return st in (INVALID, UNSUPPORTED)
+
+
+def _drop(x=P, xld=64, rows=4, n=64, p=0.5, rng=2 * P, y=3 * P, yld=64):
+    return L.moe_dropout(x, xld, rows, n, p, rng, y, yld, None)
+
+
+def _norm(**kw):
+    d = dict(rows=4, n=64, x=P, x_ld=64, p=0.5, rng=2 * P, residual=3 * P, residual_ld=64, residual_dtype=FP32,
+             sum=4 * P, sum_ld=64, weight=5 * P, weight_dtype=BF16, eps=1e-6, y=6 * P, y_ld=64, quant=1, q=7 * P,
+             q_ld=64, scales=8 * P, scales_ld=2)
+    return L.moe_rmsnorm(ctypes.byref(moe.block.MoeRmsnormArgs(**{**d, **kw})), None)
+
+
+def _norm_bwd(**kw):
+    d = dict(rows=4, n=64, dy=P, dy_ld=64, dsum=2 * P, dsum_ld=64, sum=3 * P, sum_ld=64, sum_dtype=FP32, weight=4 * P,
+             weight_dtype=BF16, eps=1e-6, p=0.5, rng=5 * P, dresidual=6 * P, dresidual_ld=64, dx=7 * P, dx_ld=64,
+             dweight=8 * P, workspace=9 * P, workspace_bytes=1 << 24)
+    return L.moe_rmsnorm_backward(ctypes.byref(moe.block.MoeRmsnormBackwardArgs(**{**d, **kw})), None)
+
+
+def test_dropout_rejects(no_device):
+    assert not refused(_drop())
+    assert not refused(_drop(y=P))                      # in place
+    assert not refused(_drop(p=0.0, rng=None)) and not refused(_drop(p=1.0)) and not refused(_drop(rows=0, x=None, y=None))
+    assert not refused(_drop(p=2.0 ** -18, rng=None))   # a threshold of 0
+    for bad in (dict(rows=-1), dict(n=60), dict(n=0), dict(n=1 << 31), dict(rows=1 << 58), dict(p=-0.1), dict(p=1.1),
+                dict(p=float("nan")), dict(rng=None), dict(rng=P + 4), dict(x=None), dict(y=None), dict(x=P + 8),
+                dict(y=3 * P + 2), dict(xld=56), dict(yld=68), dict(y=P + 16), dict(y=P, yld=72), dict(y=2 * P),
+                dict(rng=3 * P + 64), dict(rows=1 << 30, xld=1 << 40)):
+        assert _drop(**bad) == INVALID, bad
+
+
+def test_norm_rejects(no_device):
+    assert not refused(_norm()) and L.moe_rmsnorm(None, None) == INVALID
+    assert not refused(_norm(sum=3 * P))                                           # the residual in place
+    assert not refused(_norm(residual=None, sum=None, p=0.0, rng=None))
+    assert not refused(_norm(y=None)) and not refused(_norm(quant=0, q=None, scales=None, q_ld=0, scales_ld=0))
+    assert not refused(_norm(quant=2, scales_ld=0)) and not refused(_norm(rows=0, x=None, y=None, q=None, scales=None))
+    assert not refused(_norm(n=8, quant=2)) and not refused(_norm(eps=0.0))
+    for bad in (dict(rows=-1), dict(rows=1 << 31), dict(n=40), dict(n=0), dict(n=60, quant=0), dict(eps=-1e-6),
+                dict(eps=float("inf")), dict(eps=float("nan")), dict(p=2.0), dict(rng=None), dict(weight=None),
+                dict(weight=5 * P + 8), dict(x=None), dict(x=P + 2), dict(x_ld=63), dict(x_ld=56), dict(residual=3 * P + 4),
+                dict(residual_ld=60), dict(sum_ld=60), dict(sum=4 * P + 8), dict(y_ld=60), dict(y=6 * P + 8),
+                dict(quant=0, y=None), dict(quant=3), dict(q=None), dict(scales=None), dict(q_ld=60), dict(q=7 * P + 4),
+                dict(scales_ld=1), dict(quant=2, scales=8 * P + 2), dict(rows=1 << 30, y_ld=1 << 40)):
+        assert _norm(**bad) == INVALID, bad
+    assert _norm(n=16384 + 32, x_ld=1 << 15) == UNSUPPORTED
+    assert _norm(residual_dtype=moe.MOE_E4M3) == UNSUPPORTED and _norm(weight_dtype=0) == UNSUPPORTED
+
+
+def test_norm_backward_rejects(no_device):
+    assert not refused(_norm_bwd()) and L.moe_rmsnorm_backward(None, None) == INVALID
+    assert not refused(_norm_bwd(dresidual=2 * P)) and not refused(_norm_bwd(dsum=None))
+    assert not refused(_norm_bwd(dweight=None, workspace=None, workspace_bytes=0))
+    assert not refused(_norm_bwd(dresidual=None, dx=None))
+    for bad in (dict(rows=-1), dict(n=60), dict(eps=-1.0), dict(rng=None), dict(dy=None), dict(sum=None),
+                dict(weight=None), dict(dy=P + 8), dict(dsum=2 * P + 8), dict(dy_ld=60), dict(sum_ld=60),
+                dict(dsum_ld=60), dict(dresidual_ld=60), dict(dx_ld=60), dict(dresidual=None, dx=None, dweight=None),
+                dict(dweight=8 * P + 2), dict(workspace=None), dict(workspace=9 * P + 8),
+                dict(workspace_bytes=moe.moe_rmsnorm_backward_workspace_bytes(4, 64) - 1)):
+        assert _norm_bwd(**bad) == INVALID, bad
+    assert _norm_bwd(n=16392, dy_ld=1 << 15) == UNSUPPORTED and _norm_bwd(sum_dtype=0) == UNSUPPORTED
+
+
+def test_workspaces():
+    f = moe.moe_rmsnorm_backward_workspace_bytes
+    assert f(0, 64) >= 0 and f(-1, 64) == -1 and f(4, 60) == -1 and f(4, 16392) == -1 and f(4, 0) == -1
+    assert f(1 << 30, 16384) == f(1 << 20, 16384) <= 256 << 20    # partial sums of workgroups, not rows
+
+
+def _overlaps(call, outputs, inputs, allowed=()):
+    names = outputs + inputs
+    ptr = {n: (i + 20) << 32 for i, n in enumerate(names)}
+    assert not refused(call(**ptr))
+    for i, a in enumerate(outputs):
+        for b in outputs[i + 1:] + inputs:
+            st = call(**{**ptr, a: ptr[b]})
+            assert refused(st) == ((a, b) not in allowed), (a, b)
+            assert refused(call(**{**ptr, a: ptr[b] + 16})), (a, b)
+
+
+def test_overlaps_are_rejected(no_device):
+    _overlaps(_drop, ["y"], ["x"], [("y", "x")])
+    _overlaps(_norm, ["sum", "y", "q"], ["x", "residual", "weight"], [("sum", "residual")])
+    _overlaps(_norm_bwd, ["dresidual", "dx", "dweight", "workspace"], ["dy", "dsum", "sum", "weight"],
+              [("dresidual", "dsum")])
+    assert _norm(scales=7 * P) == INVALID and _norm(rng=6 * P) == INVALID and _norm_bwd(rng=7 * P) == INVALID
+
+
+def test_binding_rejects_before_the_library():
+    x, w, r = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(64), torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError):            # not on a device
+        moe.moe_dropout(x, 0.5, r)
+    with pytest.raises(TypeError):
+        moe.moe_dropout(x.float(), 0.5, r)
+    with pytest.raises(ValueError):
+        moe.moe_rmsnorm(x, w)
+    with pytest.raises(TypeError):
+        moe.moe_rmsnorm(x.half(), w)
+    with pytest.raises(ValueError):
+        moe.moe_rmsnorm_backward(x, x, w)
