@@ -128,7 +128,7 @@ moe_status moe_rmsnorm(const moe_rmsnorm_args* args, moe_stream_t stream) {
   p.rows = rows;
   p.pieces = (int32_t)(n / 8);
   p.eps = a.eps;
-  p.inv_n = 1.0f / (float)n;
+  p.n = (float)n;
   p.x = static_cast<const uint16_t*>(a.x);
   p.x_ld = a.x_ld;
   p.res = a.residual;
@@ -186,7 +186,7 @@ moe_status moe_rmsnorm_backward(const moe_rmsnorm_backward_args* args, moe_strea
   p.rows = rows;
   p.pieces = (int32_t)(n / 8);
   p.eps = a.eps;
-  p.inv_n = 1.0f / (float)n;
+  p.n = (float)n;
   p.x = static_cast<const uint16_t*>(a.dy);
   p.x_ld = a.dy_ld;
   p.res = a.dsum;

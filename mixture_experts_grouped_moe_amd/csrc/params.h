@@ -122,9 +122,8 @@ struct ActParams {
 // The norm and its gradient (norm.hip). Strides in elements.
 struct NormParams {
   int64_t rows;
-  int64_t row0;    // the launch's first row
   int32_t pieces;  // of 8 columns, in a row
-  float eps, inv_n;
+  float eps, n;   // n = 8 pieces
   const uint16_t* x;  // backward: dy
   int64_t x_ld;
   const void* res;  // backward: dsum
