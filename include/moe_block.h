@@ -1,7 +1,8 @@
 /*
  * moe_block.h - the part of libmoe's C ABI around the expert layer in a
- * transformer block: the root-mean-square norm with the residual's addition,
- * dropout and an 8-bit output, and dropout by itself. The
+ * transformer block and beside its projections: the root-mean-square norm with
+ * the residual's addition, dropout and an 8-bit output, dropout by itself, and
+ * low-rank adapters of many requests beside a shared projection. The
  * conventions of moe.h hold for every entry point here (caller-owned device
  * memory, host validation before any launch, nothing allocated or
  * synchronized, MOE_* status codes); ranges "overlap" as moe_train.h says.
@@ -146,6 +147,120 @@ moe_status moe_rmsnorm_backward(const moe_rmsnorm_backward_args* args, moe_strea
 
 /* Bytes of its workspace with dweight; -1 on bad sizes. */
 int64_t moe_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t n);
+
+/* ------------------------------------------------------------------------
+ * Low-rank adapters beside a shared projection. A "group" is one adapter (A, B):
+ * that of a request, or of one expert, or of a request's expert; slots are
+ * routed to groups by moe_align over group ids (slots of id -1 have none), and
+ * the block list is kept for all projections of the batch. For every slot s in
+ * a block of group g, with row = s / x_row_div:
+ *   h[s] = A[g] x[row]                            (fp32; stored when h != NULL)
+ *   C[s] = bf16( C[s] + scale[g] * B[g] h[s] )    (scale NULL: 1)
+ * C is what the shared projection wrote (moe_grouped_gemm, for one). Rows of C
+ * and h of slots in no block are neither read nor written. Products of bf16
+ * values are exact, sums fp32; the second product takes h as two bf16 terms
+ * (2^-16 relative), so an infinite value of B gives infinities or NaN. The
+ * order of the sums depends on the sizes alone: repeated calls give equal bits.
+ *
+ * With groups = experts, moe_grouped_gemm's block list serves the adapters too
+ * (block_m 8 and 64 are its block sizes). */
+typedef struct {
+  int64_t num_slots;
+  int32_t num_groups;
+  int32_t rank;
+  int64_t k;               /* width of x */
+  int64_t n;               /* width of C */
+  const void* x;           /* (device) bf16 [(num_slots - 1) / x_row_div + 1][k] */
+  int64_t x_ld;            /* strides in elements */
+  int32_t x_row_div;
+  const void* a;           /* (device) bf16 [num_groups][rank][k] */
+  int64_t a_stride_g;
+  int64_t a_ld;
+  const void* b;           /* (device) bf16 [num_groups][n][rank] */
+  int64_t b_stride_g;
+  int64_t b_ld;
+  const float* scale;      /* (device) fp32 [num_groups] or NULL */
+  const int32_t* sorted_slot_ids; /* (device) moe_align's sorted_token_ids, [max_blocks * block_m] */
+  const int32_t* group_ids;       /* (device) moe_align's expert_ids, [max_blocks] */
+  int32_t block_m;
+  int64_t max_blocks;
+  void* c;                 /* (device) bf16 [num_slots][n], read and written */
+  int64_t c_ld;
+  float* h;                /* (device) fp32 [num_slots][rank], contiguous, or NULL */
+  void* workspace;         /* (device, 16-byte aligned) not kept between calls; calls that may run
+                              at the same time (other streams, graphs replayed side by side) need one each */
+  int64_t workspace_bytes; /* >= moe_lora_workspace_bytes(...) */
+} moe_lora_args;
+
+/* Requirements: 0 <= num_slots <= 2^31 - 2^16; 1 <= num_groups <= 1024; rank a
+ * multiple of 8 from 8 to 128; k and n positive multiples of 8, below 2^24;
+ * x_row_div >= 1; strides cover their rows and matrices and are multiples of 8;
+ * x, a, b, c, h and workspace 16-byte aligned; block_m 8, 16, 32 or 64,
+ * max_blocks >= moe_align_max_blocks(num_slots, num_groups, block_m) and
+ * max_blocks * block_m < 2^31. A block whose group id lies outside
+ * [0, num_groups) and a slot id outside [0, num_slots) are skipped; no slot may
+ * stand in the list twice. c, h and workspace must not overlap each other or an
+ * input. */
+moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream);
+
+/* The block size that suits num_slots slots over num_groups groups: 16, or 64
+ * from 32 slots a group on. -1 on bad sizes. */
+int32_t moe_lora_block_m(int64_t num_slots, int32_t num_groups);
+
+/* Bytes of moe_lora's workspace; -1 on bad sizes. */
+int64_t moe_lora_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t rank, int64_t k, int64_t n,
+                                 int32_t block_m, int64_t max_blocks);
+
+/* Its gradients, from dy = the gradient of C after the addition:
+ *   dh[s]  = scale[g] * B[g]^T dy[s]
+ *   dx[s] += A[g]^T dh[s]                         (bf16, one rounding; dx NULL: not computed)
+ *   da[g]  = sum of dh[s] x[s / x_row_div]^T      (fp32 [num_groups][rank][k])
+ *   db[g]  = scale[g] * sum of dy[s] h[s]^T       (fp32 [num_groups][n][rank])
+ * dx has a row per slot (the shared projection's gradient, to which this adds);
+ * where x_row_div > 1, moe_combine_routed adds the rows of a token. dy passes
+ * through to the shared projection unchanged. da and db are written for every
+ * group, zeros for one without slots; both NULL: not computed (h and x are then
+ * not read). The second products take dh, and the weights' gradients dh and h,
+ * as two bf16 terms (2^-16 relative). Rows of dx of slots in no block are left. */
+typedef struct {
+  int64_t num_slots;
+  int32_t num_groups;
+  int32_t rank;
+  int64_t k;
+  int64_t n;
+  const void* dy;          /* (device) bf16 [num_slots][n] */
+  int64_t dy_ld;
+  const void* x;           /* as in the forward pass, and so on */
+  int64_t x_ld;
+  int32_t x_row_div;
+  const void* a;
+  int64_t a_stride_g;
+  int64_t a_ld;
+  const void* b;
+  int64_t b_stride_g;
+  int64_t b_ld;
+  const float* scale;
+  const int32_t* sorted_slot_ids;
+  const int32_t* group_ids;
+  int32_t block_m;
+  int64_t max_blocks;
+  const float* h;          /* (device) fp32 [num_slots][rank] as the forward pass stored it */
+  void* dx;                /* (device) bf16 [num_slots][k], read and written, or NULL */
+  int64_t dx_ld;
+  float* da;               /* (device) fp32, contiguous, or NULL */
+  float* db;
+  void* workspace;
+  int64_t workspace_bytes; /* >= moe_lora_backward_workspace_bytes(...) */
+} moe_lora_backward_args;
+
+/* Requirements as for moe_lora, and moe_align's order of the block list (groups
+ * ascending, each group's blocks together, -1 behind the last); da and db both
+ * or neither, and one of dx and the two at least; da and db 16-byte aligned.
+ * dx, da, db and workspace must not overlap each other or an input. */
+moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t stream);
+
+int64_t moe_lora_backward_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t rank, int64_t k, int64_t n,
+                                          int32_t block_m, int64_t max_blocks);
 
 #ifdef __cplusplus
 }

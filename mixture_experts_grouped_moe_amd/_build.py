@@ -32,7 +32,7 @@ FLAGS = [
 ]
 SOURCES = ["api.cpp", "align.hip", "gemm.hip", "decode.hip", "decode_layer.hip", "combine.hip", "wgrad.hip", "pack.hip",
            "quant.hip", "gemm_f8.hip", "api_train.cpp", "route.hip", "act.hip", "wgrad_mxfp8.hip",
-           "api_block.cpp", "dropout.hip", "norm.hip"]
+           "api_block.cpp", "dropout.hip", "norm.hip", "lora.hip", "lora_grad.hip"]
 
 
 def _hipcc():

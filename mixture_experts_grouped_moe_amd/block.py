@@ -8,6 +8,16 @@ MXFP8 activations, with dropout of the layer's output:
     ... y to the router, q and s to moe_grouped_gemm(a_scale=s), r the next block's residual ...
 
     dx, dres, dweight = moe_rmsnorm_backward(dy, r, weight, dsum=dr, p=p, rng=rng)
+
+Adapters of many requests beside a projection, one block list for all
+projections of the batch (group = adapter; or adapter * E + expert):
+
+    routing = moe_align(adapter_of_slot, G, moe_lora_block_m(S, G))
+    c = moe_grouped_gemm(...)                                  # or any shared projection
+    c, h = moe_lora(c, x, a, b, routing, scale, keep_h=True)   # c += scale B (A x)
+
+    dx = moe_grouped_gemm(dc, ...)                             # the projection's gradient
+    da, db = moe_lora_backward(dc, x, a, b, routing, h, scale, dx=dx)
 """
 
 import ctypes
@@ -19,7 +29,8 @@ from .training import _flat, _mat, _new, _on_stream, _same_device, _stream
 
 __all__ = [
     "moe_dropout", "moe_rmsnorm", "moe_rmsnorm_backward", "moe_rmsnorm_backward_workspace_bytes",
-    "MOE_QUANT_NONE", "MOE_QUANT_MXFP8", "MOE_QUANT_PER_TOKEN",
+    "moe_lora", "moe_lora_backward", "moe_lora_block_m", "moe_lora_workspace_bytes",
+    "moe_lora_backward_workspace_bytes", "MOE_QUANT_NONE", "MOE_QUANT_MXFP8", "MOE_QUANT_PER_TOKEN",
 ]
 
 MOE_QUANT_NONE, MOE_QUANT_MXFP8, MOE_QUANT_PER_TOKEN = 0, 1, 2
@@ -49,12 +60,40 @@ class MoeRmsnormBackwardArgs(ctypes.Structure):
     ]
 
 
+_LORA = [
+    ("x", _vp), ("x_ld", _i64), ("x_row_div", _i32), ("a", _vp), ("a_stride_g", _i64), ("a_ld", _i64), ("b", _vp),
+    ("b_stride_g", _i64), ("b_ld", _i64), ("scale", _vp), ("sorted_slot_ids", _vp), ("group_ids", _vp),
+    ("block_m", _i32), ("max_blocks", _i64),
+]
+_LORA_SIZES = [("num_slots", _i64), ("num_groups", _i32), ("rank", _i32), ("k", _i64), ("n", _i64)]
+
+
+class MoeLoraArgs(ctypes.Structure):
+    """ctypes mirror of moe_lora_args (include/moe_block.h)."""
+    _fields_ = _LORA_SIZES + _LORA + [
+        ("c", _vp), ("c_ld", _i64), ("h", _vp), ("workspace", _vp), ("workspace_bytes", _i64),
+    ]
+
+
+class MoeLoraBackwardArgs(ctypes.Structure):
+    """ctypes mirror of moe_lora_backward_args (include/moe_block.h)."""
+    _fields_ = _LORA_SIZES + [("dy", _vp), ("dy_ld", _i64)] + _LORA + [
+        ("h", _vp), ("dx", _vp), ("dx_ld", _i64), ("da", _vp), ("db", _vp), ("workspace", _vp),
+        ("workspace_bytes", _i64),
+    ]
+
+
 def _bind():
     sig = {
         "moe_dropout": (_i32, [_vp, _i64, _i64, _i64, _f32, _vp, _vp, _i64, _vp]),
         "moe_rmsnorm": (_i32, [ctypes.POINTER(MoeRmsnormArgs), _vp]),
         "moe_rmsnorm_backward": (_i32, [ctypes.POINTER(MoeRmsnormBackwardArgs), _vp]),
         "moe_rmsnorm_backward_workspace_bytes": (_i64, [_i64, _i64]),
+        "moe_lora": (_i32, [ctypes.POINTER(MoeLoraArgs), _vp]),
+        "moe_lora_backward": (_i32, [ctypes.POINTER(MoeLoraBackwardArgs), _vp]),
+        "moe_lora_block_m": (_i32, [_i64, _i32]),
+        "moe_lora_workspace_bytes": (_i64, [_i64, _i32, _i32, _i64, _i64, _i32, _i64]),
+        "moe_lora_backward_workspace_bytes": (_i64, [_i64, _i32, _i32, _i64, _i64, _i32, _i64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -219,3 +258,130 @@ def moe_rmsnorm_backward(dy, sum, weight, dsum=None, eps=1e-6, p=0.0, rng=None, 
         dx.data_ptr() if dx is not None else None, dxld, dw.data_ptr() if dw is not None else None, ws_p, ws_n)),
         _stream(dy)))
     return result
+
+
+def moe_lora_block_m(num_slots, num_groups):
+    """The block size to align num_slots slots over num_groups groups with."""
+    return int(lib.moe_lora_block_m(int(num_slots), int(num_groups)))
+
+
+def moe_lora_workspace_bytes(num_slots, num_groups, rank, k, n, block_m, max_blocks):
+    """Bytes of moe_lora's workspace."""
+    return int(lib.moe_lora_workspace_bytes(num_slots, num_groups, rank, k, n, block_m, max_blocks))
+
+
+def moe_lora_backward_workspace_bytes(num_slots, num_groups, rank, k, n, block_m, max_blocks):
+    """Bytes of moe_lora_backward's workspace."""
+    return int(lib.moe_lora_backward_workspace_bytes(num_slots, num_groups, rank, k, n, block_m, max_blocks))
+
+
+def _adapters(t, name):
+    """(groups, rows, columns, group stride, row stride) of adapter matrices."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+        _need(t, name, torch.bfloat16, 3)
+    (G, r, c), (sg, ld, one) = t.shape, t.stride()
+    if one != 1 and G * r * c:
+        _need(t, name, torch.bfloat16, 3)
+    if r == 1:  # (a stride that is stepped by never means nothing)
+        ld = -(-c // 8) * 8
+    return G, r, c, sg if G > 1 else r * ld, ld
+
+
+def _lora_args(x, a, b, routing, scale, row_div, S, N):
+    """The arguments that both adapter entry points share: (sizes, fields, G, R, K)."""
+    G, R, K, a_g, a_ld = _adapters(a, "a")
+    G2, N2, R2, b_g, b_ld = _adapters(b, "b")
+    if (G2, N2, R2) != (G, N, R):
+        raise ValueError(f"b must be [{G}, {N}, {R}] beside a [{G}, {R}, {K}], got {[G2, N2, R2]}")
+    div = int(row_div)
+    if div < 1:
+        raise ValueError(f"row_div must be >= 1, got {div}")
+    x_ld = _mat(x, "x", torch.bfloat16, -(-S // div), K)[2]
+    ids, groups = routing[0], routing[1]
+    for t, name in ((ids, "sorted_slot_ids"), (groups, "group_ids")):
+        _need(t, name, torch.int32, 1)
+    blocks = groups.numel()
+    bm = ids.numel() // blocks if blocks else moe_lora_block_m(S, G)
+    if bm * blocks != ids.numel():
+        raise ValueError("the routing's arrays do not belong together")
+    scale_p = None
+    if scale is not None:
+        _flat(scale, "scale", torch.float32, (G,))
+        scale_p = scale.data_ptr()
+    _same_device(x, a, b, ids, groups, scale)
+    sizes = S, G, R, K, N
+    return sizes, (x.data_ptr(), x_ld, div, a.data_ptr(), a_g, a_ld, b.data_ptr(), b_g, b_ld, scale_p, ids.data_ptr(),
+                   groups.data_ptr(), bm, blocks)
+
+
+def _workspace(workspace, need, like):
+    """The address and size of the caller's workspace, or of a new one."""
+    if workspace is None:
+        if need < 0:
+            return None, 0, None  # (the call says what is wrong with the sizes)
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1)
+        _same_device(like, workspace)
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+@_on_stream
+def moe_lora(c, x, a, b, routing, scale=None, row_div=1, keep_h=False, workspace=None):
+    """Adds low-rank adapters to a shared projection's output, in place:
+    c[s] += scale[g] * b[g] @ (a[g] @ x[s // row_div]) for the slots s of every
+    group g.
+
+    c: bf16 [S, N], the projection's output; x: bf16 [S / row_div, K], its
+    input; a: bf16 [G, R, K], b: bf16 [G, N, R] (8 <= R <= 128, a multiple of 8;
+    rows and matrices may be strided); scale: fp32 [G]; routing: moe_align's
+    over the slots' group ids, at block size 8, 16, 32 or 64
+    (moe_lora_block_m(S, G); with groups = experts, the grouped GEMM's own).
+    Slots in no group keep their rows. Returns c; with keep_h (c, h), h fp32
+    [S, R] = a @ x of the routed slots for moe_lora_backward."""
+    S, N, c_ld = _mat(c, "c", torch.bfloat16)
+    sizes, args = _lora_args(x, a, b, routing, scale, row_div, S, N)
+    h = torch.empty((S, sizes[2]), dtype=torch.float32, device=c.device) if keep_h else None
+    need = 0 if workspace is not None else lib.moe_lora_workspace_bytes(*sizes, *args[-2:])
+    ws_p, ws_n, ws = _workspace(workspace, need, c)
+    _same_device(c, x)
+    _check(lib.moe_lora(ctypes.byref(MoeLoraArgs(*sizes, *args, c.data_ptr(), c_ld, h.data_ptr() if keep_h else None,
+                                                 ws_p, ws_n)), _stream(c)))
+    return (c, h) if keep_h else c
+
+
+@_on_stream
+def moe_lora_backward(dy, x, a, b, routing, h, scale=None, row_div=1, dx=None, weights=True, out=None,
+                      workspace=None):
+    """Gradients of moe_lora from dy (bf16 [S, N], the gradient of c after the
+    addition) and the h that the forward pass kept.
+
+    Returns (da fp32 [G, R, K], db fp32 [G, N, R]), zeros for groups without
+    slots; (None, None) with weights=False. dx (bf16 [S, K], the shared
+    projection's gradient of its input, a row per slot) gets the adapters' part
+    added in place. The other arguments as in the forward pass; `out` may give
+    da and db."""
+    S, N, dy_ld = _mat(dy, "dy", torch.bfloat16)
+    sizes, args = _lora_args(x, a, b, routing, scale, row_div, S, N)
+    _, G, R, K, _ = sizes
+    h_p = da_p = db_p = dx_p = da = db = None
+    dx_ld = 0
+    if weights:
+        _flat(h, "h", torch.float32, (S, R))
+        h_p = h.data_ptr()
+        if out is None:
+            da = torch.empty((G, R, K), dtype=torch.float32, device=dy.device)
+            db = torch.empty((G, N, R), dtype=torch.float32, device=dy.device)
+        else:
+            da, db = out
+            _flat(da, "da", torch.float32, (G, R, K))
+            _flat(db, "db", torch.float32, (G, N, R))
+        da_p, db_p = da.data_ptr(), db.data_ptr()
+    if dx is not None:
+        dx_ld, dx_p = _mat(dx, "dx", torch.bfloat16, S, K)[2], dx.data_ptr()
+    need = 0 if workspace is not None else lib.moe_lora_backward_workspace_bytes(*sizes, *args[-2:])
+    ws_p, ws_n, ws = _workspace(workspace, need, dy)
+    _same_device(dy, x, h if weights else None, dx, da, db)
+    _check(lib.moe_lora_backward(ctypes.byref(MoeLoraBackwardArgs(
+        *sizes, dy.data_ptr(), dy_ld, *args, h_p, dx_p, dx_ld, da_p, db_p, ws_p, ws_n)), _stream(dy)))
+    return da, db

@@ -9,6 +9,7 @@
 
 #include "dropout_util.h"
 #include "host.h"
+#include "lora_host.h"
 #include "params.h"
 #include "ranges.h"
 
@@ -19,12 +20,15 @@ using moe::check_device;
 using moe::clash;
 using moe::fail;
 using moe::hip_status;
+using moe::kAlignMaxExperts;
 using moe::misaligned;
 using moe::ok;
 using moe::Range;
 using moe::span;
 
 constexpr int64_t kNormMaxWidth = 16384;
+constexpr int32_t kLoraMaxRank = 128;
+constexpr int64_t kLoraMaxWidth = (int64_t)1 << 24;
 
 int64_t dtype_bytes(int32_t dtype) { return dtype == MOE_FP32 ? 4 : 2; }
 
@@ -63,6 +67,92 @@ moe_status check_norm(int64_t rows, int64_t n, int64_t multiple, int32_t dtype, 
   if (weight == nullptr) return fail(MOE_ERR_INVALID_ARGUMENT, "weight is null");
   if (misaligned(weight, 16)) return fail(MOE_ERR_INVALID_ARGUMENT, "weight must be 16-byte aligned");
   return check_dropout(p, rng);
+}
+
+// What the adapters' two entry points share: their arguments but the matrices
+// by slot.
+struct LoraCommon {
+  int64_t S, K, N;
+  int32_t G, R;
+  const void* x;
+  int64_t x_ld;
+  int32_t x_row_div;
+  const void* a;
+  int64_t a_stride_g, a_ld;
+  const void* b;
+  int64_t b_stride_g, b_ld;
+  const float* scale;
+  const int32_t* sorted;
+  const int32_t* groups;
+  int32_t block_m;
+  int64_t max_blocks;
+};
+
+template <class T>
+LoraCommon lora_common(const T& a) {
+  return {a.num_slots, a.k,          a.n,    a.num_groups, a.rank,           a.x,
+          a.x_ld,      a.x_row_div,  a.a,    a.a_stride_g, a.a_ld,           a.b,
+          a.b_stride_g, a.b_ld,      a.scale, a.sorted_slot_ids, a.group_ids, a.block_m,
+          a.max_blocks};
+}
+
+moe_status check_lora_sizes(int64_t S, int32_t G, int32_t R, int64_t K, int64_t N, int32_t bm, int64_t max_blocks) {
+  if (S < 0 || S > INT32_MAX - 65536)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "num_slots must be in [0, 2^31 - 2^16]");
+  if (G < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "num_groups < 1");
+  if (G > kAlignMaxExperts) return fail(MOE_ERR_UNSUPPORTED, "num_groups %d > %d", G, kAlignMaxExperts);
+  if (R < 8 || R % 8 != 0) return fail(MOE_ERR_INVALID_ARGUMENT, "rank must be a positive multiple of 8");
+  if (R > kLoraMaxRank) return fail(MOE_ERR_UNSUPPORTED, "rank %d > %d", R, kLoraMaxRank);
+  if (K < 8 || K % 8 != 0 || N < 8 || N % 8 != 0 || K >= kLoraMaxWidth || N >= kLoraMaxWidth)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "k and n must be positive multiples of 8, below 2^24");
+  if (bm != 8 && bm != 16 && bm != 32 && bm != 64)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "block_m must be 8, 16, 32 or 64");
+  const int64_t need = moe_align_max_blocks(S, G, bm);
+  if (max_blocks < need)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "max_blocks %lld < required %lld", (long long)max_blocks, (long long)need);
+  if (max_blocks * bm >= INT32_MAX) return fail(MOE_ERR_INVALID_ARGUMENT, "max_blocks too large");
+  return MOE_OK;
+}
+
+moe_status check_lora(const LoraCommon& a) {
+  moe_status st = check_lora_sizes(a.S, a.G, a.R, a.K, a.N, a.block_m, a.max_blocks);
+  if (st != MOE_OK) return st;
+  if (a.x_row_div < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "x_row_div < 1");
+  const int64_t rows = a.S > 0 ? (a.S - 1) / a.x_row_div + 1 : 0;
+  st = check_rows("x", a.x, a.x_ld, rows, a.K, true);
+  if (st == MOE_OK) st = check_rows("a", a.a, a.a_ld, a.R, a.K, true);
+  if (st == MOE_OK) st = check_rows("b", a.b, a.b_ld, a.N, a.R, true);
+  if (st != MOE_OK) return st;
+  if (bad_ld(a.a_stride_g, a.R * a.a_ld, 8, a.G) || bad_ld(a.b_stride_g, a.N * a.b_ld, 8, a.G))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "a_stride_g and b_stride_g must cover a matrix and be multiples of 8");
+  if (a.max_blocks > 0 && (a.sorted == nullptr || a.groups == nullptr))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "the block list is null");
+  if (misaligned(a.scale, 4) || misaligned(a.sorted, 4) || misaligned(a.groups, 4))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "scale and the block list must be 4-byte aligned");
+  return MOE_OK;
+}
+
+// One of `outs` overlaps another or an input of both entry points.
+bool lora_clash(const LoraCommon& a, std::initializer_list<Range> outs) {
+  const int64_t rows = a.S > 0 ? (a.S - 1) / a.x_row_div + 1 : 0;
+  return clash(outs, {span(a.x, rows, a.x_ld, a.K, 2), {a.a, ((a.G - 1) * a.a_stride_g + (a.R - 1) * a.a_ld + a.K) * 2},
+                      {a.b, ((a.G - 1) * a.b_stride_g + (a.N - 1) * a.b_ld + a.R) * 2}, {a.scale, a.G * 4},
+                      {a.sorted, a.max_blocks * a.block_m * 4}, {a.groups, a.max_blocks * 4}});
+}
+
+moe::LoraParams lora_params(const LoraCommon& a) {
+  moe::LoraParams p{};
+  p.S = (int32_t)a.S;
+  p.G = a.G;
+  p.R = a.R;
+  p.K = (int32_t)a.K;
+  p.N = (int32_t)a.N;
+  p.bm = a.block_m;
+  p.max_blocks = (int32_t)a.max_blocks;
+  p.sorted = a.sorted;
+  p.groups = a.groups;
+  p.scale = a.scale;
+  return p;
 }
 
 }  // namespace
@@ -204,6 +294,153 @@ moe_status moe_rmsnorm_backward(const moe_rmsnorm_backward_args* args, moe_strea
   p.partial = static_cast<float*>(a.workspace);
   return hip_status(moe::launch_norm_backward(p, moe::make_dropout(a.p, a.rng), (hipStream_t)stream),
                     "moe_rmsnorm_backward launch");
+}
+
+int32_t moe_lora_block_m(int64_t num_slots, int32_t num_groups) {
+  if (num_slots < 0 || num_groups < 1) return -1;
+  return num_slots >= 32 * (int64_t)num_groups ? 64 : 16;
+}
+
+int64_t moe_lora_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t rank, int64_t k, int64_t n,
+                                 int32_t block_m, int64_t max_blocks) {
+  if (check_lora_sizes(num_slots, num_groups, rank, k, n, block_m, max_blocks) != MOE_OK) return -1;
+  return moe::lora_k_splits(max_blocks, k) * num_slots * rank * 4;
+}
+
+moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream) {
+  if (args == nullptr) return fail(MOE_ERR_INVALID_ARGUMENT, "args is null");
+  const LoraCommon a = lora_common(*args);
+  moe_status st = check_lora(a);
+  if (st == MOE_OK) st = check_rows("c", args->c, args->c_ld, a.S, a.N, true);
+  if (st != MOE_OK) return st;
+  if (misaligned(args->h, 16) || misaligned(args->workspace, 16))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "h and workspace must be 16-byte aligned");
+  const int64_t need = moe_lora_workspace_bytes(a.S, a.G, a.R, a.K, a.N, a.block_m, a.max_blocks);
+  if (args->workspace_bytes < need || (need > 0 && args->workspace == nullptr))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "workspace of %lld bytes, %lld needed", (long long)args->workspace_bytes,
+                (long long)need);
+  if (lora_clash(a, {span(args->c, a.S, args->c_ld, a.N, 2), {args->h, a.S * a.R * 4}, {args->workspace, need}}))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "c, h or workspace overlaps another or an input");
+  st = check_device();
+  if (st != MOE_OK) return st;
+  if (a.S == 0) return ok();
+  moe::LoraParams p = lora_params(a);
+  p.x = static_cast<const uint16_t*>(a.x);
+  p.x_ld = a.x_ld;
+  moe::lora_set_division(a.x_row_div, p.div_magic, p.div_shift);
+  p.w = static_cast<const uint16_t*>(a.a);
+  p.w_g = a.a_stride_g;
+  p.w_ld = a.a_ld;
+  p.splits = moe::lora_k_splits(a.max_blocks, a.K);
+  p.h = args->h;
+  p.part = p.splits == 1 && p.h != nullptr ? p.h : static_cast<float*>(args->workspace);
+  st = hip_status(moe::launch_lora_down(p, (hipStream_t)stream), "moe_lora launch");
+  if (st != MOE_OK) return st;
+  p.w = static_cast<const uint16_t*>(a.b);
+  p.w_g = a.b_stride_g;
+  p.w_ld = a.b_ld;
+  p.c = static_cast<uint16_t*>(args->c);
+  p.c_ld = args->c_ld;
+  return hip_status(moe::launch_lora_up(p, (hipStream_t)stream), "moe_lora launch");
+}
+
+int64_t moe_lora_backward_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t rank, int64_t k, int64_t n,
+                                          int32_t block_m, int64_t max_blocks) {
+  if (check_lora_sizes(num_slots, num_groups, rank, k, n, block_m, max_blocks) != MOE_OK) return -1;
+  return moe::lora_grad_sizes(num_slots, num_groups, rank, k, n, max_blocks).bytes;
+}
+
+moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t stream) {
+  if (args == nullptr) return fail(MOE_ERR_INVALID_ARGUMENT, "args is null");
+  const LoraCommon a = lora_common(*args);
+  const bool weights = args->da != nullptr;
+  if (weights != (args->db != nullptr)) return fail(MOE_ERR_INVALID_ARGUMENT, "da and db: both or neither");
+  moe_status st = check_lora(a);
+  if (st == MOE_OK) st = check_rows("dy", args->dy, args->dy_ld, a.S, a.N, true);
+  if (st == MOE_OK) st = check_rows("dx", args->dx, args->dx_ld, a.S, a.K, false);
+  if (st != MOE_OK) return st;
+  if (!weights && args->dx == nullptr && a.S > 0)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "one of dx and the weights' gradients is needed");
+  if (weights && a.S > 0 && args->h == nullptr) return fail(MOE_ERR_INVALID_ARGUMENT, "h is null");
+  if (misaligned(args->h, 16) || misaligned(args->da, 16) || misaligned(args->db, 16) ||
+      misaligned(args->workspace, 16))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "h, da, db and workspace must be 16-byte aligned");
+  const moe::LoraGradSizes z = moe::lora_grad_sizes(a.S, a.G, a.R, a.K, a.N, a.max_blocks);
+  if (args->workspace_bytes < z.bytes || args->workspace == nullptr)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "workspace of %lld bytes, %lld needed", (long long)args->workspace_bytes,
+                (long long)z.bytes);
+  const Range dy = span(args->dy, a.S, args->dy_ld, a.N, 2), h = {args->h, a.S * a.R * 4};
+  const Range dx = span(args->dx, a.S, args->dx_ld, a.K, 2), ws = {args->workspace, z.bytes};
+  const Range da = {args->da, a.G * a.R * a.K * 4}, db = {args->db, a.G * a.R * a.N * 4};
+  if (lora_clash(a, {dx, da, db, ws}) || clash({dx, da, db, ws}, {dy, h}))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dx, da, db or workspace overlaps another or an input");
+  st = check_device();
+  if (st != MOE_OK) return st;
+  if (a.S == 0 && !weights) return ok();
+  char* base = static_cast<char*>(args->workspace);
+  moe::LoraGradParams q{};
+  q.S = (int32_t)a.S;
+  q.G = a.G;
+  q.R = a.R;
+  q.K = (int32_t)a.K;
+  q.N = (int32_t)a.N;
+  q.bm = a.block_m;
+  q.max_blocks = (int32_t)a.max_blocks;
+  q.sorted = a.sorted;
+  q.groups = a.groups;
+  q.scale = a.scale;
+  q.x = static_cast<const uint16_t*>(a.x);
+  q.x_ld = a.x_ld;
+  moe::lora_set_division(a.x_row_div, q.div_magic, q.div_shift);
+  q.dy = static_cast<const uint16_t*>(args->dy);
+  q.dy_ld = args->dy_ld;
+  q.h = args->h;
+  q.splits = z.splits;
+  q.da = args->da;
+  q.db = args->db;
+  q.a = static_cast<const uint16_t*>(a.a);
+  q.a_g = a.a_stride_g;
+  q.a_ld = a.a_ld;
+  q.b = static_cast<const uint16_t*>(a.b);
+  q.b_g = a.b_stride_g;
+  q.b_ld = a.b_ld;
+  q.at = reinterpret_cast<uint16_t*>(base + z.at);
+  q.bt = reinterpret_cast<uint16_t*>(base + z.bt);
+  q.dh = reinterpret_cast<float*>(base + z.dh);
+  q.table = reinterpret_cast<int32_t*>(base + z.table);
+  q.seg_blocks = z.seg_blocks;
+  q.max_segs = z.max_segs;
+  q.max_parts = z.max_parts;
+  q.da_part = reinterpret_cast<float*>(base + z.da_part);
+  q.db_part = reinterpret_cast<float*>(base + z.db_part);
+  st = hip_status(moe::launch_lora_grad_prepare(q, (hipStream_t)stream), "moe_lora_backward launch");
+  if (st != MOE_OK) return st;
+  if (a.S > 0) {
+    moe::LoraParams p = lora_params(a);
+    p.K = (int32_t)a.N;
+    p.N = (int32_t)a.K;
+    p.x = q.dy;
+    p.x_ld = q.dy_ld;
+    moe::lora_set_division(1, p.div_magic, p.div_shift);
+    p.w = q.bt;
+    p.w_g = (int64_t)a.R * a.N;
+    p.w_ld = a.N;
+    p.splits = z.splits;
+    p.part = const_cast<float*>(q.dh);
+    st = hip_status(moe::launch_lora_down(p, (hipStream_t)stream), "moe_lora_backward launch");
+    if (st != MOE_OK) return st;
+    if (args->dx != nullptr) {
+      p.w = q.at;
+      p.w_g = (int64_t)a.R * a.K;
+      p.w_ld = a.R;
+      p.c = static_cast<uint16_t*>(args->dx);
+      p.c_ld = args->dx_ld;
+      st = hip_status(moe::launch_lora_up(p, (hipStream_t)stream), "moe_lora_backward launch");
+      if (st != MOE_OK) return st;
+    }
+  }
+  if (!weights) return ok();
+  return hip_status(moe::launch_lora_grad_weights(q, (hipStream_t)stream), "moe_lora_backward launch");
 }
 
 }  // extern "C"

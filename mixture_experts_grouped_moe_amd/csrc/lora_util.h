@@ -1,0 +1,57 @@
+// Building blocks of the low-rank adapter kernels (lora.hip, lora_grad.hip).
+#pragma once
+
+#include "common.h"
+#include "params.h"
+
+namespace moe {
+
+constexpr int kLoraThreads = 256;  // four waves
+
+typedef __bf16 lora_bf16x8 __attribute__((ext_vector_type(8)));
+
+// 16 bytes as 8 bf16 of an MFMA operand.
+__device__ __forceinline__ lora_bf16x8 lora_frag(u32x4_t v) { return __builtin_bit_cast(lora_bf16x8, v); }
+
+// D[16 x 16] += A[16 x 32] B[32 x 16]: lane l gives row (of A) or column (of B)
+// l % 16 at 8 consecutive k from 8 (l / 16), and holds column l % 16, rows
+// 4 (l / 16) .. + 3 of D.
+__device__ __forceinline__ f32x4_t lora_mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(lora_frag(a), lora_frag(b), c, 0, 0, 0);
+}
+
+// Two floats as bf16 in one dword, rounded to nearest even.
+__device__ __forceinline__ uint32_t lora_pack(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// f = hi + lo to 2^-16 of f for two floats, both terms bf16 pairs. hi is rounded
+// to nearest, or towards zero where that would pass bf16's range; an infinite or
+// NaN f is hi alone.
+__device__ __forceinline__ void lora_split(float f0, float f1, uint32_t& hi, uint32_t& lo) {
+  constexpr float kMost = 0x1.FEp127f;  // bf16's largest
+  const float m0 = fabsf(f0) < INFINITY ? fminf(fmaxf(f0, -kMost), kMost) : f0;
+  const float m1 = fabsf(f1) < INFINITY ? fminf(fmaxf(f1, -kMost), kMost) : f1;
+  hi = lora_pack(m0, m1);
+  const float r0 = f0 - __uint_as_float(hi << 16), r1 = f1 - __uint_as_float(hi & 0xffff0000u);
+  lo = lora_pack(fabsf(f0) < INFINITY ? r0 : 0.0f, fabsf(f1) < INFINITY ? r1 : 0.0f);
+}
+
+// floor(s / d) for s < 2^31 (lora_set_division).
+__device__ __forceinline__ uint32_t lora_div(uint32_t s, uint32_t magic, int32_t shift) {
+  return (uint32_t)(((uint64_t)s * magic) >> shift);
+}
+
+// Rank r in the kernels: padded to 8, 16, 32, 64 or 128.
+template <class F>
+inline hipError_t lora_rank(int r, F f) {
+  if (r <= 8) return f(std::integral_constant<int, 1>{});
+  if (r <= 16) return f(std::integral_constant<int, 2>{});
+  if (r <= 32) return f(std::integral_constant<int, 4>{});
+  if (r <= 64) return f(std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 16>{});
+}
+
+}  // namespace moe

@@ -146,6 +146,57 @@ struct NormParams {
   float* partial;
 };
 
+// The low-rank adapters (lora.hip, lora_grad.hip). Strides in elements; `part`
+// holds `splits` partial sums of h, [splits][S][R].
+struct LoraParams {
+  int32_t S, G, R, K, N;
+  int32_t bm, max_blocks;
+  int32_t block0;  // the launch's first block
+  const int32_t* sorted;
+  const int32_t* groups;
+  const float* scale;
+  const uint16_t* x;  // backward: dy where h's gradient is formed, x for dA
+  int64_t x_ld;
+  uint32_t div_magic;  // of the division of slots by x_row_div
+  int32_t div_shift;
+  const uint16_t* w;  // A (or B transposed) [G][R][K], then B (or A transposed) [G][N][R]
+  int64_t w_g, w_ld;
+  float* part;
+  int32_t splits, n_splits;
+  float* h;  // where the sum of the parts is wanted
+  uint16_t* c;
+  int64_t c_ld;
+};
+
+struct LoraGradParams {
+  int32_t S, G, R, K, N;
+  int32_t bm, max_blocks;
+  const int32_t* sorted;
+  const int32_t* groups;
+  const float* scale;
+  const uint16_t* x;
+  int64_t x_ld;
+  uint32_t div_magic;
+  int32_t div_shift;
+  const uint16_t* dy;
+  int64_t dy_ld;
+  const float* h;
+  const float* dh;  // [splits][S][R]
+  int32_t splits;
+  float* da;
+  float* db;
+  const uint16_t* a;
+  int64_t a_g, a_ld;
+  const uint16_t* b;
+  int64_t b_g, b_ld;
+  uint16_t* at;  // A transposed, [G][K][R]
+  uint16_t* bt;  // B transposed, [G][R][N]
+  int32_t* table;
+  int32_t seg_blocks, max_segs, max_parts;
+  float* da_part;
+  float* db_part;
+};
+
 hipError_t launch_align(const int32_t* ids, int32_t S, int32_t E, int32_t B, int32_t* sorted_ids,
                         int32_t* expert_ids, int32_t* post_pad, int32_t max_blocks, hipStream_t stream);
 hipError_t launch_block_map(const int32_t* group_sizes, int32_t E, int32_t B, int32_t rows, int32_t* expert_ids,
@@ -184,6 +235,17 @@ hipError_t launch_dropout(const uint16_t* x, int64_t x_ld, int64_t rows, int64_t
 hipError_t launch_norm(const NormParams& p, const Dropout& d, hipStream_t stream);
 hipError_t launch_norm_backward(const NormParams& p, const Dropout& d, hipStream_t stream);
 int64_t norm_backward_workspace_bytes(int64_t rows, int64_t n);
+// The launch shapes of the adapters, a function of the sizes alone.
+int lora_k_splits(int64_t max_blocks, int64_t k);
+hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream);
+hipError_t launch_lora_up(const LoraParams& p, hipStream_t stream);
+struct LoraGradSizes {
+  int32_t splits, seg_blocks, max_segs, max_parts;
+  int64_t at, bt, dh, table, da_part, db_part, bytes;  // offsets into the workspace and its size
+};
+LoraGradSizes lora_grad_sizes(int64_t S, int32_t G, int32_t R, int64_t K, int64_t N, int64_t max_blocks);
+hipError_t launch_lora_grad_prepare(const LoraGradParams& p, hipStream_t stream);
+hipError_t launch_lora_grad_weights(const LoraGradParams& p, hipStream_t stream);
 int gemm_block_m_large();
 int gemm_block_m_f8();
 int gemm_block_m_decode();

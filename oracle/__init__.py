@@ -45,6 +45,7 @@ other than itself:
     block.dropout           pinned  (bit order by hand, share of kept elements, closed forms)
     block.rmsnorm / rmsnorm_backward  pinned (closed forms, scale invariance, central differences)
     block.quantize_per_token  pinned (torch's float8_e4m3fn cast)
+    block.lora / lora_backward  pinned (a merged weight, central differences)
 """
 
 from . import formats, bucket, align, gemm, wgrad, layer, layout, quant, train, block  # noqa: F401

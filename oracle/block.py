@@ -1,6 +1,6 @@
 """The operators around the expert layer (oracle; test infrastructure only):
 dropout from a counter-based generator and the root-mean-square norm of a
-residual stream with its gradient.
+residual stream with its gradient, and low-rank adapters with theirs.
 
 Plain definitions in float64, as include/moe_block.h states them. The generator
 is exact integer arithmetic, pinned by its authors' known answers; the gradient
@@ -80,3 +80,29 @@ def rmsnorm_backward(dy, v, weight, eps, dsum=None):
     g = dy * w
     d = s * (g - v * s * s * (g * v).mean(axis=1, keepdims=True))
     return d if dsum is None else d + np.asarray(dsum, dtype=np.float64), (dy * v * s).sum(axis=0)
+
+
+def lora(c, x, a, b, ids, scale=None, row_div=1):
+    """(C with the adapters' products added, h): ids [S] the slots' groups;
+    slots outside [0, G) keep their rows, their h is 0."""
+    c, x, a, b = (np.asarray(t, dtype=np.float64) for t in (c, x, a, b))
+    out, h = c.copy(), np.zeros((len(ids), a.shape[1]))
+    for s, g in enumerate(ids):
+        if 0 <= g < a.shape[0]:
+            h[s] = a[g] @ x[s // row_div]
+            out[s] += (1.0 if scale is None else float(scale[g])) * (b[g] @ h[s])
+    return out, h
+
+
+def lora_backward(dy, x, a, b, ids, h, scale=None, row_div=1):
+    """(the adapters' part of dx by slot, da, db)."""
+    dy, x, a, b, h = (np.asarray(t, dtype=np.float64) for t in (dy, x, a, b, h))
+    dx, da, db = np.zeros((len(ids), x.shape[1])), np.zeros(a.shape), np.zeros(b.shape)
+    for s, g in enumerate(ids):
+        if 0 <= g < a.shape[0]:
+            w = 1.0 if scale is None else float(scale[g])
+            dh = w * (b[g].T @ dy[s])
+            dx[s] = a[g].T @ dh
+            da[g] += np.outer(dh, x[s // row_div])
+            db[g] += w * np.outer(dy[s], h[s])
+    return dx, da, db

@@ -133,7 +133,8 @@ def _overlaps(call, outputs, inputs, allowed=()):
         for b in outputs[i + 1:] + inputs:
             st = call(**{**ptr, a: ptr[b]})
             assert refused(st) == ((a, b) not in allowed), (a, b)
-            assert refused(call(**{**ptr, a: ptr[b] + 16})), (a, b)
+            if b not in ("scale", "group_ids"):   # (of 16 bytes and less)
+                assert refused(call(**{**ptr, a: ptr[b] + 16})), (a, b)
 
 
 def test_overlaps_are_rejected(no_device):
@@ -156,3 +157,82 @@ def test_binding_rejects_before_the_library():
         moe.moe_rmsnorm(x.half(), w)
     with pytest.raises(ValueError):
         moe.moe_rmsnorm_backward(x, x, w)
+
+
+# ----------------------------------------------------------------- adapters
+
+_LORA = dict(num_slots=20, num_groups=3, rank=16, k=64, n=48, x=20 * P, x_ld=64, x_row_div=2, a=21 * P, a_stride_g=1024,
+             a_ld=64, b=22 * P, b_stride_g=768, b_ld=16, scale=23 * P, sorted_slot_ids=24 * P, group_ids=25 * P,
+             block_m=16, max_blocks=4)
+
+
+def _lora(**kw):
+    d = dict(_LORA, c=26 * P, c_ld=48, h=27 * P, workspace=28 * P, workspace_bytes=1 << 30)
+    return L.moe_lora(ctypes.byref(moe.block.MoeLoraArgs(**{**d, **kw})), None)
+
+
+def _lora_bwd(**kw):
+    d = dict(_LORA, dy=29 * P, dy_ld=48, h=27 * P, dx=30 * P, dx_ld=64, da=31 * P, db=32 * P, workspace=28 * P,
+             workspace_bytes=1 << 30)
+    return L.moe_lora_backward(ctypes.byref(moe.block.MoeLoraBackwardArgs(**{**d, **kw})), None)
+
+
+def _lora_bytes(f, S=20, G=3, R=16, K=64, N=48, bm=16, mb=4):
+    return f(S, G, R, K, N, bm, mb)
+
+
+def test_lora_rejects(no_device):
+    assert moe.moe_align_max_blocks(20, 3, 16) == 4
+    assert L.moe_lora(None, None) == INVALID and L.moe_lora_backward(None, None) == INVALID
+    for call in (_lora, _lora_bwd):
+        assert not refused(call()) and not refused(call(scale=None)) and not refused(call(num_groups=1, a_stride_g=1024))
+        assert not refused(call(rank=8, a_stride_g=512, b_ld=8, b_stride_g=384)) and not refused(call(b_ld=24, b_stride_g=2000))
+        assert not refused(call(num_slots=0, max_blocks=0, x=None, sorted_slot_ids=None, group_ids=None))
+        for bad in (dict(num_slots=-1), dict(num_slots=1 << 31), dict(num_groups=0), dict(rank=0), dict(rank=12),
+                    dict(k=60), dict(n=44), dict(k=0), dict(k=1 << 24, x_ld=1 << 24), dict(x_row_div=0), dict(x=None),
+                    dict(a=None), dict(b=None), dict(x=20 * P + 8), dict(a=21 * P + 8), dict(b=22 * P + 8), dict(x_ld=56),
+                    dict(x_ld=68), dict(a_ld=60), dict(a_ld=72), dict(a_stride_g=1016), dict(b_ld=8), dict(b_stride_g=760),
+                    dict(a_stride_g=1028), dict(scale=23 * P + 2), dict(sorted_slot_ids=None), dict(group_ids=None),
+                    dict(group_ids=25 * P + 2), dict(block_m=24), dict(block_m=128), dict(max_blocks=3),
+                    dict(max_blocks=1 << 27), dict(workspace=None), dict(workspace=28 * P + 8), dict(h=27 * P + 8),
+                    dict(x_ld=1 << 60), dict(a_stride_g=1 << 60)):
+            assert call(**bad) == INVALID, bad
+        assert call(num_groups=1025, max_blocks=30) == UNSUPPORTED
+        assert call(rank=136, a_stride_g=1 << 14, b_ld=136, b_stride_g=1 << 14) == UNSUPPORTED
+    assert not refused(_lora(h=None))
+    assert _lora(c=None) == INVALID and _lora(c_ld=40) == INVALID and _lora(c=26 * P + 8) == INVALID
+    assert _lora(workspace_bytes=_lora_bytes(moe.moe_lora_workspace_bytes) - 1) == INVALID
+    assert not refused(_lora_bwd(dx=None)) and not refused(_lora_bwd(da=None, db=None, h=None))
+    for bad in (dict(dy=None), dict(dy_ld=40), dict(dx_ld=56), dict(da=None), dict(db=None), dict(h=None),
+                dict(dx=None, da=None, db=None), dict(da=31 * P + 8),
+                dict(workspace_bytes=_lora_bytes(moe.moe_lora_backward_workspace_bytes) - 1)):
+        assert _lora_bwd(**bad) == INVALID, bad
+
+
+def test_lora_sizes():
+    f, g = moe.moe_lora_workspace_bytes, moe.moe_lora_backward_workspace_bytes
+    for h in (f, g):
+        assert _lora_bytes(h) >= 0
+        for bad in (dict(S=-1), dict(G=0), dict(G=1025), dict(R=4), dict(R=136), dict(K=4), dict(N=0), dict(bm=7), dict(mb=3)):
+            assert _lora_bytes(h, **bad) == -1, bad
+    m = moe.moe_lora_block_m
+    assert m(0, 1) == 16 and m(31, 1) == 16 and m(32, 1) == 64 and m(1 << 30, 1024) == 64 and m(-1, 1) == -1 and m(4, 0) == -1
+    # partial sums by segments of the list, not by slots: 512 workgroups' worth
+    assert g(1 << 24, 1, 16, 2880, 5760, 64, 1 << 18) - 8 * (1 << 24) * 16 * 4 < 128 << 20
+
+
+def test_lora_overlaps_are_rejected(no_device):
+    shared = ["x", "a", "b", "scale", "sorted_slot_ids", "group_ids"]
+    _overlaps(_lora, ["c", "h", "workspace"], shared)
+    _overlaps(_lora_bwd, ["dx", "da", "db", "workspace"], shared + ["dy", "h"])
+
+
+def test_lora_binding_rejects_before_the_library():
+    x, a, b = (torch.zeros(s, dtype=torch.bfloat16) for s in ((4, 64), (2, 8, 64), (2, 48, 8)))
+    c, ids = torch.zeros(4, 48, dtype=torch.bfloat16), torch.zeros(16, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        moe.moe_lora(c, x, a, b, (ids, ids, ids))
+    with pytest.raises(TypeError):
+        moe.moe_lora(c.float(), x, a, b, (ids, ids, ids))
+    with pytest.raises(ValueError):
+        moe.moe_lora_backward(c, x, a, b, (ids, ids, ids), torch.zeros(4, 8))

@@ -96,3 +96,45 @@ def test_quantize_mxfp8_is_the_rule_of_the_quantizer():
     back = formats.e4m3_to_f64(q) * np.repeat(np.exp2(s.astype(float) - 127), 32, axis=1)
     assert (np.abs(back - u) <= np.maximum(2.0 ** -4 * np.abs(u), np.repeat(np.exp2(s - 137.0), 32, axis=1)) +
             np.repeat(64 * np.exp2(s - 127.0), 32, axis=1) * (np.abs(u) > 448 * np.repeat(np.exp2(s - 127.0), 32, axis=1))).all()
+
+
+def _lora_case(S, G, R, K, N, div, seed):
+    g = np.random.default_rng(seed)
+    ids = g.integers(-1, G, S)
+    return (g.standard_normal((S, N)), g.standard_normal((-(-S // div), K)), g.standard_normal((G, R, K)),
+            g.standard_normal((G, N, R)), ids, g.standard_normal(G), div)
+
+
+def test_lora_is_a_merged_weight():
+    c, x, a, b, ids, scale, div = _lora_case(11, 3, 2, 5, 4, 2, 1)
+    out, h = block.lora(c, x, a, b, ids, scale, div)
+    for s, g in enumerate(ids):
+        want = c[s] if g < 0 else c[s] + (scale[g] * b[g] @ a[g]) @ x[s // div]
+        np.testing.assert_allclose(out[s], want)
+    assert (h[ids < 0] == 0).all()
+    np.testing.assert_array_equal(block.lora(c, x, a, b, ids, None, div)[0], block.lora(c, x, a, b, ids, np.ones(3), div)[0])
+
+
+def test_lora_backward_by_differences():
+    c, x, a, b, ids, scale, _ = _lora_case(6, 3, 2, 5, 4, 1, 2)
+    dy = np.random.default_rng(3).standard_normal(c.shape)
+    dx, da, db = block.lora_backward(dy, x, a, b, ids, block.lora(c, x, a, b, ids, scale)[1], scale)
+    for t, d in ((x, dx), (a, da), (b, db)):
+        for i in np.ndindex(*t.shape):
+            old, f = t[i], []
+            for e in (1e-6, -1e-6):
+                t[i] = old + e
+                f.append((dy * block.lora(c, x, a, b, ids, scale)[0]).sum())
+            t[i] = old
+            assert abs((f[0] - f[1]) / 2e-6 - d[i]) < 1e-6
+
+
+def test_lora_backward_of_shared_rows():
+    # two slots of one row of x: dx stays by slot, da adds them
+    c, x, a, b, _, scale, _ = _lora_case(4, 2, 2, 5, 4, 2, 4)
+    dy, ids = np.random.default_rng(5).standard_normal(c.shape), np.array([0, 1, 1, -1])
+    h = block.lora(c, x, a, b, ids, scale, 2)[1]
+    dx, da, db = block.lora_backward(dy, x, a, b, ids, h, scale, 2)
+    wide = block.lora_backward(dy, x[[0, 0, 1, 1]], a, b, ids, h, scale, 1)
+    for u, v in zip((dx, da, db), wide):
+        np.testing.assert_allclose(u, v)
