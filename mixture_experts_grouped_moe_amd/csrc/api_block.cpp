@@ -304,7 +304,7 @@ int32_t moe_lora_block_m(int64_t num_slots, int32_t num_groups) {
 int64_t moe_lora_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t rank, int64_t k, int64_t n,
                                  int32_t block_m, int64_t max_blocks) {
   if (check_lora_sizes(num_slots, num_groups, rank, k, n, block_m, max_blocks) != MOE_OK) return -1;
-  return moe::lora_k_splits(max_blocks, k) * num_slots * rank * 4;
+  return moe::lora_sizes(rank, k, block_m, max_blocks).bytes;
 }
 
 moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream) {
@@ -331,23 +331,33 @@ moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream) {
   p.w = static_cast<const uint16_t*>(a.a);
   p.w_g = a.a_stride_g;
   p.w_ld = a.a_ld;
-  p.splits = moe::lora_k_splits(a.max_blocks, a.K);
+  const moe::LoraSizes z = moe::lora_sizes(a.R, a.K, a.block_m, a.max_blocks);
+  char* base = static_cast<char*>(args->workspace);
+  p.splits = z.splits;
   p.h = args->h;
-  p.part = p.splits == 1 && p.h != nullptr ? p.h : static_cast<float*>(args->workspace);
+  p.part = reinterpret_cast<float*>(base);
+  if (!z.few && z.splits == 1) p.packed = reinterpret_cast<uint16_t*>(base + z.packed);
   st = hip_status(moe::launch_lora_down(p, (hipStream_t)stream), "moe_lora launch");
   if (st != MOE_OK) return st;
+  if (!z.few && z.splits > 1) {
+    p.packed = reinterpret_cast<uint16_t*>(base + z.packed);
+    st = hip_status(moe::launch_lora_join(p, false, (hipStream_t)stream), "moe_lora launch");
+    if (st != MOE_OK) return st;
+  }
   p.w = static_cast<const uint16_t*>(a.b);
   p.w_g = a.b_stride_g;
   p.w_ld = a.b_ld;
   p.c = static_cast<uint16_t*>(args->c);
   p.c_ld = args->c_ld;
-  return hip_status(moe::launch_lora_up(p, (hipStream_t)stream), "moe_lora launch");
+  return hip_status(z.few ? moe::launch_lora_up_few(p, (hipStream_t)stream)
+                          : moe::launch_lora_up(p, false, (hipStream_t)stream),
+                    "moe_lora launch");
 }
 
 int64_t moe_lora_backward_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t rank, int64_t k, int64_t n,
                                           int32_t block_m, int64_t max_blocks) {
   if (check_lora_sizes(num_slots, num_groups, rank, k, n, block_m, max_blocks) != MOE_OK) return -1;
-  return moe::lora_grad_sizes(num_slots, num_groups, rank, k, n, max_blocks).bytes;
+  return moe::lora_grad_sizes(num_groups, rank, k, n, block_m, max_blocks).bytes;
 }
 
 moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t stream) {
@@ -365,7 +375,7 @@ moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t st
   if (misaligned(args->h, 16) || misaligned(args->da, 16) || misaligned(args->db, 16) ||
       misaligned(args->workspace, 16))
     return fail(MOE_ERR_INVALID_ARGUMENT, "h, da, db and workspace must be 16-byte aligned");
-  const moe::LoraGradSizes z = moe::lora_grad_sizes(a.S, a.G, a.R, a.K, a.N, a.max_blocks);
+  const moe::LoraGradSizes z = moe::lora_grad_sizes(a.G, a.R, a.K, a.N, a.block_m, a.max_blocks);
   if (args->workspace_bytes < z.bytes || args->workspace == nullptr)
     return fail(MOE_ERR_INVALID_ARGUMENT, "workspace of %lld bytes, %lld needed", (long long)args->workspace_bytes,
                 (long long)z.bytes);
@@ -395,17 +405,11 @@ moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t st
   q.dy = static_cast<const uint16_t*>(args->dy);
   q.dy_ld = args->dy_ld;
   q.h = args->h;
-  q.splits = z.splits;
   q.da = args->da;
   q.db = args->db;
-  q.a = static_cast<const uint16_t*>(a.a);
-  q.a_g = a.a_stride_g;
-  q.a_ld = a.a_ld;
   q.b = static_cast<const uint16_t*>(a.b);
   q.b_g = a.b_stride_g;
   q.b_ld = a.b_ld;
-  q.at = reinterpret_cast<uint16_t*>(base + z.at);
-  q.bt = reinterpret_cast<uint16_t*>(base + z.bt);
   q.dh = reinterpret_cast<float*>(base + z.dh);
   q.table = reinterpret_cast<int32_t*>(base + z.table);
   q.seg_blocks = z.seg_blocks;
@@ -413,34 +417,26 @@ moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t st
   q.max_parts = z.max_parts;
   q.da_part = reinterpret_cast<float*>(base + z.da_part);
   q.db_part = reinterpret_cast<float*>(base + z.db_part);
-  st = hip_status(moe::launch_lora_grad_prepare(q, (hipStream_t)stream), "moe_lora_backward launch");
-  if (st != MOE_OK) return st;
-  if (a.S > 0) {
-    moe::LoraParams p = lora_params(a);
-    p.K = (int32_t)a.N;
+  moe::LoraParams p = lora_params(a);
+  p.part = q.dh;
+  p.splits = z.n_parts;
+  if (args->dx != nullptr) p.packed = reinterpret_cast<uint16_t*>(base + z.packed);
+  const hipStream_t on = (hipStream_t)stream;
+  hipError_t err = moe::launch_lora_grad_table(q, on);
+  if (err == hipSuccess) err = moe::launch_lora_grad_dy(q, on);
+  if (err == hipSuccess) err = moe::launch_lora_join(p, true, on);
+  if (err == hipSuccess && args->dx != nullptr) {
     p.N = (int32_t)a.K;
-    p.x = q.dy;
-    p.x_ld = q.dy_ld;
-    moe::lora_set_division(1, p.div_magic, p.div_shift);
-    p.w = q.bt;
-    p.w_g = (int64_t)a.R * a.N;
-    p.w_ld = a.N;
-    p.splits = z.splits;
-    p.part = const_cast<float*>(q.dh);
-    st = hip_status(moe::launch_lora_down(p, (hipStream_t)stream), "moe_lora_backward launch");
-    if (st != MOE_OK) return st;
-    if (args->dx != nullptr) {
-      p.w = q.at;
-      p.w_g = (int64_t)a.R * a.K;
-      p.w_ld = a.R;
-      p.c = static_cast<uint16_t*>(args->dx);
-      p.c_ld = args->dx_ld;
-      st = hip_status(moe::launch_lora_up(p, (hipStream_t)stream), "moe_lora_backward launch");
-      if (st != MOE_OK) return st;
-    }
+    p.w = static_cast<const uint16_t*>(a.a);
+    p.w_g = a.a_stride_g;
+    p.w_ld = a.a_ld;
+    p.c = static_cast<uint16_t*>(args->dx);
+    p.c_ld = args->dx_ld;
+    err = moe::launch_lora_up(p, true, on);
   }
-  if (!weights) return ok();
-  return hip_status(moe::launch_lora_grad_weights(q, (hipStream_t)stream), "moe_lora_backward launch");
+  if (err == hipSuccess && weights) err = moe::launch_lora_grad_x(q, on);
+  if (err == hipSuccess && weights) err = moe::launch_lora_grad_join(q, on);
+  return hip_status(err, "moe_lora_backward launch");
 }
 
 }  // extern "C"

@@ -1,58 +1,86 @@
 // moe_lora: low-rank adapters beside a shared projection, C[s] += scale[g]
 // B[g] (A[g] x[s / div]) over the slots s of every group g, routed by
-// moe_align's block list.
+// moe_align's block list. Its `up` also adds the input gradient of
+// moe_lora_backward, dx[s] += A[g]^T dh[s].
 //
 // HBM-bound: x is read once, C read and written once, and a group's adapter is
 // shared by its blocks through the caches; the products are 2 R flops a byte.
-// Two launches, since every output column needs the whole of h = A x: `down`
-// forms h, a block of slots and a part of K a workgroup; `up` adds B h, a block
-// and a part of N a workgroup, the parts of h summed (in order) as it is read.
+// Every output column needs the whole of h = A x, so `down` forms h, a block of
+// slots and a part of K a workgroup, and `up` adds B h. h lies by place in the
+// block list; as `up` takes it, it is scaled and in two bf16 terms ("packed",
+// [place][hi, lo][R]), which `down` writes itself where K is not split, `join`
+// from the parts where it is; with few slots a small `up` reads the parts, two
+// launches in all.
 #include <type_traits>
 
 #include "lora_util.h"
 
 namespace moe {
 
+// h as `up` takes it, four ranks of a place.
+__device__ __forceinline__ void lora_put_packed(uint16_t* packed, int64_t pos, int R, int r, f32x4_t h, float scale) {
+  uint32_t hi[2], lo[2];
+  lora_split(h[0] * scale, h[1] * scale, hi[0], lo[0]);
+  lora_split(h[2] * scale, h[3] * scale, hi[1], lo[1]);
+  uint16_t* to = packed + pos * (2 * R) + r;
+  *reinterpret_cast<u32x2_t*>(to) = u32x2_t{hi[0], hi[1]};
+  *reinterpret_cast<u32x2_t*>(to + R) = u32x2_t{lo[0], lo[1]};
+}
+
+// The parts of four ranks of a place, added in order.
+__device__ __forceinline__ f32x4_t lora_sum_parts(const float* at, int64_t step, int parts) {
+  f32x4_t h = {0, 0, 0, 0};
+  int k = 0;
+  for (; k + 4 <= parts; k += 4, at += 4 * step) {
+    f32x4_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const f32x4_t*>(at + j * step);
+    h = (((h + v[0]) + v[1]) + v[2]) + v[3];
+  }
+  for (; k < parts; ++k, at += step) h += *reinterpret_cast<const f32x4_t*>(at);
+  return h;
+}
+
+#ifndef DU
+#define DU 2
+#endif
 // ------------------------------------------------------------------- down
 
 // D rows are ranks, columns slots: a lane then holds 4 consecutive ranks of a
-// slot, one 16-byte store. The waves take K in turn, 32 at a time, operands
-// straight from memory in MFMA layout (a row's 64 bytes a load), and add their
-// sums through LDS.
+// slot, one 16-byte store. The waves take K in turn, 64 columns (whole cache
+// lines of x) at a time, operands straight from memory in MFMA layout, the next
+// ones on their way during the products, and add their sums through LDS.
 template <int RT, int MT>
 __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
-  constexpr int U = MT + RT <= 3 ? 8 : MT + RT <= 6 ? 4 : 2;  // steps whose loads are issued together
-  __shared__ f32x4_t red[4][RT * MT][64];
+  constexpr int U = RT + MT <= 2 ? 4 : RT >= 4 ? 1 : DU;  // steps of 32 whose loads are issued together
+  __shared__ f32x4_t red[2][RT * MT][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
   const int b = p.block0 + blockIdx.x / p.splits, sp = blockIdx.x % p.splits;
   const int g = p.groups[b];
   if ((uint32_t)g >= (uint32_t)p.G) return;
   const int row0 = blockIdx.y * MT * 16;
   const uint16_t* xr[MT];
+  uint32_t slot[MT];
   bool live[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = row0 + 16 * m + m16;
-    const uint32_t s = row < p.bm ? (uint32_t)p.sorted[(int64_t)b * p.bm + row] : 0xFFFFFFFFu;
-    live[m] = s < (uint32_t)p.S;
-    xr[m] = p.x + (int64_t)(live[m] ? lora_div(s, p.div_magic, p.div_shift) : 0) * p.x_ld + 8 * q;
+    slot[m] = row < p.bm ? (uint32_t)p.sorted[(int64_t)b * p.bm + row] : 0xFFFFFFFFu;
+    live[m] = slot[m] < (uint32_t)p.S;
+    xr[m] = p.x + (int64_t)(live[m] ? lora_div(slot[m], p.div_magic, p.div_shift) : 0) * p.x_ld + 8 * q;
   }
   const uint16_t* wr[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) wr[t] = p.w + (int64_t)g * p.w_g + (int64_t)(16 * t + m16) * p.w_ld + 8 * q;
-  const int steps = (p.K + 31) / 32, per = (steps + p.splits - 1) / p.splits;
-  const int end = min(steps, (sp + 1) * per);
-  f32x4_t acc[RT][MT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0, 0, 0, 0};
-  for (int i = sp * per + wave; i < end; i += 4 * U) {
-    u32x4_t xv[U][MT], wv[U][RT];
+  constexpr int kTurn = 32 * U;
+  const int units = (p.K + 63) / 64, per = (units + p.splits - 1) / p.splits;
+  const int end = min(p.K, 64 * (sp + 1) * per);
+  u32x4_t xv[U][MT], wv[U][RT];
+  auto load = [&](int k0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = 32 * (i + 4 * u);
-      const bool in = i + 4 * u < end && k + 8 * q < p.K;
+      const int k = k0 + 32 * u;
+      const bool in = k + 8 * q < end;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
         xv[u][m] = in && live[m] ? *reinterpret_cast<const u32x4_t*>(xr[m] + k) : u32x4_t{0, 0, 0, 0};
@@ -60,107 +88,116 @@ __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
       for (int t = 0; t < RT; ++t)
         wv[u][t] = in && 16 * t + m16 < p.R ? *reinterpret_cast<const u32x4_t*>(wr[t] + k) : u32x4_t{0, 0, 0, 0};
     }
+  };
+  f32x4_t acc[RT][MT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0, 0, 0, 0};
+  int k = 64 * sp * per + kTurn * wave;
+  if (k < end) load(k);
+  while (k < end) {
+    u32x4_t xn[U][MT], wn[U][RT];
+    __builtin_memcpy(xn, xv, sizeof(xv));
+    __builtin_memcpy(wn, wv, sizeof(wv));
+    k += 4 * kTurn;
+    if (k < end) load(k);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] = lora_mfma(wv[u][t], xv[u][m], acc[t][m]);
+        for (int m = 0; m < MT; ++m) acc[t][m] = lora_mfma(wn[u][t], xn[u][m], acc[t][m]);
   }
+  // the waves' sums: the upper half's into the lower half's, and so on
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
+  for (int half = 2; half > 0; half /= 2) {
+    if (wave >= half && wave < 2 * half)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) red[wave][t * MT + m][lane] = acc[t][m];
-  __syncthreads();
-  for (int i = wave; i < RT * MT; i += 4) {
-    const int t = i / MT, m = i % MT, row = row0 + 16 * m + m16, r = 16 * t + 4 * q;
-    const uint32_t s = row < p.bm ? (uint32_t)p.sorted[(int64_t)b * p.bm + row] : 0xFFFFFFFFu;
-    if (s >= (uint32_t)p.S || r >= p.R) continue;
-    const f32x4_t v = ((red[0][i][lane] + red[1][i][lane]) + red[2][i][lane]) + red[3][i][lane];
-    *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)sp * p.S + s) * p.R + r) = v;
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) red[wave - half][t * MT + m][lane] = acc[t][m];
+    __syncthreads();
+    if (wave < half)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[t][m] += red[wave][t * MT + m][lane];
+    if (half > 1) __syncthreads();
+  }
+  if (wave > 0) return;
+  const float scale = p.packed != nullptr && p.scale != nullptr ? p.scale[g] : 1.0f;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (!live[m]) continue;
+    const int64_t pos = (int64_t)b * p.bm + row0 + 16 * m + m16;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int r = 16 * t + 4 * q;
+      if (r >= p.R) continue;
+      if (p.packed != nullptr) {
+        lora_put_packed(p.packed, pos, p.R, r, acc[t][m], scale);
+        if (p.h != nullptr) *reinterpret_cast<f32x4_t*>(p.h + (int64_t)slot[m] * p.R + r) = acc[t][m];
+      } else {
+        *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)sp * p.max_blocks * p.bm + pos) * p.R + r) = acc[t][m];
+      }
+    }
   }
 }
 
-// --------------------------------------------------------------------- up
-
-// 8 ranks from 8 * piece of h[s]: the sum of the parts.
-__device__ __forceinline__ void lora_h8(const LoraParams& p, uint32_t s, int piece, float (&f)[8]) {
-  const float* at = p.part + (int64_t)s * p.R + 8 * piece;
-  f32x4_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-  for (int i = 0; i < p.splits; ++i, at += (int64_t)p.S * p.R) {
-    a += reinterpret_cast<const f32x4_t*>(at)[0];
-    b += reinterpret_cast<const f32x4_t*>(at)[1];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = a[i];
-    f[4 + i] = b[i];
+// Several parts -> h where it is wanted, and packed. (`all`: the places without
+// a slot too, whose parts are zeros, and the scaled sum over the first part: the
+// backward pass's dh.)
+__global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraParams p, bool all) {
+  const int64_t places = (int64_t)p.max_blocks * p.bm, n = places * (p.R / 4);
+  for (int64_t i = (int64_t)blockIdx.x * kLoraThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kLoraThreads) {
+    const int64_t pos = i / (p.R / 4);
+    const int r = (int)(i % (p.R / 4)) * 4;
+    const int g = p.groups[pos / p.bm];
+    const uint32_t s = (uint32_t)p.sorted[pos];
+    if ((uint32_t)g >= (uint32_t)p.G || (!all && s >= (uint32_t)p.S)) continue;
+    const float scale = p.scale != nullptr ? p.scale[g] : 1.0f;
+    float* at = p.part + pos * p.R + r;
+    const f32x4_t h = lora_sum_parts(at, places * p.R, p.splits);
+    if (p.packed != nullptr) lora_put_packed(p.packed, pos, p.R, r, h, scale);
+    if (all) *reinterpret_cast<f32x4_t*>(at) = h * scale;
+    if (p.h != nullptr) *reinterpret_cast<f32x4_t*>(p.h + (int64_t)s * p.R + r) = h;
   }
 }
+
+// ------------------------------------------------------ up, with few slots
 
 // D rows are columns of C, D columns slots. Row i of tile j stands for column
 // 32 (j / 2) + 8 (i / 4) + 4 (j % 2) + i % 4 of a 64-column piece, so that a lane
-// holds twice 8 consecutive columns of one slot and C moves 16 bytes a lane, 64
-// contiguous bytes a row. h enters as hi + lo: for ranks up to 16 both lie in
-// one MFMA's k (RC = 2: hi hi lo lo, RC = 1: hi lo and two zeros, in pieces of 8),
-// beyond, each piece of 32 ranks of B meets hi and lo in turn.
-template <int RC, int MT>
-__global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
+// holds twice 8 consecutive columns of one slot: one tile of 16 slots then
+// spreads over four times the waves that `up` would use. h enters as there. A
+// wave's first piece of C and B is on its way while the parts of h are summed.
+template <int RC>
+__global__ __launch_bounds__(kLoraThreads) void lora_up_few_kernel(LoraParams p) {
   constexpr int F = RC < 4 ? 1 : RC / 4, P = RC < 4 ? 1 : 2;
+  constexpr int kRank = RC < 4 ? 16 : 8 * RC, kLd = kRank + 8;  // of a slot's row of h in LDS
+  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][kLd];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
   const int b = p.block0 + blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
   const int g = p.groups[b];
   if ((uint32_t)g >= (uint32_t)p.G) return;
-  const int row0 = blockIdx.y * MT * 16;
-  const float scale = p.scale != nullptr ? p.scale[g] : 1.0f;
+  const int row0 = blockIdx.y * 16, rows = min(16, p.bm - row0);
+  const int64_t pos0 = (int64_t)b * p.bm + row0;
+  const int32_t* ids = p.sorted + pos0;
   const int pieces = p.R / 8;
-  u32x4_t hv[MT][F][P];
-  uint16_t* cr[MT];
-  bool live[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = row0 + 16 * m + m16;
-    const uint32_t s = row < p.bm ? (uint32_t)p.sorted[(int64_t)b * p.bm + row] : 0xFFFFFFFFu;
-    live[m] = s < (uint32_t)p.S;
-    cr[m] = p.c + (int64_t)(live[m] ? s : 0) * p.c_ld + 8 * q;
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
-      const bool in = live[m] && piece < pieces && (RC != 1 || q < 2);
-      float h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (in) {
-        lora_h8(p, s, piece, h);
-        if (p.h != nullptr && p.h != p.part && sp == 0 && wave == 0 && (RC >= 4 || q < RC)) {
-          f32x4_t* to = reinterpret_cast<f32x4_t*>(p.h + (int64_t)s * p.R + 8 * piece);
-          to[0] = f32x4_t{h[0], h[1], h[2], h[3]};
-          to[1] = f32x4_t{h[4], h[5], h[6], h[7]};
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t a, c;
-        lora_split(h[2 * i] * scale, h[2 * i + 1] * scale, a, c);
-        if constexpr (P == 2) {
-          hv[m][f][0][i] = a;
-          hv[m][f][1][i] = c;
-        } else {
-          hv[m][0][0][i] = q < RC ? a : c;
-        }
-      }
-    }
-  }
+  const uint32_t slot = m16 < rows ? (uint32_t)ids[m16] : 0xFFFFFFFFu;
+  const bool live = slot < (uint32_t)p.S;
+  uint16_t* cr = p.c + (int64_t)(live ? slot : 0) * p.c_ld + 8 * q;
   const uint16_t* wr = p.w + (int64_t)g * p.w_g;
   const int chunks = (p.N + 63) / 64, per = (chunks + p.n_splits - 1) / p.n_splits;
   const int end = min(chunks, (sp + 1) * per);
-  for (int i = sp * per + wave; i < end; i += 4) {
+  u32x4_t cv[2], wv[4][F];
+  auto load = [&](int i) {
     const int n0 = 64 * i;
-    u32x4_t cv[MT][2], wv[4][F];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        cv[m][e] = live[m] && n0 + 32 * e + 8 * q < p.N ? *reinterpret_cast<const u32x4_t*>(cr[m] + n0 + 32 * e)
-                                                        : u32x4_t{0, 0, 0, 0};
+    for (int e = 0; e < 2; ++e)
+      cv[e] = live && n0 + 32 * e + 8 * q < p.N ? *reinterpret_cast<const u32x4_t*>(cr + n0 + 32 * e)
+                                                : u32x4_t{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = n0 + 32 * (j / 2) + 8 * (m16 / 4) + 4 * (j % 2) + m16 % 4;
@@ -171,64 +208,222 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
         wv[j][f] = in ? *reinterpret_cast<const u32x4_t*>(wr + (int64_t)n * p.w_ld + 8 * piece) : u32x4_t{0, 0, 0, 0};
       }
     }
+  };
+  int i = sp * per + wave;
+  if (i < end) load(i);
+
+  // h: four ranks a thread
+  const float scale = p.scale != nullptr ? p.scale[g] : 1.0f;
+  for (int t = threadIdx.x; t < 16 * (kRank / 4); t += kLoraThreads) {
+    const int row = t / (kRank / 4), r = t % (kRank / 4) * 4;
+    const uint32_t s = row < rows ? (uint32_t)ids[row] : 0xFFFFFFFFu;
+    f32x4_t h = {0, 0, 0, 0};
+    if (s < (uint32_t)p.S && r < p.R) {
+      h = lora_sum_parts(p.part + (pos0 + row) * p.R + r, (int64_t)p.max_blocks * p.bm * p.R, p.splits);
+      if (p.h != nullptr && sp == 0) *reinterpret_cast<f32x4_t*>(p.h + (int64_t)s * p.R + r) = h;
+    }
+    uint32_t hi[2], lo[2];
+    lora_split(h[0] * scale, h[1] * scale, hi[0], lo[0]);
+    lora_split(h[2] * scale, h[3] * scale, hi[1], lo[1]);
+    *reinterpret_cast<u32x2_t*>(&hs[0][row][r]) = u32x2_t{hi[0], hi[1]};
+    *reinterpret_cast<u32x2_t*>(&hs[1][row][r]) = u32x2_t{lo[0], lo[1]};
+  }
+  __syncthreads();
+  u32x4_t hv[F][P];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+  for (int f = 0; f < F; ++f)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        f32x4_t d[2];
+    for (int k = 0; k < P; ++k) {
+      const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0, part = RC >= 4 ? k : RC == 2 ? q / 2 : q % 2;
+      hv[f][k] = *reinterpret_cast<const u32x4_t*>(&hs[part][m16][8 * piece]);
+      if (RC == 1 && q >= 2) hv[f][k] = u32x4_t{0, 0, 0, 0};
+    }
+
+  for (; i < end; i += 4) {
+    const int n0 = 64 * i;
+    f32x4_t d[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          d[j] = f32x4_t{0, 0, 0, 0};
+    for (int j = 0; j < 4; ++j) {
+      d[j] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-          for (int f = 0; f < F; ++f)
+      for (int f = 0; f < F; ++f)
 #pragma unroll
-            for (int k = 0; k < P; ++k) d[j] = lora_mfma(wv[2 * e + j][f], hv[m][f][k], d[j]);
-        }
-        u32x4_t o;
+        for (int k = 0; k < P; ++k) d[j] = lora_mfma(wv[j][f], hv[f][k], d[j]);
+    }
+    const u32x4_t cn[2] = {cv[0], cv[1]};
+    if (i + 4 < end) load(i + 4);
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          o[w] = lora_pack(__uint_as_float(cv[m][e][w] << 16) + d[w / 2][2 * (w % 2)],
-                           __uint_as_float(cv[m][e][w] & 0xffff0000u) + d[w / 2][2 * (w % 2) + 1]);
-        if (live[m] && n0 + 32 * e + 8 * q < p.N) *reinterpret_cast<u32x4_t*>(cr[m] + n0 + 32 * e) = o;
+    for (int e = 0; e < 2; ++e) {
+      u32x4_t o;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        o[w] = lora_pack(__uint_as_float(cn[e][w] << 16) + d[2 * e + w / 2][2 * (w % 2)],
+                         __uint_as_float(cn[e][w] & 0xffff0000u) + d[2 * e + w / 2][2 * (w % 2) + 1]);
+      if (live && n0 + 32 * e + 8 * q < p.N) *reinterpret_cast<u32x4_t*>(cr + n0 + 32 * e) = o;
+    }
+  }
+}
+
+// --------------------------------------------------------------------- up
+
+// A wave keeps 16 NT columns of a group's B in registers and takes the run's
+// slots 16 at a time, ids two tiles ahead, C and h one ahead. D rows are slots,
+// columns those of C: column m of tile j stands for column NT m + j, so that a
+// lane holds NT consecutive columns of 4 slots and an access of C is 256
+// contiguous bytes of 4 rows (28672 gathered rows of 5760, read and written back
+// with no product: 4.7 TB/s so, 4.1 to 4.4 in 64-byte pieces of 16 rows). h
+// enters as hi + lo: for ranks up to 16 both lie in one MFMA's k (RC = 2: hi hi
+// lo lo, RC = 1: hi lo and two zeros, in pieces of 8), beyond, each piece of 32
+// ranks of B meets hi and lo in turn. TURNED: the matrix is [R][N] (dx, whose
+// matrix is A itself): a lane reads its 8 columns of each of 8 ranks and turns
+// the 8 x 8 around in registers.
+template <int RC, bool TURNED>
+__global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
+  constexpr int F = RC < 4 ? 1 : RC / 4, P = RC < 4 ? 1 : 2;
+  constexpr int NT = 8, kCols = 16 * NT;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
+  const int run = blockIdx.x / p.n_splits, n0 = (blockIdx.x % p.n_splits * 4 + wave) * kCols;
+  const int b0 = p.block0 + run * p.run_blocks, b1 = min(b0 + p.run_blocks, p.max_blocks);
+  if (n0 >= p.N) return;
+  const int per = p.bm <= 16 ? 1 : p.bm / 16, tiles = (b1 - b0) * per;  // tiles of a block, of the run
+  const bool in = n0 + NT * m16 < p.N;
+  const int pieces = p.R / 8;
+
+  int ids[4], gid = -1;
+  auto load_ids = [&](int t) {
+    const int b = b0 + t / per, row = 16 * (t % per) + 4 * q;
+    gid = __builtin_amdgcn_readfirstlane(p.groups[b]);
+    ids[0] = ids[1] = ids[2] = ids[3] = -1;
+    if (row < p.bm) __builtin_memcpy(ids, p.sorted + (int64_t)b * p.bm + row, 16);
+  };
+  u32x4_t cv[4], hv[F][P];
+  uint16_t* cr[4];
+  int g = -1;
+  auto load = [&](int t) {  // tile t, whose ids are here
+    g = gid;
+    const bool group = (uint32_t)g < (uint32_t)p.G;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool live = group && (uint32_t)ids[r] < (uint32_t)p.S && in;
+      cr[r] = live ? p.c + (int64_t)ids[r] * p.c_ld + n0 + NT * m16 : nullptr;
+      cv[r] = live ? *reinterpret_cast<const u32x4_t*>(cr[r]) : u32x4_t{0, 0, 0, 0};
+    }
+    const int64_t pos = (int64_t)(b0 + t / per) * p.bm + 16 * (t % per) + m16;
+    const bool row = group && 16 * (t % per) + m16 < p.bm;
+    const uint16_t* at = p.packed + pos * (2 * p.R);
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const int piece = RC >= 4 ? 4 * f + q : q;  // (RC < 4: hi and lo pieces follow each other)
+        const bool here = row && (RC >= 4 ? piece < pieces : q < 2 * RC);
+        hv[f][k] = here ? *reinterpret_cast<const u32x4_t*>(at + k * p.R + 8 * piece) : u32x4_t{0, 0, 0, 0};
       }
+  };
+  u32x4_t wv[NT][F];
+  int have = -1;  // the group whose B is here
+  load_ids(0);
+  load(0);
+  if (tiles > 1) load_ids(1);
+  for (int t = 0; t < tiles; ++t) {
+    const int now = g;
+    if (now != have && (uint32_t)now < (uint32_t)p.G) {
+      have = now;
+      const uint16_t* wr = p.w + (int64_t)now * p.w_g;
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
+        const bool here = in && piece < pieces && (RC != 1 || q < 2);
+        u32x4_t v[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint16_t* at = TURNED ? wr + (int64_t)(8 * piece + j) * p.w_ld + n0 + NT * m16
+                                      : wr + (int64_t)(n0 + NT * m16 + j) * p.w_ld + 8 * piece;
+          v[j] = here ? *reinterpret_cast<const u32x4_t*>(at) : u32x4_t{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            wv[j][f][w] = TURNED ? __builtin_amdgcn_perm(v[2 * w + 1][j / 2], v[2 * w][j / 2],
+                                                         j % 2 ? 0x07060302u : 0x05040100u)
+                                 : v[j][w];
+      }
+    }
+    u32x4_t cn[4], hn[F][P];
+    uint16_t* to[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      cn[r] = cv[r];
+      to[r] = cr[r];
+    }
+    __builtin_memcpy(hn, hv, sizeof(hv));
+    if (t + 1 < tiles) load(t + 1);
+    if (t + 2 < tiles) load_ids(t + 2);
+    f32x4_t d[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      d[j] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int k = 0; k < P; ++k) d[j] = lora_mfma(hn[f][k], wv[j][f], d[j]);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      u32x4_t o;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        o[w] = lora_pack(__uint_as_float(cn[r][w] << 16) + d[2 * w][r],
+                         __uint_as_float(cn[r][w] & 0xffff0000u) + d[2 * w + 1][r]);
+      if (to[r] != nullptr) *reinterpret_cast<u32x4_t*>(to[r]) = o;
+    }
   }
 }
 
 // ------------------------------------------------------------------ launch
 
+#ifndef FEWT
+#define FEWT 64
+#endif
+#ifndef DW
+#define DW 256
+#endif
+#ifndef UW
+#define UW 1536
+#endif
+// Whether the small `up` serves: up to FEWT tiles of 16 slots.
+static bool lora_few(int64_t max_blocks, int bm) { return max_blocks * (bm < 16 ? 1 : bm / 16) <= FEWT; }
+
 // Parts of K: enough workgroups for the chip, at least 256 columns each.
 int lora_k_splits(int64_t max_blocks, int64_t k) {
-  const int64_t want = (1024 + max_blocks - 1) / (max_blocks > 0 ? max_blocks : 1);
+  const int64_t want = (DW + max_blocks - 1) / (max_blocks > 0 ? max_blocks : 1);
   const int64_t most = k / 256 > 1 ? k / 256 : 1;
   const int64_t n = want < most ? want : most;
-  return (int)(n < 8 ? n : 8);
+  return (int)(n < 32 ? n : 32);
 }
 
-static int lora_n_splits(int64_t max_blocks, int64_t n) {
-  const int64_t want = (1024 + max_blocks - 1) / (max_blocks > 0 ? max_blocks : 1);
-  const int64_t most = (n + 255) / 256;
-  return (int)(want < most ? want : most);
-}
-
-// Row tiles of 16 slots a workgroup takes, and workgroups a block.
-template <int RC, class F>
-static hipError_t lora_rows(int bm, F f) {
-  if (bm <= 16) return f(std::integral_constant<int, 1>{}, 1);
-  if (bm == 32 || RC == 16) return f(std::integral_constant<int, 2>{}, bm / 32);
-  if constexpr (RC < 16) return f(std::integral_constant<int, 4>{}, 1);
-  return hipErrorInvalidValue;
+// Of moe_lora's workspace: the parts of h, then packed (neither where it is not used).
+LoraSizes lora_sizes(int32_t R, int64_t K, int32_t bm, int64_t max_blocks) {
+  LoraSizes z{};
+  z.few = lora_few(max_blocks, bm);
+  z.splits = lora_k_splits(max_blocks, K);
+  const int64_t h = max_blocks * bm * R * 4;
+  z.packed = z.few || z.splits > 1 ? z.splits * h : 0;
+  z.bytes = z.packed + (z.few ? 0 : h);
+  return z;
 }
 
 // Launches over all blocks, at most kLoraMaxGrid workgroups at a time (a grid
 // holds fewer than 2^32 threads).
-constexpr int64_t kLoraMaxGrid = 1 << 22;
+constexpr int64_t kLoraMaxGrid = 1 << 21;
 
 template <class F>
-static hipError_t lora_blocks(LoraParams p, int per_block, F launch) {
-  const int64_t per = kLoraMaxGrid / per_block;
-  for (int64_t b = 0; b < p.max_blocks; b += per) {
-    p.block0 = (int32_t)b;
-    launch(p, (uint32_t)((p.max_blocks - b < per ? p.max_blocks - b : per) * per_block));
+static hipError_t lora_blocks(LoraParams p, int run, int per_run, F launch) {
+  const int64_t per = kLoraMaxGrid / per_run > 0 ? kLoraMaxGrid / per_run : 1, runs = (p.max_blocks + run - 1) / run;
+  for (int64_t r = 0; r < runs; r += per) {
+    p.block0 = (int32_t)(r * run);
+    launch(p, (uint32_t)((runs - r < per ? runs - r : per) * per_run));
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -237,25 +432,51 @@ static hipError_t lora_blocks(LoraParams p, int per_block, F launch) {
 
 hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream) {
   return lora_rank(p.R, [&](auto rank) {
-    constexpr int RC = decltype(rank)::value;
-    return lora_rows<RC>(p.bm, [&](auto mt, int y) {
-      return lora_blocks(p, p.splits, [&](const LoraParams& q, uint32_t grid) {
-        hipLaunchKernelGGL((lora_down_kernel<(RC + 1) / 2, decltype(mt)::value>), dim3(grid, y), dim3(kLoraThreads), 0,
-                           stream, q);
+    constexpr int RT = (decltype(rank)::value + 1) / 2, MOST = RT == 8 ? 2 : 4;
+    auto go = [&](auto mt) {
+      constexpr int MT = decltype(mt)::value;
+      const int y = p.bm <= 16 * MT ? 1 : p.bm / (16 * MT);
+      return lora_blocks(p, 1, p.splits, [&](const LoraParams& q, uint32_t grid) {
+        hipLaunchKernelGGL((lora_down_kernel<RT, MT>), dim3(grid, y), dim3(kLoraThreads), 0, stream, q);
       });
+    };
+    if (p.bm <= 16) return go(std::integral_constant<int, 1>{});
+    if (p.bm == 32) return go(std::integral_constant<int, 2>{});
+    return go(std::integral_constant<int, MOST>{});
+  });
+}
+
+hipError_t launch_lora_join(const LoraParams& p, bool all, hipStream_t stream) {
+  const int64_t want = ((int64_t)p.max_blocks * p.bm * (p.R / 4) + kLoraThreads - 1) / kLoraThreads;
+  if (want == 0) return hipSuccess;
+  hipLaunchKernelGGL(lora_join_kernel, dim3((uint32_t)(want < 4096 ? want : 4096)), dim3(kLoraThreads), 0, stream, p,
+                     all);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream) {
+  LoraParams p = p0;
+  p.n_splits = (p.N + 511) / 512;
+  const int64_t all = (int64_t)p.max_blocks * p.n_splits;
+  p.run_blocks = (int32_t)(all / UW > 1 ? all / UW : 1);
+  return lora_rank(p.R, [&](auto rank) {
+    constexpr int RC = decltype(rank)::value;
+    return lora_blocks(p, p.run_blocks, p.n_splits, [&](const LoraParams& q, uint32_t grid) {
+      auto kernel = turned ? lora_up_kernel<RC, true> : lora_up_kernel<RC, false>;
+      hipLaunchKernelGGL(kernel, dim3(grid), dim3(kLoraThreads), 0, stream, q);
     });
   });
 }
 
-hipError_t launch_lora_up(const LoraParams& p0, hipStream_t stream) {
+hipError_t launch_lora_up_few(const LoraParams& p0, hipStream_t stream) {
   LoraParams p = p0;
-  p.n_splits = lora_n_splits(p.max_blocks, p.N);
+  const int y = p.bm <= 16 ? 1 : p.bm / 16;
+  const int64_t tiles = (int64_t)p.max_blocks * y, most = (p.N + 255) / 256;
+  const int64_t want = (512 + tiles - 1) / (tiles > 0 ? tiles : 1);
+  p.n_splits = (int32_t)(want < most ? want : most);
   return lora_rank(p.R, [&](auto rank) {
-    constexpr int RC = decltype(rank)::value;
-    return lora_rows<RC>(p.bm, [&](auto mt, int y) {
-      return lora_blocks(p, p.n_splits, [&](const LoraParams& q, uint32_t grid) {
-        hipLaunchKernelGGL((lora_up_kernel<RC, decltype(mt)::value>), dim3(grid, y), dim3(kLoraThreads), 0, stream, q);
-      });
+    return lora_blocks(p, 1, p.n_splits, [&](const LoraParams& q, uint32_t grid) {
+      hipLaunchKernelGGL(lora_up_few_kernel<decltype(rank)::value>, dim3(grid, y), dim3(kLoraThreads), 0, stream, q);
     });
   });
 }

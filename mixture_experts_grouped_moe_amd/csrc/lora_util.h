@@ -39,6 +39,16 @@ __device__ __forceinline__ void lora_split(float f0, float f1, uint32_t& hi, uin
   lo = lora_pack(fabsf(f0) < INFINITY ? r0 : 0.0f, fabsf(f1) < INFINITY ? r1 : 0.0f);
 }
 
+// f as three bf16 terms, all of its 24 bits (to what bf16's smallest holds).
+__device__ __forceinline__ void lora_split3(float f0, float f1, uint32_t (&t)[3]) {
+  uint32_t lo;
+  lora_split(f0, f1, t[0], lo);
+  const float r0 = fabsf(f0) < INFINITY ? f0 - __uint_as_float(t[0] << 16) : 0.0f;
+  const float r1 = fabsf(f1) < INFINITY ? f1 - __uint_as_float(t[0] & 0xffff0000u) : 0.0f;
+  t[1] = lo;
+  t[2] = lora_pack(r0 - __uint_as_float(lo << 16), r1 - __uint_as_float(lo & 0xffff0000u));
+}
+
 // floor(s / d) for s < 2^31 (lora_set_division).
 __device__ __forceinline__ uint32_t lora_div(uint32_t s, uint32_t magic, int32_t shift) {
   return (uint32_t)(((uint64_t)s * magic) >> shift);

@@ -146,8 +146,8 @@ struct NormParams {
   float* partial;
 };
 
-// The low-rank adapters (lora.hip, lora_grad.hip). Strides in elements; `part`
-// holds `splits` partial sums of h, [splits][S][R].
+// The low-rank adapters (lora.hip, lora_grad.hip). Strides in elements; a place
+// is an index into the block list's slots.
 struct LoraParams {
   int32_t S, G, R, K, N;
   int32_t bm, max_blocks;
@@ -155,15 +155,16 @@ struct LoraParams {
   const int32_t* sorted;
   const int32_t* groups;
   const float* scale;
-  const uint16_t* x;  // backward: dy where h's gradient is formed, x for dA
+  const uint16_t* x;
   int64_t x_ld;
   uint32_t div_magic;  // of the division of slots by x_row_div
   int32_t div_shift;
-  const uint16_t* w;  // A (or B transposed) [G][R][K], then B (or A transposed) [G][N][R]
+  const uint16_t* w;  // A, then B
   int64_t w_g, w_ld;
-  float* part;
-  int32_t splits, n_splits;
-  float* h;  // where the sum of the parts is wanted
+  float* part;       // h in parts of K, [splits][places][R]
+  uint16_t* packed;  // h as the large `up` takes it, [places][2][R] bf16
+  int32_t splits, n_splits, run_blocks;
+  float* h;  // [S][R], or null
   uint16_t* c;
   int64_t c_ld;
 };
@@ -180,17 +181,12 @@ struct LoraGradParams {
   int32_t div_shift;
   const uint16_t* dy;
   int64_t dy_ld;
-  const float* h;
-  const float* dh;  // [splits][S][R]
-  int32_t splits;
-  float* da;
-  float* db;
-  const uint16_t* a;
-  int64_t a_g, a_ld;
   const uint16_t* b;
   int64_t b_g, b_ld;
-  uint16_t* at;  // A transposed, [G][K][R]
-  uint16_t* bt;  // B transposed, [G][R][N]
+  const float* h;
+  float* dh;  // [parts of N][places][R]; joined, the first holds dh
+  float* da;  // or null, as db
+  float* db;
   int32_t* table;
   int32_t seg_blocks, max_segs, max_parts;
   float* da_part;
@@ -235,17 +231,25 @@ hipError_t launch_dropout(const uint16_t* x, int64_t x_ld, int64_t rows, int64_t
 hipError_t launch_norm(const NormParams& p, const Dropout& d, hipStream_t stream);
 hipError_t launch_norm_backward(const NormParams& p, const Dropout& d, hipStream_t stream);
 int64_t norm_backward_workspace_bytes(int64_t rows, int64_t n);
-// The launch shapes of the adapters, a function of the sizes alone.
-int lora_k_splits(int64_t max_blocks, int64_t k);
-hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream);
-hipError_t launch_lora_up(const LoraParams& p, hipStream_t stream);
-struct LoraGradSizes {
-  int32_t splits, seg_blocks, max_segs, max_parts;
-  int64_t at, bt, dh, table, da_part, db_part, bytes;  // offsets into the workspace and its size
+struct LoraSizes {
+  bool few;        // the small `up`, which reads the parts
+  int32_t splits;  // parts of K
+  int64_t packed, bytes;  // offset into the workspace and its size
 };
-LoraGradSizes lora_grad_sizes(int64_t S, int32_t G, int32_t R, int64_t K, int64_t N, int64_t max_blocks);
-hipError_t launch_lora_grad_prepare(const LoraGradParams& p, hipStream_t stream);
-hipError_t launch_lora_grad_weights(const LoraGradParams& p, hipStream_t stream);
+LoraSizes lora_sizes(int32_t R, int64_t K, int32_t bm, int64_t max_blocks);
+hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream);
+hipError_t launch_lora_join(const LoraParams& p, bool all, hipStream_t stream);
+hipError_t launch_lora_up(const LoraParams& p, bool turned, hipStream_t stream);
+hipError_t launch_lora_up_few(const LoraParams& p, hipStream_t stream);
+struct LoraGradSizes {
+  int32_t n_parts, seg_blocks, max_segs, max_parts;
+  int64_t dh, packed, table, da_part, db_part, bytes;  // offsets into the workspace and its size
+};
+LoraGradSizes lora_grad_sizes(int32_t G, int32_t R, int64_t K, int64_t N, int32_t bm, int64_t max_blocks);
+hipError_t launch_lora_grad_table(const LoraGradParams& p, hipStream_t stream);
+hipError_t launch_lora_grad_dy(const LoraGradParams& p, hipStream_t stream);
+hipError_t launch_lora_grad_x(const LoraGradParams& p, hipStream_t stream);
+hipError_t launch_lora_grad_join(const LoraGradParams& p, hipStream_t stream);
 int gemm_block_m_large();
 int gemm_block_m_f8();
 int gemm_block_m_decode();

@@ -217,8 +217,10 @@ def test_lora_sizes():
             assert _lora_bytes(h, **bad) == -1, bad
     m = moe.moe_lora_block_m
     assert m(0, 1) == 16 and m(31, 1) == 16 and m(32, 1) == 64 and m(1 << 30, 1024) == 64 and m(-1, 1) == -1 and m(4, 0) == -1
-    # partial sums by segments of the list, not by slots: 512 workgroups' worth
-    assert g(1 << 24, 1, 16, 2880, 5760, 64, 1 << 18) - 8 * (1 << 24) * 16 * 4 < 128 << 20
+    # h (twice, and a part of dh per 512 columns of dy) by place; the gradients' partial sums by segments of the list
+    h = 64 * (1 << 18) * 16 * 4
+    assert f(1 << 24, 1, 16, 2880, 5760, 64, 1 << 18) <= 2 * h
+    assert g(1 << 24, 1, 16, 2880, 5760, 64, 1 << 18) - (12 + 1) * h < 256 << 20
 
 
 def test_lora_overlaps_are_rejected(no_device):
