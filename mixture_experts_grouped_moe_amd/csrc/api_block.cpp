@@ -417,7 +417,9 @@ moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t st
   q.max_parts = z.max_parts;
   q.da_part = reinterpret_cast<float*>(base + z.da_part);
   q.db_part = reinterpret_cast<float*>(base + z.db_part);
+  if (a.S == 0) q.max_blocks = 0;  // (a list then names no slot)
   moe::LoraParams p = lora_params(a);
+  p.max_blocks = q.max_blocks;
   p.part = q.dh;
   p.splits = z.n_parts;
   if (args->dx != nullptr) p.packed = reinterpret_cast<uint16_t*>(base + z.packed);

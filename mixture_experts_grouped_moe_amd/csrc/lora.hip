@@ -47,67 +47,88 @@ __device__ __forceinline__ f32x4_t lora_sum_parts(const float* at, int64_t step,
 // ------------------------------------------------------------------- down
 
 // D rows are ranks, columns slots: a lane then holds 4 consecutive ranks of a
-// slot, one 16-byte store. The waves take K in turn, 64 columns (whole cache
-// lines of x) at a time, operands straight from memory in MFMA layout, the next
-// ones on their way during the products, and add their sums through LDS.
+// slot, one 16-byte store. The waves take K in turn, whole cache lines of x at a
+// time, operands straight from memory in MFMA layout, the next ones on their way
+// during the products, and add their sums through LDS. Loads are not masked: a
+// place without a slot reads the block's first row, a rank past R the last one,
+// and their rows and columns of D are not stored.
 template <int RT, int MT>
 __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
-  constexpr int U = RT + MT <= 2 ? 4 : RT >= 4 ? 1 : DU;  // steps of 32 whose loads are issued together
+  constexpr int U = RT + MT <= 2 ? 4 : RT >= 4 ? 1 : DU;  // steps of 32 columns of a turn
+  constexpr int kTurn = 32 * U;
   __shared__ f32x4_t red[2][RT * MT][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
   const int b = p.block0 + blockIdx.x / p.splits, sp = blockIdx.x % p.splits;
   const int g = p.groups[b];
-  if ((uint32_t)g >= (uint32_t)p.G) return;
   const int row0 = blockIdx.y * MT * 16;
-  const uint16_t* xr[MT];
+  const int32_t* ids = p.sorted + (int64_t)b * p.bm;
+  const uint32_t first = (uint32_t)ids[0];
   uint32_t slot[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) slot[m] = (uint32_t)ids[min(row0 + 16 * m + m16, p.bm - 1)];
+  if ((uint32_t)g >= (uint32_t)p.G) return;
+  const uint16_t* xr[MT];
   bool live[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int row = row0 + 16 * m + m16;
-    slot[m] = row < p.bm ? (uint32_t)p.sorted[(int64_t)b * p.bm + row] : 0xFFFFFFFFu;
-    live[m] = slot[m] < (uint32_t)p.S;
-    xr[m] = p.x + (int64_t)(live[m] ? lora_div(slot[m], p.div_magic, p.div_shift) : 0) * p.x_ld + 8 * q;
+    live[m] = row0 + 16 * m + m16 < p.bm && slot[m] < (uint32_t)p.S;
+    const uint32_t s = live[m] ? slot[m] : first < (uint32_t)p.S ? first : 0;
+    xr[m] = p.x + (int64_t)lora_div(s, p.div_magic, p.div_shift) * p.x_ld + 8 * q;
   }
   const uint16_t* wr[RT];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) wr[t] = p.w + (int64_t)g * p.w_g + (int64_t)(16 * t + m16) * p.w_ld + 8 * q;
-  constexpr int kTurn = 32 * U;
-  const int units = (p.K + 63) / 64, per = (units + p.splits - 1) / p.splits;
-  const int end = min(p.K, 64 * (sp + 1) * per);
-  u32x4_t xv[U][MT], wv[U][RT];
-  auto load = [&](int k0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + 32 * u;
-      const bool in = k + 8 * q < end;
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-        xv[u][m] = in && live[m] ? *reinterpret_cast<const u32x4_t*>(xr[m] + k) : u32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-        wv[u][t] = in && 16 * t + m16 < p.R ? *reinterpret_cast<const u32x4_t*>(wr[t] + k) : u32x4_t{0, 0, 0, 0};
-    }
-  };
+  for (int t = 0; t < RT; ++t)
+    wr[t] = p.w + (int64_t)g * p.w_g + (int64_t)min(16 * t + m16, p.R - 1) * p.w_ld + 8 * q;
   f32x4_t acc[RT][MT];
 #pragma unroll
   for (int t = 0; t < RT; ++t)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0, 0, 0, 0};
-  int k = 64 * sp * per + kTurn * wave;
-  if (k < end) load(k);
-  while (k < end) {
-    u32x4_t xn[U][MT], wn[U][RT];
-    __builtin_memcpy(xn, xv, sizeof(xv));
-    __builtin_memcpy(wn, wv, sizeof(wv));
-    k += 4 * kTurn;
-    if (k < end) load(k);
+  struct Turn {
+    u32x4_t x[U][MT], w[U][RT];
+  };
+  auto load = [&](Turn& v, int turn) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = kTurn * turn + 32 * u;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) v.x[u][m] = *reinterpret_cast<const u32x4_t*>(xr[m] + k);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) v.w[u][t] = *reinterpret_cast<const u32x4_t*>(wr[t] + k);
+    }
+  };
+  auto add = [&](const Turn& v) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] = lora_mfma(wn[u][t], xn[u][m], acc[t][m]);
+        for (int m = 0; m < MT; ++m) acc[t][m] = lora_mfma(v.w[u][t], v.x[u][m], acc[t][m]);
+  };
+  const int turns = p.K / kTurn, per = (turns + p.splits - 1) / p.splits;
+  const int end = min(turns, (sp + 1) * per);
+  Turn v, next;
+  int i = sp * per + wave;
+  if (i < end) load(v, i);
+  for (; i + 4 < end; i += 8) {
+    load(next, i + 4);
+    add(v);
+    if (i + 8 < end) load(v, i + 8);
+    add(next);
+  }
+  if (i < end) add(v);
+  if (kTurn * turns < p.K && sp == p.splits - 1 && wave == 0) {  // the columns behind the last whole turn
+    Turn z = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = kTurn * turns + 32 * u;
+      if (k + 8 * q >= p.K) continue;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) z.x[u][m] = *reinterpret_cast<const u32x4_t*>(xr[m] + k);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) z.w[u][t] = *reinterpret_cast<const u32x4_t*>(wr[t] + k);
+    }
+    add(z);
   }
   // the waves' sums: the upper half's into the lower half's, and so on
 #pragma unroll
@@ -185,9 +206,9 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_few_kernel(LoraParams p)
   const int64_t pos0 = (int64_t)b * p.bm + row0;
   const int32_t* ids = p.sorted + pos0;
   const int pieces = p.R / 8;
-  const uint32_t slot = m16 < rows ? (uint32_t)ids[m16] : 0xFFFFFFFFu;
-  const bool live = slot < (uint32_t)p.S;
-  uint16_t* cr = p.c + (int64_t)(live ? slot : 0) * p.c_ld + 8 * q;
+  const uint32_t slot = (uint32_t)ids[min(m16, rows - 1)], first = (uint32_t)p.sorted[(int64_t)b * p.bm];
+  const bool live = m16 < rows && slot < (uint32_t)p.S;
+  uint16_t* cr = p.c + (int64_t)(live ? slot : first < (uint32_t)p.S ? first : 0) * p.c_ld;
   const uint16_t* wr = p.w + (int64_t)g * p.w_g;
   const int chunks = (p.N + 63) / 64, per = (chunks + p.n_splits - 1) / p.n_splits;
   const int end = min(chunks, (sp + 1) * per);
@@ -196,16 +217,16 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_few_kernel(LoraParams p)
     const int n0 = 64 * i;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      cv[e] = live && n0 + 32 * e + 8 * q < p.N ? *reinterpret_cast<const u32x4_t*>(cr + n0 + 32 * e)
-                                                : u32x4_t{0, 0, 0, 0};
+      cv[e] = *reinterpret_cast<const u32x4_t*>(cr + min(n0 + 32 * e + 8 * q, p.N - 8));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 32 * (j / 2) + 8 * (m16 / 4) + 4 * (j % 2) + m16 % 4;
+      const int n = min(n0 + 32 * (j / 2) + 8 * (m16 / 4) + 4 * (j % 2) + m16 % 4, p.N - 1);
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
-        const bool in = n < p.N && piece < pieces && (RC != 1 || q < 2);
-        wv[j][f] = in ? *reinterpret_cast<const u32x4_t*>(wr + (int64_t)n * p.w_ld + 8 * piece) : u32x4_t{0, 0, 0, 0};
+        const bool in = piece < pieces && (RC != 1 || q < 2);
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(wr + (int64_t)n * p.w_ld + (in ? 8 * piece : 0));
+        wv[j][f] = in ? v : u32x4_t{0, 0, 0, 0};
       }
     }
   };
@@ -259,7 +280,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_few_kernel(LoraParams p)
       for (int w = 0; w < 4; ++w)
         o[w] = lora_pack(__uint_as_float(cn[e][w] << 16) + d[2 * e + w / 2][2 * (w % 2)],
                          __uint_as_float(cn[e][w] & 0xffff0000u) + d[2 * e + w / 2][2 * (w % 2) + 1]);
-      if (live && n0 + 32 * e + 8 * q < p.N) *reinterpret_cast<u32x4_t*>(cr + n0 + 32 * e) = o;
+      if (live && n0 + 32 * e + 8 * q < p.N) *reinterpret_cast<u32x4_t*>(cr + n0 + 32 * e + 8 * q) = o;
     }
   }
 }
@@ -289,77 +310,78 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
   const bool in = n0 + NT * m16 < p.N;
   const int pieces = p.R / 8;
 
-  int ids[4], gid = -1;
-  auto load_ids = [&](int t) {
-    const int b = b0 + t / per, row = 16 * (t % per) + 4 * q;
-    gid = __builtin_amdgcn_readfirstlane(p.groups[b]);
-    ids[0] = ids[1] = ids[2] = ids[3] = -1;
-    if (row < p.bm) __builtin_memcpy(ids, p.sorted + (int64_t)b * p.bm + row, 16);
+  // Loads are not masked: a place without a slot reads the block's first row, a
+  // column past N the last ones; what comes of them is not stored. (A tile of a
+  // block without a group is passed over.)
+  const int col = n0 + NT * m16 < p.N ? n0 + NT * m16 : p.N - NT;
+  struct Ids {
+    int slot[4], first, group;
   };
-  u32x4_t cv[4], hv[F][P];
-  uint16_t* cr[4];
-  int g = -1;
-  auto load = [&](int t) {  // tile t, whose ids are here
-    g = gid;
-    const bool group = (uint32_t)g < (uint32_t)p.G;
+  struct Tile {
+    u32x4_t c[4], h[F][P];
+    uint16_t* to[4];
+    int group;
+  };
+  auto load_ids = [&](Ids& v, int t) {
+    const int b = b0 + t / per, row = 16 * (t % per) + 4 * q;
+    const int32_t* at = p.sorted + (int64_t)b * p.bm;
+    v.group = p.groups[b];
+    v.first = at[0];
+    __builtin_memcpy(v.slot, at + (row < p.bm ? row : 0), 16);
+  };
+  auto load = [&](Tile& v, const Ids& ids, int t) {
+    const int row = 16 * (t % per);
+    v.group = __builtin_amdgcn_readfirstlane(ids.group);
+    if ((uint32_t)v.group >= (uint32_t)p.G) return;
+    const int first = (uint32_t)ids.first < (uint32_t)p.S ? ids.first : 0;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const bool live = group && (uint32_t)ids[r] < (uint32_t)p.S && in;
-      cr[r] = live ? p.c + (int64_t)ids[r] * p.c_ld + n0 + NT * m16 : nullptr;
-      cv[r] = live ? *reinterpret_cast<const u32x4_t*>(cr[r]) : u32x4_t{0, 0, 0, 0};
+      const bool live = row + 4 * q < p.bm && (uint32_t)ids.slot[r] < (uint32_t)p.S;
+      uint16_t* at = p.c + (int64_t)(live ? ids.slot[r] : first) * p.c_ld + col;
+      v.to[r] = live && in ? at : nullptr;
+      v.c[r] = *reinterpret_cast<const u32x4_t*>(at);
     }
-    const int64_t pos = (int64_t)(b0 + t / per) * p.bm + 16 * (t % per) + m16;
-    const bool row = group && 16 * (t % per) + m16 < p.bm;
+    const int64_t pos = (int64_t)(b0 + t / per) * p.bm + min(row + m16, p.bm - 1);
     const uint16_t* at = p.packed + pos * (2 * p.R);
 #pragma unroll
     for (int f = 0; f < F; ++f)
 #pragma unroll
       for (int k = 0; k < P; ++k) {
         const int piece = RC >= 4 ? 4 * f + q : q;  // (RC < 4: hi and lo pieces follow each other)
-        const bool here = row && (RC >= 4 ? piece < pieces : q < 2 * RC);
-        hv[f][k] = here ? *reinterpret_cast<const u32x4_t*>(at + k * p.R + 8 * piece) : u32x4_t{0, 0, 0, 0};
+        const bool here = RC >= 4 ? piece < pieces : q < 2 * RC;
+        const u32x4_t h = *reinterpret_cast<const u32x4_t*>(at + (here ? k * p.R + 8 * piece : 0));
+        v.h[f][k] = here ? h : u32x4_t{0, 0, 0, 0};
       }
   };
   u32x4_t wv[NT][F];
   int have = -1;  // the group whose B is here
-  load_ids(0);
-  load(0);
-  if (tiles > 1) load_ids(1);
-  for (int t = 0; t < tiles; ++t) {
-    const int now = g;
-    if (now != have && (uint32_t)now < (uint32_t)p.G) {
-      have = now;
-      const uint16_t* wr = p.w + (int64_t)now * p.w_g;
+  auto add = [&](const Tile& v) {
+    if ((uint32_t)v.group >= (uint32_t)p.G) return;
+    if (v.group != have) {
+      have = v.group;
+      const uint16_t* wr = p.w + (int64_t)have * p.w_g;
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
-        const bool here = in && piece < pieces && (RC != 1 || q < 2);
-        u32x4_t v[NT];
+        const bool here = piece < pieces && (RC != 1 || q < 2);
+        u32x4_t w[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const uint16_t* at = TURNED ? wr + (int64_t)(8 * piece + j) * p.w_ld + n0 + NT * m16
-                                      : wr + (int64_t)(n0 + NT * m16 + j) * p.w_ld + 8 * piece;
-          v[j] = here ? *reinterpret_cast<const u32x4_t*>(at) : u32x4_t{0, 0, 0, 0};
+          const int rank = here ? 8 * piece : 0;
+          w[j] = *reinterpret_cast<const u32x4_t*>(TURNED ? wr + (int64_t)(rank + j) * p.w_ld + col
+                                                          : wr + (int64_t)(col + j) * p.w_ld + rank);
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            wv[j][f][w] = TURNED ? __builtin_amdgcn_perm(v[2 * w + 1][j / 2], v[2 * w][j / 2],
-                                                         j % 2 ? 0x07060302u : 0x05040100u)
-                                 : v[j][w];
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t b = TURNED ? __builtin_amdgcn_perm(w[2 * e + 1][j / 2], w[2 * e][j / 2],
+                                                              j % 2 ? 0x07060302u : 0x05040100u)
+                                      : w[j][e];
+            wv[j][f][e] = here ? b : 0u;
+          }
       }
     }
-    u32x4_t cn[4], hn[F][P];
-    uint16_t* to[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      cn[r] = cv[r];
-      to[r] = cr[r];
-    }
-    __builtin_memcpy(hn, hv, sizeof(hv));
-    if (t + 1 < tiles) load(t + 1);
-    if (t + 2 < tiles) load_ids(t + 2);
     f32x4_t d[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -367,17 +389,35 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
 #pragma unroll
       for (int f = 0; f < F; ++f)
 #pragma unroll
-        for (int k = 0; k < P; ++k) d[j] = lora_mfma(hn[f][k], wv[j][f], d[j]);
+        for (int k = 0; k < P; ++k) d[j] = lora_mfma(v.h[f][k], wv[j][f], d[j]);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       u32x4_t o;
 #pragma unroll
       for (int w = 0; w < 4; ++w)
-        o[w] = lora_pack(__uint_as_float(cn[r][w] << 16) + d[2 * w][r],
-                         __uint_as_float(cn[r][w] & 0xffff0000u) + d[2 * w + 1][r]);
-      if (to[r] != nullptr) *reinterpret_cast<u32x4_t*>(to[r]) = o;
+        o[w] = lora_pack(__uint_as_float(v.c[r][w] << 16) + d[2 * w][r],
+                         __uint_as_float(v.c[r][w] & 0xffff0000u) + d[2 * w + 1][r]);
+      if (v.to[r] != nullptr) *reinterpret_cast<u32x4_t*>(v.to[r]) = o;
     }
+  };
+  Ids ids;
+  Tile v, next;
+  load_ids(ids, 0);
+  load(v, ids, 0);
+  if (tiles > 1) load_ids(ids, 1);
+  for (int t = 0; t < tiles; t += 2) {
+    if (t + 1 < tiles) {
+      load(next, ids, t + 1);
+      if (t + 2 < tiles) load_ids(ids, t + 2);
+    }
+    add(v);
+    if (t + 1 >= tiles) break;
+    if (t + 2 < tiles) {
+      load(v, ids, t + 2);
+      if (t + 3 < tiles) load_ids(ids, t + 3);
+    }
+    add(next);
   }
 }
 

@@ -25,11 +25,10 @@ constexpr int kLgSegInts = 5;  // group, first block, end, partial slot (-1: non
 // ------------------------------------------------------------------ table
 
 // The segments, one workgroup: table[0] their number, then kLgSegInts each.
-// Segments hold seg_blocks blocks (a group's last one fewer), groups ascending;
-// a group without blocks has an empty one, which writes its zeros.
+// Segments hold seg_blocks blocks (a group's last one fewer); a group without blocks has an empty one, which writes its zeros.
 __global__ __launch_bounds__(1024) void lora_table_kernel(LoraGradParams p) {
   const int tid = threadIdx.x;
-  __shared__ int first[kLgMaxGroups + 1], count[kLgMaxGroups], scan[2][kLgMaxGroups];
+  __shared__ int first[kLgMaxGroups + 1], count[kLgMaxGroups], scan[kLgMaxGroups];
   if (tid < p.G) {
     first[tid] = 0;
     count[tid] = 0;
@@ -47,35 +46,49 @@ __global__ __launch_bounds__(1024) void lora_table_kernel(LoraGradParams p) {
     if (b + 1 == p.max_blocks || p.groups[b + 1] != g) count[g] = b + 1 > first[g] ? b + 1 - first[g] : 0;
   }
   __syncthreads();
-  // segments before each group, and partial slots before it
+  // partial slots before each group
   const int n = tid < p.G ? count[tid] : 0;
   const int segs = tid < p.G ? (n + p.seg_blocks - 1) / p.seg_blocks : 0;
   const int mine = tid < p.G ? (segs > 1 ? segs : 1) : 0, parts = segs > 1 ? segs : 0;
-  scan[0][tid] = mine;
-  scan[1][tid] = parts;
+  scan[tid] = parts;
   __syncthreads();
-  for (int d = 1; d < 1024; d *= 2) {
-    const int a = tid >= d ? scan[0][tid - d] : 0, b = tid >= d ? scan[1][tid - d] : 0;
+  for (int d = 1; d < p.G; d *= 2) {
+    const int a = tid >= d ? scan[tid - d] : 0;
     __syncthreads();
-    scan[0][tid] += a;
-    scan[1][tid] += b;
+    scan[tid] += a;
     __syncthreads();
   }
-  if (tid == 1023) p.table[0] = scan[0][tid] < p.max_segs ? scan[0][tid] : p.max_segs;
-  if (tid < p.G) {
-    const int at = scan[0][tid] - mine, part = scan[1][tid] - parts;
-    for (int i = 0; i < mine; ++i) {
-      if (at + i >= p.max_segs) break;
-      // (the sizes allow for every list of moe_align; of another one, whose groups
-      // recur, what does not fit is left out)
-      const bool fits = parts == 0 || part + parts <= p.max_parts;
-      int32_t* e = p.table + 1 + (int64_t)(at + i) * kLgSegInts;
-      e[0] = tid;
-      e[1] = fits ? first[tid] + i * p.seg_blocks : 0;
-      e[2] = fits ? min(first[tid] + (i + 1) * p.seg_blocks, first[tid] + n) : 0;
-      e[3] = parts && fits ? part + i : -1;
-      e[4] = parts && fits && i == 0 ? segs : 0;
-    }
+  // Longest segments first, so that none is left for the end: by size in kBuckets
+  // steps (the order inside one, an atomic's, decides nothing but who runs when).
+  constexpr int kBuckets = 64;
+  __shared__ int bucket[kBuckets + 1];
+  if (tid <= kBuckets) bucket[tid] = 0;
+  __syncthreads();
+  auto in = [&](int blocks) { return kBuckets - 1 - (int)((int64_t)blocks * (kBuckets - 1) / p.seg_blocks); };
+  const int rest = n - (mine - 1) * p.seg_blocks;  // blocks of the group's last segment
+  if (mine > 0) {
+    if (mine > 1) atomicAdd(&bucket[in(p.seg_blocks) + 1], mine - 1);
+    atomicAdd(&bucket[in(rest) + 1], 1);
+  }
+  __syncthreads();
+  if (tid == 0)
+    for (int i = 1; i <= kBuckets; ++i) bucket[i] += bucket[i - 1];
+  __syncthreads();
+  if (tid == 0) p.table[0] = min(bucket[kBuckets], p.max_segs);
+  const int part = scan[tid] - parts;
+  // (the sizes allow for every list of moe_align; of another one, whose groups
+  // recur, what does not fit is left out)
+  const bool fits = parts == 0 || part + parts <= p.max_parts;
+  __syncthreads();
+  for (int i = 0; i < mine; ++i) {
+    const int at = atomicAdd(&bucket[in(i + 1 < mine ? p.seg_blocks : rest)], 1);
+    if (at >= p.max_segs) continue;
+    int32_t* e = p.table + 1 + (int64_t)at * kLgSegInts;
+    e[0] = tid;
+    e[1] = fits ? first[tid] + i * p.seg_blocks : 0;
+    e[2] = fits ? min(first[tid] + (i + 1) * p.seg_blocks, first[tid] + n) : 0;
+    e[3] = parts && fits ? part + i : -1;
+    e[4] = parts && fits && i == 0 ? segs : 0;
   }
 }
 
@@ -109,6 +122,7 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
   __shared__ __attribute__((aligned(16))) uint8_t wide[kLgSlots * kLgCols * 2];
   __shared__ __attribute__((aligned(16))) uint16_t narrow[3][RT * 16][kNarrowLd];
   __shared__ f32x4_t red[OF_X || NP == 1 ? 1 : NP][2 * RT][64];
+  const lora_lds_u8* base = (const lora_lds_u8*)wide;
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, q = lane / 16, m16 = lane % 16;
   if ((int)blockIdx.y >= p.table[0]) return;
   const int32_t* e = p.table + 1 + (int64_t)blockIdx.y * kLgSegInts;
@@ -125,55 +139,43 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
 #pragma unroll
     for (int j = 0; j < NC; ++j) acc[t][j] = f32x4_t{0, 0, 0, 0};
 
-  // B of this wave's dh tiles: rank tile rt at its part of the columns
-  const int rt = wave % RT, st = ST == 2 ? 0 : wave / RT % 2, np = NP == 1 ? 0 : wave / (2 * RT);
-  u32x4_t bv[OF_X ? 1 : KS];
-  if constexpr (!OF_X) {
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int r = 16 * rt + m16, n = c0 + np * (kLgCols / NP) + 32 * s + 8 * q;
-      const uint16_t* at = p.b + (int64_t)g * p.b_g + (int64_t)n * p.b_ld + r;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const bool in = r < p.R && n < width && pos0 < pos1;  // (n % 8 == 0 and so is the width)
-        const uint32_t lo = in ? at[(2 * w) * p.b_ld] : 0, hi = in ? at[(2 * w + 1) * p.b_ld] : 0;
-        bv[s][w] = lo | hi << 16;
-      }
-    }
-  }
-
   const int srow = tid / 16, piece = tid % 16;            // of the wide tile: NV pieces of 8 columns, 16 apart
   const int nslot = tid % kLgSlots, nr = tid / kLgSlots;  // of the narrow one: ranks 4 nr, + 64
-  uint32_t wide_id = 0xFFFFFFFFu, narrow_id = 0xFFFFFFFFu;
+  const int rt = wave % RT, st = ST == 2 ? 0 : wave / RT % 2, np = NP == 1 ? 0 : wave / (2 * RT);
+  u32x4_t bv[OF_X ? 1 : KS];
+  // Loads are not masked: a place without a slot, or past the segment, reads the
+  // segment's first row, a column past the width the last ones, and becomes zeros
+  // on the way to LDS.
+  struct {
+    uint32_t wide, narrow;
+  } ids;  // of the step after the one in `o`
+  struct {
+    u32x4_t v[NV];
+    f32x4_t h[NH];
+    bool wide, narrow;
+  } o;  // a step's loads
+  const uint32_t first = pos0 < pos1 ? (uint32_t)p.sorted[pos0] : 0;
+  const uint32_t spare = first < (uint32_t)p.S ? first : 0;
   auto load_ids = [&](int64_t pos) {
-    wide_id = pos + srow < pos1 ? (uint32_t)p.sorted[pos + srow] : 0xFFFFFFFFu;
-    if (!OF_X) narrow_id = pos + nslot < pos1 ? (uint32_t)p.sorted[pos + nslot] : 0xFFFFFFFFu;
+    ids.wide = (uint32_t)p.sorted[min(pos + srow, pos1 - 1)];
+    if (!OF_X) ids.narrow = (uint32_t)p.sorted[min(pos + nslot, pos1 - 1)];
   };
-  u32x4_t v[NV];
-  f32x4_t h[NH];
   auto load = [&](int64_t pos) {
-    const bool live = wide_id < (uint32_t)p.S;
-    const uint16_t* row =
-        big + (int64_t)(live ? (OF_X ? lora_div(wide_id, p.div_magic, p.div_shift) : wide_id) : 0) * ld + c0;
+    o.wide = pos + srow < pos1 && ids.wide < (uint32_t)p.S;
+    const uint32_t s = o.wide ? ids.wide : spare;
+    const uint16_t* row = big + (int64_t)(OF_X ? lora_div(s, p.div_magic, p.div_shift) : s) * ld;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (piece + 16 * i);
-      v[i] = live && c0 + c < width ? *reinterpret_cast<const u32x4_t*>(row + c) : u32x4_t{0, 0, 0, 0};
-    }
+    for (int i = 0; i < NV; ++i)
+      o.v[i] = *reinterpret_cast<const u32x4_t*>(row + min(c0 + 8 * (piece + 16 * i), width - 8));
+    o.narrow = pos + nslot < pos1 && (OF_X || ids.narrow < (uint32_t)p.S);
+    if (!OF_X && !weights) return;
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
-      const int r = 4 * nr + 64 * i;
-      h[i] = f32x4_t{0, 0, 0, 0};
-      if (r >= p.R) continue;
-      if constexpr (OF_X) {
-        if (pos + nslot < pos1) h[i] = *reinterpret_cast<const f32x4_t*>(p.dh + (pos + nslot) * p.R + r);
-      } else {
-        if (weights && narrow_id < (uint32_t)p.S)
-          h[i] = *reinterpret_cast<const f32x4_t*>(p.h + (int64_t)narrow_id * p.R + r) * scale;
-      }
+      const int r = min(4 * nr + 64 * i, p.R - 4);
+      o.h[i] = *reinterpret_cast<const f32x4_t*>(
+          OF_X ? p.dh + min(pos + nslot, pos1 - 1) * p.R + r : p.h + (int64_t)(o.narrow ? ids.narrow : spare) * p.R + r);
     }
   };
-  const lora_lds_u8* base = (const lora_lds_u8*)wide;
   constexpr int kRowB = kLgCols * 2;
   auto put_dh = [&](int64_t pos, int tile, f32x4_t d) {  // tile = 2 * rank tile + slot tile
     const int64_t at = pos + 16 * (tile % 2) + m16;
@@ -181,12 +183,7 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
     if (at < pos1 && r < p.R)
       *reinterpret_cast<f32x4_t*>(p.dh + ((int64_t)blockIdx.x * p.max_blocks * p.bm + at) * p.R + r) = d;
   };
-  if (pos0 < pos1) {
-    load_ids(pos0);
-    load(pos0);
-    load_ids(pos0 + kLgSlots);
-  }
-  for (int64_t pos = pos0; pos < pos1; pos += kLgSlots) {
+  auto step = [&](int64_t pos) {
     __syncthreads();  // the last step's reads are done, its parts of dh written
     if (!OF_X && NP > 1 && pos > pos0)
       for (int i = wave; i < 2 * RT; i += 8) {
@@ -197,19 +194,23 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
       }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      *reinterpret_cast<u32x4_t*>(wide + srow * kRowB + 16 * lora_swz(srow, piece + 16 * i)) = v[i];
+      *reinterpret_cast<u32x4_t*>(wide + srow * kRowB + 16 * lora_swz(srow, piece + 16 * i)) =
+          o.wide && c0 + 8 * (piece + 16 * i) < width ? o.v[i] : u32x4_t{0, 0, 0, 0};
+    if (OF_X || weights) {
 #pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      const int r = 4 * nr + 64 * i;
-      if (r >= RT * 16) continue;
+      for (int i = 0; i < NH; ++i) {
+        const int r = 4 * nr + 64 * i;
+        if (r >= RT * 16) continue;
+        const f32x4_t h = o.narrow && r < p.R ? (OF_X ? o.h[i] : o.h[i] * scale) : f32x4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t term[3];
-        lora_split3(h[i][2 * k], h[i][2 * k + 1], term);
+        for (int k = 0; k < 2; ++k) {
+          uint32_t term[3];
+          lora_split3(h[2 * k], h[2 * k + 1], term);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          narrow[j][r + 2 * k][nslot] = (uint16_t)term[j];
-          narrow[j][r + 2 * k + 1][nslot] = (uint16_t)(term[j] >> 16);
+          for (int j = 0; j < 3; ++j) {
+            narrow[j][r + 2 * k][nslot] = (uint16_t)term[j];
+            narrow[j][r + 2 * k + 1][nslot] = (uint16_t)(term[j] >> 16);
+          }
         }
       }
     }
@@ -261,6 +262,42 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
             acc[t][j] = lora_mfma(*reinterpret_cast<const u32x4_t*>(&narrow[k][16 * t + m16][8 * q]), wv, acc[t][j]);
       }
     }
+  };
+  if (pos0 < pos1) {
+    load_ids(pos0);
+    load(pos0);
+    load_ids(pos0 + kLgSlots);
+    // B of this wave's dh tiles, rank tile rt at its part of the columns: rows of
+    // 16 ranks of the columns to LDS, where a rank tile after another is read
+    // transposed
+    if constexpr (!OF_X) {
+      constexpr int kRowsB = kLgSlots * kLgCols * 2 / 32;  // columns of B that the tile's LDS holds at 16 ranks: all
+      static_assert(kRowsB >= kLgCols, "B's rows fit");
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        if (t > 0) __syncthreads();
+        for (int i = tid; i < kLgCols * 2; i += kLgThreads) {  // 16 bytes: 8 ranks of a column
+          const int n = min(c0 + i / 2, width - 1), r = 16 * t + 8 * (i % 2);
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(p.b + (int64_t)g * p.b_g + (int64_t)n * p.b_ld +
+                                                              min(r, p.R - 8));
+          *reinterpret_cast<u32x4_t*>(wide + 16 * i) = c0 + i / 2 < width && r < p.R ? v : u32x4_t{0, 0, 0, 0};
+        }
+        __syncthreads();
+        if (t != rt) continue;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          lora_s16x4 w[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int n = np * (kLgCols / NP) + 32 * k + 8 * q + 4 * half + m16 / 4;
+            w[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) lora_s16x4*)(base + n * 32 + 8 * (m16 % 4)));
+          }
+          __builtin_memcpy(&bv[k], w, 16);
+        }
+      }
+    }
+    for (int64_t pos = pos0; pos < pos1; pos += kLgSlots) step(pos);
   }
   if (!OF_X && NP > 1 && pos0 < pos1) {
     __syncthreads();
