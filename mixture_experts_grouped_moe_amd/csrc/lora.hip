@@ -41,9 +41,6 @@ __device__ __forceinline__ f32x4_t lora_sum_parts(const float* at, int64_t step,
   return h;
 }
 
-#ifndef DU
-#define DU 2
-#endif
 // ------------------------------------------------------------------- down
 
 // D rows are ranks, columns slots: a lane then holds 4 consecutive ranks of a
@@ -54,7 +51,7 @@ __device__ __forceinline__ f32x4_t lora_sum_parts(const float* at, int64_t step,
 // and their rows and columns of D are not stored.
 template <int RT, int MT>
 __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
-  constexpr int U = RT + MT <= 2 ? 4 : RT >= 4 ? 1 : DU;  // steps of 32 columns of a turn
+  constexpr int U = RT + MT <= 2 ? 4 : RT >= 4 ? 1 : 2;  // steps of 32 columns of a turn
   constexpr int kTurn = 32 * U;
   __shared__ f32x4_t red[2][RT * MT][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
@@ -166,22 +163,21 @@ __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
   }
 }
 
-// Several parts -> h where it is wanted, and packed. (`all`: the places without
-// a slot too, whose parts are zeros, and the scaled sum over the first part: the
-// backward pass's dh.)
-__global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraParams p, bool all) {
+// Several parts -> h where it is wanted, and packed. (`over`: the scaled sum over
+// the first part, the backward pass's dh.)
+__global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraParams p, bool over) {
   const int64_t places = (int64_t)p.max_blocks * p.bm, n = places * (p.R / 4);
   for (int64_t i = (int64_t)blockIdx.x * kLoraThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kLoraThreads) {
     const int64_t pos = i / (p.R / 4);
     const int r = (int)(i % (p.R / 4)) * 4;
     const int g = p.groups[pos / p.bm];
     const uint32_t s = (uint32_t)p.sorted[pos];
-    if ((uint32_t)g >= (uint32_t)p.G || (!all && s >= (uint32_t)p.S)) continue;
+    if ((uint32_t)g >= (uint32_t)p.G || s >= (uint32_t)p.S) continue;
     const float scale = p.scale != nullptr ? p.scale[g] : 1.0f;
     float* at = p.part + pos * p.R + r;
     const f32x4_t h = lora_sum_parts(at, places * p.R, p.splits);
     if (p.packed != nullptr) lora_put_packed(p.packed, pos, p.R, r, h, scale);
-    if (all) *reinterpret_cast<f32x4_t*>(at) = h * scale;
+    if (over) *reinterpret_cast<f32x4_t*>(at) = h * scale;
     if (p.h != nullptr) *reinterpret_cast<f32x4_t*>(p.h + (int64_t)s * p.R + r) = h;
   }
 }
@@ -355,10 +351,9 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
   };
   u32x4_t wv[NT][F];
   int have = -1;  // the group whose B is here
-  auto add = [&](const Tile& v) {
-    if ((uint32_t)v.group >= (uint32_t)p.G) return;
-    if (v.group != have) {
-      have = v.group;
+  auto matrix = [&](int group) {
+    if (group != have && (uint32_t)group < (uint32_t)p.G) {
+      have = group;
       const uint16_t* wr = p.w + (int64_t)have * p.w_g;
 #pragma unroll
       for (int f = 0; f < F; ++f) {
@@ -382,6 +377,9 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
           }
       }
     }
+  };
+  auto add = [&](const Tile& v) {
+    if ((uint32_t)v.group >= (uint32_t)p.G) return;
     f32x4_t d[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -405,14 +403,17 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
   Tile v, next;
   load_ids(ids, 0);
   load(v, ids, 0);
+  matrix(v.group);
   if (tiles > 1) load_ids(ids, 1);
   for (int t = 0; t < tiles; t += 2) {
+    matrix(v.group);
     if (t + 1 < tiles) {
       load(next, ids, t + 1);
       if (t + 2 < tiles) load_ids(ids, t + 2);
     }
     add(v);
     if (t + 1 >= tiles) break;
+    matrix(next.group);
     if (t + 2 < tiles) {
       load(v, ids, t + 2);
       if (t + 3 < tiles) load_ids(ids, t + 3);
@@ -423,21 +424,17 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
 
 // ------------------------------------------------------------------ launch
 
-#ifndef FEWT
-#define FEWT 64
-#endif
-#ifndef DW
-#define DW 256
-#endif
-#ifndef UW
-#define UW 1536
-#endif
-// Whether the small `up` serves: up to FEWT tiles of 16 slots.
-static bool lora_few(int64_t max_blocks, int bm) { return max_blocks * (bm < 16 ? 1 : bm / 16) <= FEWT; }
+// Whether the small `up` serves: up to 64 tiles of 16 slots. (28 slots of 16
+// groups, 1856 columns, rank 16: 6.6 us for the whole call, 8.2 through `up`;
+// 256 slots of 32 groups, 7168 columns: 13.1, and 16.3 us with `join` and `up`.)
+static bool lora_few(int64_t max_blocks, int bm) { return max_blocks * (bm < 16 ? 1 : bm / 16) <= 64; }
 
-// Parts of K: enough workgroups for the chip, at least 256 columns each.
+// Parts of K: a workgroup for each CU, at least 256 columns and at most 32 parts.
+// (8192 slots, 8 groups, K = 7168, rank 32: 68 us for the whole call at 2 parts,
+// 75 at 3, 70 at 4, 79 at 1; 7 slots of 7 groups, rank 128: 15 us at 28 parts, 25
+// at 8.)
 int lora_k_splits(int64_t max_blocks, int64_t k) {
-  const int64_t want = (DW + max_blocks - 1) / (max_blocks > 0 ? max_blocks : 1);
+  const int64_t want = (256 + max_blocks - 1) / (max_blocks > 0 ? max_blocks : 1);
   const int64_t most = k / 256 > 1 ? k / 256 : 1;
   const int64_t n = want < most ? want : most;
   return (int)(n < 32 ? n : 32);
@@ -486,11 +483,11 @@ hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream) {
   });
 }
 
-hipError_t launch_lora_join(const LoraParams& p, bool all, hipStream_t stream) {
+hipError_t launch_lora_join(const LoraParams& p, bool over, hipStream_t stream) {
   const int64_t want = ((int64_t)p.max_blocks * p.bm * (p.R / 4) + kLoraThreads - 1) / kLoraThreads;
   if (want == 0) return hipSuccess;
   hipLaunchKernelGGL(lora_join_kernel, dim3((uint32_t)(want < 4096 ? want : 4096)), dim3(kLoraThreads), 0, stream, p,
-                     all);
+                     over);
   return hipGetLastError();
 }
 
@@ -498,7 +495,9 @@ hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream)
   LoraParams p = p0;
   p.n_splits = (p.N + 511) / 512;
   const int64_t all = (int64_t)p.max_blocks * p.n_splits;
-  p.run_blocks = (int32_t)(all / UW > 1 ? all / UW : 1);
+  // about 3072 workgroups: many more than run at once, so that they end together
+  // (32768 slots of 128 groups, 5760 columns: 180 us for the whole call, 184 at 1536)
+  p.run_blocks = (int32_t)(all / 3072 > 1 ? all / 3072 : 1);
   return lora_rank(p.R, [&](auto rank) {
     constexpr int RC = decltype(rank)::value;
     return lora_blocks(p, p.run_blocks, p.n_splits, [&](const LoraParams& q, uint32_t grid) {

@@ -17,78 +17,112 @@ constexpr int kLgThreads = 512;
 constexpr int lora_wide_cols(int R) { return R > 64 ? 256 : 512; }
 constexpr int kLgSlots = 32;   // slots a step
 constexpr int kLgMaxGroups = 1024;
-constexpr int kLgSegInts = 5;  // group, first block, end, partial slot (-1: none), segments of the group (0: not its first)
-#ifndef SEGW
-#define SEGW 1024
-#endif
+constexpr int kLgSegInts = 4;   // group (-1: no segment), first place, end, partial slot (-1: none)
+constexpr int kLgJoinInts = 3;  // group of several segments, its first partial slot, their number (0: no group)
 
 // ------------------------------------------------------------------ table
 
-// The segments, one workgroup: table[0] their number, then kLgSegInts each.
-// Segments hold seg_blocks blocks (a group's last one fewer); a group without blocks has an empty one, which writes its zeros.
+// The segments, one workgroup: max_segs entries of kLgSegInts, then for the join
+// an entry of kLgJoinInts for each group of several. Segments hold seg_blocks
+// blocks (a group's last one fewer, and no places behind its last slot); a group
+// without blocks has an empty one, which writes its zeros. Longest segments
+// first, so that none is left for the end: by size in kBuckets steps (the order
+// inside one, an atomic's, decides nothing but who runs when).
 __global__ __launch_bounds__(1024) void lora_table_kernel(LoraGradParams p) {
-  const int tid = threadIdx.x;
-  __shared__ int first[kLgMaxGroups + 1], count[kLgMaxGroups], scan[kLgMaxGroups];
-  if (tid < p.G) {
-    first[tid] = 0;
-    count[tid] = 0;
-  }
-  __syncthreads();
-  for (int b = tid; b < p.max_blocks; b += 1024) {
-    const int g = p.groups[b];
-    if ((uint32_t)g >= (uint32_t)p.G) continue;
-    if (b == 0 || p.groups[b - 1] != g) first[g] = b;
-  }
-  __syncthreads();
-  for (int b = tid; b < p.max_blocks; b += 1024) {
-    const int g = p.groups[b];
-    if ((uint32_t)g >= (uint32_t)p.G) continue;
-    if (b + 1 == p.max_blocks || p.groups[b + 1] != g) count[g] = b + 1 > first[g] ? b + 1 - first[g] : 0;
-  }
-  __syncthreads();
-  // partial slots before each group
-  const int n = tid < p.G ? count[tid] : 0;
-  const int segs = tid < p.G ? (n + p.seg_blocks - 1) / p.seg_blocks : 0;
-  const int mine = tid < p.G ? (segs > 1 ? segs : 1) : 0, parts = segs > 1 ? segs : 0;
-  scan[tid] = parts;
-  __syncthreads();
-  for (int d = 1; d < p.G; d *= 2) {
-    const int a = tid >= d ? scan[tid - d] : 0;
-    __syncthreads();
-    scan[tid] += a;
-    __syncthreads();
-  }
-  // Longest segments first, so that none is left for the end: by size in kBuckets
-  // steps (the order inside one, an atomic's, decides nothing but who runs when).
   constexpr int kBuckets = 64;
-  __shared__ int bucket[kBuckets + 1];
+  __shared__ int first[kLgMaxGroups], last[kLgMaxGroups], end[kLgMaxGroups], segs[kLgMaxGroups], parts[kLgMaxGroups];
+  __shared__ int bucket[kBuckets + 1], joins;
+  const int tid = threadIdx.x;
+  first[tid] = 0;
+  last[tid] = -1;
+  end[tid] = 0;
   if (tid <= kBuckets) bucket[tid] = 0;
+  if (tid == 0) joins = 0;
+  for (int i = tid; i < p.max_segs; i += 1024) p.table[i * kLgSegInts] = -1;
+  int32_t* join = p.table + p.max_segs * kLgSegInts;
+  for (int i = tid; i < p.max_parts / 2; i += 1024) join[i * kLgJoinInts + 2] = 0;
   __syncthreads();
-  auto in = [&](int blocks) { return kBuckets - 1 - (int)((int64_t)blocks * (kBuckets - 1) / p.seg_blocks); };
-  const int rest = n - (mine - 1) * p.seg_blocks;  // blocks of the group's last segment
-  if (mine > 0) {
-    if (mine > 1) atomicAdd(&bucket[in(p.seg_blocks) + 1], mine - 1);
-    atomicAdd(&bucket[in(rest) + 1], 1);
+  for (int b = tid; b < p.max_blocks; b += 1024) {
+    const int g = p.groups[b], before = b > 0 ? p.groups[b - 1] : -1;
+    const int after = b + 1 < p.max_blocks ? p.groups[b + 1] : -1;
+    if ((uint32_t)g >= (uint32_t)p.G) continue;
+    if (before != g) first[g] = b;
+    if (after != g) last[g] = b;
   }
   __syncthreads();
-  if (tid == 0)
-    for (int i = 1; i <= kBuckets; ++i) bucket[i] += bucket[i - 1];
+  // places up to the last slot of a group's last block, bm lanes a group (8 to 64, a power of two)
+  for (int i = tid; i < (p.G * p.bm + 63) / 64 * 64; i += 1024) {
+    const int g = i >> __builtin_ctz(p.bm), at = i & (p.bm - 1);
+    const bool here = g < p.G && last[g] >= 0;
+    const uint64_t live = __ballot(here && (uint32_t)p.sorted[(int64_t)last[g] * p.bm + at] < (uint32_t)p.S);
+    const uint64_t mine = live >> (tid % 64 - at) & (p.bm == 64 ? ~0ull : (1ull << p.bm) - 1);
+    if (here && at == 0) end[g] = mine != 0 ? 64 - __builtin_clzll(mine) : 0;
+  }
+  const int n = tid < p.G && last[tid] >= first[tid] ? last[tid] + 1 - first[tid] : 0;
+  const int many = (n + p.seg_blocks - 1) / p.seg_blocks, mine = tid < p.G ? (many > 1 ? many : 1) : 0;
+  segs[tid] = mine;
+  parts[tid] = many > 1 ? many : 0;
   __syncthreads();
-  if (tid == 0) p.table[0] = min(bucket[kBuckets], p.max_segs);
-  const int part = scan[tid] - parts;
-  // (the sizes allow for every list of moe_align; of another one, whose groups
-  // recur, what does not fit is left out)
-  const bool fits = parts == 0 || part + parts <= p.max_parts;
+  for (int d = 1; d < p.G; d *= 2) {  // running sums over the groups
+    const int a = tid >= d ? segs[tid - d] : 0, b = tid >= d ? parts[tid - d] : 0;
+    __syncthreads();
+    segs[tid] += a;
+    parts[tid] += b;
+    __syncthreads();
+  }
+  const int total = min(segs[p.G - 1], p.max_segs);
+  // a segment by its number: its group, and which of the group's it is
+  auto find = [&](int i, int& g) {
+    int lo = 0, hi = p.G - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (segs[mid] > i) hi = mid; else lo = mid + 1;
+    }
+    g = lo;
+    return i - (lo > 0 ? segs[lo - 1] : 0);
+  };
+  auto size = [&](int g, int k) {
+    const int blocks = last[g] >= first[g] ? last[g] + 1 - first[g] : 0;
+    return min(p.seg_blocks, blocks - k * p.seg_blocks);
+  };
+  auto in = [&](int blocks) { return kBuckets - 1 - (int)((int64_t)blocks * (kBuckets - 1) / p.seg_blocks); };
+  for (int i = tid; i < total; i += 1024) {
+    int g;
+    const int k = find(i, g);
+    atomicAdd(&bucket[in(size(g, k)) + 1], 1);
+  }
   __syncthreads();
-  for (int i = 0; i < mine; ++i) {
-    const int at = atomicAdd(&bucket[in(i + 1 < mine ? p.seg_blocks : rest)], 1);
-    if (at >= p.max_segs) continue;
-    int32_t* e = p.table + 1 + (int64_t)at * kLgSegInts;
-    e[0] = tid;
-    e[1] = fits ? first[tid] + i * p.seg_blocks : 0;
-    e[2] = fits ? min(first[tid] + (i + 1) * p.seg_blocks, first[tid] + n) : 0;
-    e[3] = parts && fits ? part + i : -1;
-    e[4] = parts && fits && i == 0 ? segs : 0;
+  if (tid < 64) {  // running sums over the buckets
+    int v = bucket[tid + 1];
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int a = __shfl_up(v, d);
+      if (tid >= d) v += a;
+    }
+    bucket[tid + 1] = v;
+  }
+  __syncthreads();
+  for (int i = tid; i < total; i += 1024) {
+    int g;
+    const int k = find(i, g), s = size(g, k), at = atomicAdd(&bucket[in(s)], 1);
+    const int of = parts[g] - (g > 0 ? parts[g - 1] : 0), part = parts[g] - of;
+    // (the sizes allow for every list of moe_align; of another one, whose groups
+    // recur, what does not fit is left out)
+    const bool fits = of == 0 || parts[g] <= p.max_parts, ends = (k + 1) * p.seg_blocks >= last[g] + 1 - first[g];
+    const int b = first[g] + k * p.seg_blocks;
+    int32_t* e = p.table + at * kLgSegInts;
+    e[1] = fits && s > 0 ? b * p.bm : 0;
+    e[2] = fits && s > 0 ? (ends ? (b + s - 1) * p.bm + end[g] : (b + s) * p.bm) : 0;
+    e[3] = of && fits ? part + k : -1;
+    e[0] = g;
+    if (of && fits && k == 0) {
+      const int j = atomicAdd(&joins, 1);
+      if (j < p.max_parts / 2) {
+        join[j * kLgJoinInts] = g;
+        join[j * kLgJoinInts + 1] = part;
+        join[j * kLgJoinInts + 2] = of;
+      }
+    }
   }
 }
 
@@ -106,28 +140,28 @@ typedef __attribute__((__vector_size__(4 * sizeof(short)))) short lora_s16x4;
 // The wide operand (rows of x or dy) comes to LDS by row, the next step's on its
 // way meanwhile; the narrow one (dh or h, fp32) is split into three bf16 terms,
 // all its bits, and lies transposed. dA and dB: D[16 ranks x 16 columns], the
-// sum over slots, the wide operand through transposing reads; a wave takes an
-// eighth of the columns at all ranks. dy also gives dh's part of these columns while it is
+// sum over slots, the wide operand through transposing reads; a wave takes 16
+// columns of every 128, at all ranks. dy also gives dh's part of these columns while it is
 // here, D[16 ranks x 16 slots], the sum over columns, with B in registers: the
-// 2 x RT tiles are dealt out to the 8 waves, in NP parts of the columns where
-// there are fewer than 8.
+// 2 x RT tiles are dealt out to the 8 waves, in NP parts of the columns (32 of
+// every 32 NP) where there are fewer than 8. (Addresses in LDS then differ by
+// constants between a wave's tiles.)
 template <int RT, bool OF_X>
-__global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p) {
+__global__ __launch_bounds__(kLgThreads, RT == 1 ? 4 : 2) void lora_wide_kernel(LoraGradParams p) {
   constexpr int kLgCols = lora_wide_cols(16 * RT), NC = kLgCols / 128;  // 16-column tiles of a wave
   constexpr int NV = kLgCols / 128;                                     // wide loads a thread
   constexpr int kNarrowLd = 40;  // slots of a rank, padded: 80 bytes
   constexpr int NP = RT >= 4 ? 1 : 4 / RT, ST = RT == 8 ? 2 : 1;  // parts of the columns, slot tiles of a wave
   constexpr int KS = kLgCols / NP / 32;                           // steps of 32 columns of a part
   constexpr int NH = RT * 4 * kLgSlots > kLgThreads ? RT * 4 * kLgSlots / kLgThreads : 1;  // narrow loads a thread
-  __shared__ __attribute__((aligned(16))) uint8_t wide[kLgSlots * kLgCols * 2];
-  __shared__ __attribute__((aligned(16))) uint16_t narrow[3][RT * 16][kNarrowLd];
+  __shared__ __attribute__((aligned(16))) uint8_t wides[2][kLgSlots * kLgCols * 2];
+  __shared__ __attribute__((aligned(16))) uint16_t narrows[2][3][RT * 16][kNarrowLd];
   __shared__ f32x4_t red[OF_X || NP == 1 ? 1 : NP][2 * RT][64];
-  const lora_lds_u8* base = (const lora_lds_u8*)wide;
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, q = lane / 16, m16 = lane % 16;
-  if ((int)blockIdx.y >= p.table[0]) return;
-  const int32_t* e = p.table + 1 + (int64_t)blockIdx.y * kLgSegInts;
+  const int32_t* e = p.table + (int64_t)blockIdx.y * kLgSegInts;
   const int g = e[0], slot = e[3];
-  const int64_t pos0 = (int64_t)e[1] * p.bm, pos1 = (int64_t)e[2] * p.bm;
+  const int64_t pos0 = e[1], pos1 = e[2];
+  if (g < 0) return;  // past the last segment
   const int c0 = blockIdx.x * kLgCols, width = OF_X ? p.K : p.N;
   const uint16_t* big = OF_X ? p.x : p.dy;
   const int64_t ld = OF_X ? p.x_ld : p.dy_ld;
@@ -152,56 +186,61 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
   struct {
     u32x4_t v[NV];
     f32x4_t h[NH];
-    bool wide, narrow;
+    uint32_t live;  // bit 0: the wide row's slot, bit 1: the narrow one's
   } o;  // a step's loads
   const uint32_t first = pos0 < pos1 ? (uint32_t)p.sorted[pos0] : 0;
   const uint32_t spare = first < (uint32_t)p.S ? first : 0;
-  auto load_ids = [&](int64_t pos) {
-    ids.wide = (uint32_t)p.sorted[min(pos + srow, pos1 - 1)];
-    if (!OF_X) ids.narrow = (uint32_t)p.sorted[min(pos + nslot, pos1 - 1)];
+  const int places = (int)(pos1 - pos0);
+  const int32_t* ids_at = p.sorted + pos0;
+  auto load_ids = [&](int at) {
+    ids.wide = (uint32_t)ids_at[min(at + srow, places - 1)];
+    ids.narrow = (uint32_t)ids_at[min(at + nslot, places - 1)];
   };
-  auto load = [&](int64_t pos) {
-    o.wide = pos + srow < pos1 && ids.wide < (uint32_t)p.S;
-    const uint32_t s = o.wide ? ids.wide : spare;
-    const uint16_t* row = big + (int64_t)(OF_X ? lora_div(s, p.div_magic, p.div_shift) : s) * ld;
+  const bool whole = c0 + kLgCols <= width;
+  const uint16_t* big0 = big + (whole ? c0 + 8 * piece : 0);
+  auto load = [&](int at) {
+    const bool wide = at + srow < places && ids.wide < (uint32_t)p.S;
+    const bool narrow = at + nslot < places && ids.narrow < (uint32_t)p.S;
+    o.live = (wide ? 1 : 0) | (narrow ? 2 : 0);
+    const uint32_t s = wide ? ids.wide : spare;
+    const uint16_t* row = big0 + (int64_t)(OF_X ? lora_div(s, p.div_magic, p.div_shift) : s) * ld;
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      o.v[i] = *reinterpret_cast<const u32x4_t*>(row + min(c0 + 8 * (piece + 16 * i), width - 8));
-    o.narrow = pos + nslot < pos1 && (OF_X || ids.narrow < (uint32_t)p.S);
-    if (!OF_X && !weights) return;
+      for (int i = 0; i < NV; ++i) o.v[i] = *reinterpret_cast<const u32x4_t*>(row + 128 * i);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      const int r = min(4 * nr + 64 * i, p.R - 4);
-      o.h[i] = *reinterpret_cast<const f32x4_t*>(
-          OF_X ? p.dh + min(pos + nslot, pos1 - 1) * p.R + r : p.h + (int64_t)(o.narrow ? ids.narrow : spare) * p.R + r);
+      for (int i = 0; i < NV; ++i)
+        o.v[i] = *reinterpret_cast<const u32x4_t*>(row + min(c0 + 8 * (piece + 16 * i), width - 8));
     }
+    if (!OF_X && !weights) return;
+    const float* from = OF_X ? p.dh + (pos0 + min(at + nslot, places - 1)) * p.R
+                             : p.h + (int64_t)(narrow ? ids.narrow : spare) * p.R;
+#pragma unroll
+    for (int i = 0; i < NH; ++i) o.h[i] = *reinterpret_cast<const f32x4_t*>(from + min(4 * nr + 64 * i, p.R - 4));
   };
   constexpr int kRowB = kLgCols * 2;
-  auto put_dh = [&](int64_t pos, int tile, f32x4_t d) {  // tile = 2 * rank tile + slot tile
-    const int64_t at = pos + 16 * (tile % 2) + m16;
+  auto put_dh = [&](int pos, int tile, f32x4_t d) {  // tile = 2 * rank tile + slot tile
+    const int at = pos + 16 * (tile % 2) + m16;
     const int r = 16 * (tile / 2) + 4 * q;
-    if (at < pos1 && r < p.R)
-      *reinterpret_cast<f32x4_t*>(p.dh + ((int64_t)blockIdx.x * p.max_blocks * p.bm + at) * p.R + r) = d;
+    if (at < places && r < p.R)
+      *reinterpret_cast<f32x4_t*>(p.dh + ((int64_t)blockIdx.x * p.max_blocks * p.bm + pos0 + at) * p.R + r) = d;
   };
-  auto step = [&](int64_t pos) {
-    __syncthreads();  // the last step's reads are done, its parts of dh written
-    if (!OF_X && NP > 1 && pos > pos0)
-      for (int i = wave; i < 2 * RT; i += 8) {
-        f32x4_t d = red[0][i][lane];
-#pragma unroll
-        for (int k = 1; k < NP; ++k) d += red[OF_X ? 0 : k][i][lane];
-        put_dh(pos - kLgSlots, i, d);
-      }
+  // A step's tile goes to one of two buffers while slower waves still read the
+  // other, so a wave's next loads leave as soon as its last ones are here.
+  auto step = [&](int pos, int turn) {
+    uint8_t* wide = wides[turn];
+    auto& narrow = narrows[turn];
+    const lora_lds_u8* base = (const lora_lds_u8*)wide;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      *reinterpret_cast<u32x4_t*>(wide + srow * kRowB + 16 * lora_swz(srow, piece + 16 * i)) =
-          o.wide && c0 + 8 * (piece + 16 * i) < width ? o.v[i] : u32x4_t{0, 0, 0, 0};
+      *reinterpret_cast<u32x4_t*>(wide + srow * kRowB + 16 * lora_swz(srow, piece) + 256 * i) =
+          (o.live & 1) && (whole || c0 + 8 * (piece + 16 * i) < width) ? o.v[i] : u32x4_t{0, 0, 0, 0};
     if (OF_X || weights) {
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         const int r = 4 * nr + 64 * i;
         if (r >= RT * 16) continue;
-        const f32x4_t h = o.narrow && r < p.R ? (OF_X ? o.h[i] : o.h[i] * scale) : f32x4_t{0, 0, 0, 0};
+        const f32x4_t h = (o.live & 2) && r < p.R ? (OF_X ? o.h[i] : o.h[i] * scale) : f32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t term[3];
@@ -214,7 +253,7 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
         }
       }
     }
-    if (pos + kLgSlots < pos1) {
+    if (pos + kLgSlots < places) {
       load(pos + kLgSlots);
       load_ids(pos + 2 * kLgSlots);
     }
@@ -227,8 +266,9 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int t = 0; t < ST; ++t) {
-          const int m = 16 * (st + t) + m16, u = (np * (kLgCols / NP) + 32 * s) / 8 + q;
-          const u32x4_t rows = *reinterpret_cast<const u32x4_t*>(wide + m * kRowB + 16 * lora_swz(m, u));
+          const int m = 16 * (st + t) + m16, u = 4 * (s % (4 / NP) * NP + np) + q;
+          const u32x4_t rows =
+              *reinterpret_cast<const u32x4_t*>(wide + m * kRowB + 16 * lora_swz(m, u) + 256 * (s * NP / 4));
           d[t] = lora_mfma(bv[s], rows, d[t]);
         }
 #pragma unroll
@@ -244,14 +284,14 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         // column m16 of the tile at 8 slots from 8 q: two transposing reads of 4 slots
-        const int col = 16 * NC * wave + 16 * j + 4 * (m16 % 4);
+        const int col = 16 * wave + 4 * (m16 % 4);
         lora_s16x4 w[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int m = 8 * q + 4 * half + m16 / 4;
           w[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
               (__attribute__((address_space(3))) lora_s16x4*)(base + m * kRowB + 16 * lora_swz(m, col / 8) +
-                                                              2 * (col % 8)));
+                                                              2 * (col % 8) + 256 * j));
         }
         u32x4_t wv;
         __builtin_memcpy(&wv, w, 16);
@@ -262,11 +302,20 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
             acc[t][j] = lora_mfma(*reinterpret_cast<const u32x4_t*>(&narrow[k][16 * t + m16][8 * q]), wv, acc[t][j]);
       }
     }
+    if (!OF_X && NP > 1) {
+      __syncthreads();
+      for (int i = wave; i < 2 * RT; i += 8) {
+        f32x4_t d = red[0][i][lane];
+#pragma unroll
+        for (int k = 1; k < NP; ++k) d += red[OF_X ? 0 : k][i][lane];
+        put_dh(pos, i, d);
+      }
+    }
   };
   if (pos0 < pos1) {
-    load_ids(pos0);
-    load(pos0);
-    load_ids(pos0 + kLgSlots);
+    load_ids(0);
+    load(0);
+    load_ids(kLgSlots);
     // B of this wave's dh tiles, rank tile rt at its part of the columns: rows of
     // 16 ranks of the columns to LDS, where a rank tile after another is read
     // transposed
@@ -280,7 +329,7 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
           const int n = min(c0 + i / 2, width - 1), r = 16 * t + 8 * (i % 2);
           const u32x4_t v = *reinterpret_cast<const u32x4_t*>(p.b + (int64_t)g * p.b_g + (int64_t)n * p.b_ld +
                                                               min(r, p.R - 8));
-          *reinterpret_cast<u32x4_t*>(wide + 16 * i) = c0 + i / 2 < width && r < p.R ? v : u32x4_t{0, 0, 0, 0};
+          *reinterpret_cast<u32x4_t*>(wides[1] + 16 * i) = c0 + i / 2 < width && r < p.R ? v : u32x4_t{0, 0, 0, 0};
         }
         __syncthreads();
         if (t != rt) continue;
@@ -289,23 +338,17 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
           lora_s16x4 w[2];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int n = np * (kLgCols / NP) + 32 * k + 8 * q + 4 * half + m16 / 4;
+            const int n = 128 * (k * NP / 4) + 32 * (k % (4 / NP) * NP + np) + 8 * q + 4 * half + m16 / 4;
             w[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) lora_s16x4*)(base + n * 32 + 8 * (m16 % 4)));
+                (__attribute__((address_space(3))) lora_s16x4*)((const lora_lds_u8*)wides[1] + n * 32 + 8 * (m16 % 4)));
           }
           __builtin_memcpy(&bv[k], w, 16);
         }
       }
     }
-    for (int64_t pos = pos0; pos < pos1; pos += kLgSlots) step(pos);
-  }
-  if (!OF_X && NP > 1 && pos0 < pos1) {
-    __syncthreads();
-    for (int i = wave; i < 2 * RT; i += 8) {
-      f32x4_t d = red[0][i][lane];
-#pragma unroll
-      for (int k = 1; k < NP; ++k) d += red[OF_X ? 0 : k][i][lane];
-      put_dh(pos0 + (pos1 - pos0 - 1) / kLgSlots * kLgSlots, i, d);
+    for (int pos = 0; pos < places; pos += 2 * kLgSlots) {
+      step(pos, 0);
+      if (pos + kLgSlots < places) step(pos + kLgSlots, 1);
     }
   }
   if (!weights) return;
@@ -313,7 +356,7 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
   out += (int64_t)(slot < 0 ? g : slot) * p.R * width;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const int c = c0 + 16 * NC * wave + 16 * j + m16;
+    const int c = c0 + 128 * j + 16 * wave + m16;
     if (c >= width) continue;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -331,9 +374,8 @@ __global__ __launch_bounds__(kLgThreads) void lora_wide_kernel(LoraGradParams p)
 
 // The partial sums of groups of several segments, added in order.
 __global__ __launch_bounds__(kLoraThreads) void lora_grad_join_kernel(LoraGradParams p) {
-  if ((int)blockIdx.y >= p.table[0]) return;
-  const int32_t* e = p.table + 1 + (int64_t)blockIdx.y * kLgSegInts;
-  const int g = e[0], slot = e[3], segs = e[4];
+  const int32_t* e = p.table + p.max_segs * kLgSegInts + (int64_t)blockIdx.y * kLgJoinInts;
+  const int g = e[0], slot = e[1], segs = e[2];
   const int64_t na = (int64_t)p.R * p.K, nb = (int64_t)p.R * p.N;
   for (int64_t i = ((int64_t)blockIdx.x * kLoraThreads + threadIdx.x) * 4; segs > 0 && i < na + nb;
        i += (int64_t)gridDim.x * kLoraThreads * 4) {
@@ -352,8 +394,9 @@ LoraGradSizes lora_grad_sizes(int32_t G, int32_t R, int64_t K, int64_t N, int32_
   LoraGradSizes z{};
   const int64_t cols = lora_wide_cols(R), of_k = (K + cols - 1) / cols, of_n = (N + cols - 1) / cols;
   z.n_parts = (int32_t)of_n;
-  // about SEGW workgroups over both kernels where few groups would leave the chip idle
-  const int64_t want = (SEGW + of_k + of_n - 1) / (of_k + of_n);
+  // segments for about 512 workgroups over both kernels, where few groups would leave the chip idle (one
+  // group of 8192 slots, K = N = 4096: 89 us for the whole call, 120 at 2048 workgroups, whose partial sums cost more)
+  const int64_t want = (512 + of_k + of_n - 1) / (of_k + of_n);
   const int64_t per = (max_blocks + want - 1) / want;
   z.seg_blocks = (int32_t)(per > 1 ? per : 1);
   z.max_segs = (int32_t)(max_blocks / z.seg_blocks + G);
@@ -367,7 +410,7 @@ LoraGradSizes lora_grad_sizes(int32_t G, int32_t R, int64_t K, int64_t N, int32_
   };
   z.dh = take(z.n_parts * max_blocks * bm * R * 4);
   z.packed = take(max_blocks * bm * R * 4);
-  z.table = take((1 + (int64_t)z.max_segs * kLgSegInts) * 4);
+  z.table = take(((int64_t)z.max_segs * kLgSegInts + z.max_parts / 2 * kLgJoinInts) * 4);
   z.da_part = take((int64_t)z.max_parts * R * K * 4);
   z.db_part = take((int64_t)z.max_parts * R * N * 4);
   z.bytes = at;
@@ -396,7 +439,7 @@ hipError_t launch_lora_grad_join(const LoraGradParams& p, hipStream_t stream) {
   if (p.max_parts == 0) return hipSuccess;
   const int64_t quads = (int64_t)p.R * (p.K + p.N) / 4;
   const int64_t want = (quads + kLoraThreads - 1) / kLoraThreads;
-  hipLaunchKernelGGL(lora_grad_join_kernel, dim3((uint32_t)(want < 1024 ? want : 1024), p.max_segs),
+  hipLaunchKernelGGL(lora_grad_join_kernel, dim3((uint32_t)(want < 1024 ? want : 1024), p.max_parts / 2),
                      dim3(kLoraThreads), 0, stream, p);
   return hipGetLastError();
 }

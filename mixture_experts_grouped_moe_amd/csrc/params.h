@@ -238,7 +238,7 @@ struct LoraSizes {
 };
 LoraSizes lora_sizes(int32_t R, int64_t K, int32_t bm, int64_t max_blocks);
 hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream);
-hipError_t launch_lora_join(const LoraParams& p, bool all, hipStream_t stream);
+hipError_t launch_lora_join(const LoraParams& p, bool over, hipStream_t stream);
 hipError_t launch_lora_up(const LoraParams& p, bool turned, hipStream_t stream);
 hipError_t launch_lora_up_few(const LoraParams& p, hipStream_t stream);
 struct LoraGradSizes {
