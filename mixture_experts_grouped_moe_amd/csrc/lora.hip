@@ -27,20 +27,6 @@ __device__ __forceinline__ void lora_put_packed(uint16_t* packed, int64_t pos, i
   *reinterpret_cast<u32x2_t*>(to + R) = u32x2_t{lo[0], lo[1]};
 }
 
-// The parts of four ranks of a place, added in order.
-__device__ __forceinline__ f32x4_t lora_sum_parts(const float* at, int64_t step, int parts) {
-  f32x4_t h = {0, 0, 0, 0};
-  int k = 0;
-  for (; k + 4 <= parts; k += 4, at += 4 * step) {
-    f32x4_t v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const f32x4_t*>(at + j * step);
-    h = (((h + v[0]) + v[1]) + v[2]) + v[3];
-  }
-  for (; k < parts; ++k, at += step) h += *reinterpret_cast<const f32x4_t*>(at);
-  return h;
-}
-
 // ------------------------------------------------------------------- down
 
 // D rows are ranks, columns slots: a lane then holds 4 consecutive ranks of a
@@ -300,9 +286,10 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
   constexpr int NT = 8, kCols = 16 * NT;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
   const int run = blockIdx.x / p.n_splits, n0 = (blockIdx.x % p.n_splits * 4 + wave) * kCols;
-  const int b0 = p.block0 + run * p.run_blocks, b1 = min(b0 + p.run_blocks, p.max_blocks);
   if (n0 >= p.N) return;
-  const int per = p.bm <= 16 ? 1 : p.bm / 16, tiles = (b1 - b0) * per;  // tiles of a block, of the run
+  const int shift = p.bm <= 16 ? 0 : p.bm / 32;  // log2 of a block's tiles (1, 2 or 4)
+  const int t0 = (p.block0 << shift) + run * p.run_tiles;  // below 2^31 (as max_blocks * bm)
+  const int tiles = min(p.run_tiles, (p.max_blocks << shift) - t0);
   const bool in = n0 + NT * m16 < p.N;
   const int pieces = p.R / 8;
 
@@ -319,14 +306,14 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
     int group;
   };
   auto load_ids = [&](Ids& v, int t) {
-    const int b = b0 + t / per, row = 16 * (t % per) + 4 * q;
+    const int b = (t0 + t) >> shift, row = 16 * ((t0 + t) & ((1 << shift) - 1)) + 4 * q;
     const int32_t* at = p.sorted + (int64_t)b * p.bm;
     v.group = p.groups[b];
     v.first = at[0];
     __builtin_memcpy(v.slot, at + (row < p.bm ? row : 0), 16);
   };
   auto load = [&](Tile& v, const Ids& ids, int t) {
-    const int row = 16 * (t % per);
+    const int row = 16 * ((t0 + t) & ((1 << shift) - 1));
     v.group = __builtin_amdgcn_readfirstlane(ids.group);
     if ((uint32_t)v.group >= (uint32_t)p.G) return;
     const int first = (uint32_t)ids.first < (uint32_t)p.S ? ids.first : 0;
@@ -337,7 +324,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
       v.to[r] = live && in ? at : nullptr;
       v.c[r] = *reinterpret_cast<const u32x4_t*>(at);
     }
-    const int64_t pos = (int64_t)(b0 + t / per) * p.bm + min(row + m16, p.bm - 1);
+    const int64_t pos = (int64_t)((t0 + t) >> shift) * p.bm + min(row + m16, p.bm - 1);
     const uint16_t* at = p.packed + pos * (2 * p.R);
 #pragma unroll
     for (int f = 0; f < F; ++f)
@@ -456,11 +443,11 @@ LoraSizes lora_sizes(int32_t R, int64_t K, int32_t bm, int64_t max_blocks) {
 constexpr int64_t kLoraMaxGrid = 1 << 21;
 
 template <class F>
-static hipError_t lora_blocks(LoraParams p, int run, int per_run, F launch) {
-  const int64_t per = kLoraMaxGrid / per_run > 0 ? kLoraMaxGrid / per_run : 1, runs = (p.max_blocks + run - 1) / run;
-  for (int64_t r = 0; r < runs; r += per) {
-    p.block0 = (int32_t)(r * run);
-    launch(p, (uint32_t)((runs - r < per ? runs - r : per) * per_run));
+static hipError_t lora_blocks(LoraParams p, int per_block, F launch) {
+  const int64_t per = kLoraMaxGrid / per_block > 0 ? kLoraMaxGrid / per_block : 1;
+  for (int64_t b = 0; b < p.max_blocks; b += per) {
+    p.block0 = (int32_t)b;
+    launch(p, (uint32_t)((p.max_blocks - b < per ? p.max_blocks - b : per) * per_block));
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -473,7 +460,7 @@ hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream) {
     auto go = [&](auto mt) {
       constexpr int MT = decltype(mt)::value;
       const int y = p.bm <= 16 * MT ? 1 : p.bm / (16 * MT);
-      return lora_blocks(p, 1, p.splits, [&](const LoraParams& q, uint32_t grid) {
+      return lora_blocks(p, p.splits, [&](const LoraParams& q, uint32_t grid) {
         hipLaunchKernelGGL((lora_down_kernel<RT, MT>), dim3(grid, y), dim3(kLoraThreads), 0, stream, q);
       });
     };
@@ -494,16 +481,31 @@ hipError_t launch_lora_join(const LoraParams& p, bool over, hipStream_t stream) 
 hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream) {
   LoraParams p = p0;
   p.n_splits = (p.N + 511) / 512;
-  const int64_t all = (int64_t)p.max_blocks * p.n_splits;
-  // about 3072 workgroups: many more than run at once, so that they end together
-  // (32768 slots of 128 groups, 5760 columns: 180 us for the whole call, 184 at 1536)
-  p.run_blocks = (int32_t)(all / 3072 > 1 ? all / 3072 : 1);
+  const int per = p.bm <= 16 ? 1 : p.bm / 16;
+  const int64_t all = (int64_t)p.max_blocks * per * p.n_splits;  // tiles of 16 slots and 512 columns
+  // About 3072 workgroups: many more than run at once, so that they end together
+  // (32768 slots of 128 groups, 5760 columns: 180 us for the whole call, 184 at
+  // 1536), of whole blocks, whose slots are one group's (187 with 9 tiles in place
+  // of 8). With fewer tiles 4 a workgroup, which reads its columns of B for them,
+  // or what gives 512 workgroups (gradients of 1333 slots: 28.5 us, 31.6 at 4
+  // tiles; 4096 slots of rank 64: 35.8 us at 4, 39 at 2).
+  const int64_t share = all / 3072;
+  p.run_tiles = (int32_t)(share >= 8 ? share / per * per : share > 4 ? share : all / 512 > 4 ? 4 : all / 512 > 1 ? all / 512 : 1);
   return lora_rank(p.R, [&](auto rank) {
     constexpr int RC = decltype(rank)::value;
-    return lora_blocks(p, p.run_blocks, p.n_splits, [&](const LoraParams& q, uint32_t grid) {
+    // launches of whole blocks and whole runs
+    LoraParams q = p;
+    const int64_t runs = ((int64_t)p.max_blocks * per + p.run_tiles - 1) / p.run_tiles;
+    const int64_t most = kLoraMaxGrid / p.n_splits / per * per > 0 ? kLoraMaxGrid / p.n_splits / per * per : per;
+    for (int64_t r = 0; r < runs; r += most) {
+      q.block0 = (int32_t)(r * p.run_tiles / per);
+      const int64_t n = runs - r < most ? runs - r : most;
       auto kernel = turned ? lora_up_kernel<RC, true> : lora_up_kernel<RC, false>;
-      hipLaunchKernelGGL(kernel, dim3(grid), dim3(kLoraThreads), 0, stream, q);
-    });
+      hipLaunchKernelGGL(kernel, dim3((uint32_t)(n * p.n_splits)), dim3(kLoraThreads), 0, stream, q);
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
   });
 }
 
@@ -514,7 +516,7 @@ hipError_t launch_lora_up_few(const LoraParams& p0, hipStream_t stream) {
   const int64_t want = (512 + tiles - 1) / (tiles > 0 ? tiles : 1);
   p.n_splits = (int32_t)(want < most ? want : most);
   return lora_rank(p.R, [&](auto rank) {
-    return lora_blocks(p, 1, p.n_splits, [&](const LoraParams& q, uint32_t grid) {
+    return lora_blocks(p, p.n_splits, [&](const LoraParams& q, uint32_t grid) {
       hipLaunchKernelGGL(lora_up_few_kernel<decltype(rank)::value>, dim3(grid, y), dim3(kLoraThreads), 0, stream, q);
     });
   });

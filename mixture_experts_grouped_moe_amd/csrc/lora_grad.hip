@@ -382,9 +382,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_grad_join_kernel(LoraGradPa
     const bool of_a = i < na;
     const int64_t n = of_a ? na : nb, at = of_a ? i : i - na;
     const float* part = (of_a ? p.da_part : p.db_part) + slot * n + at;
-    f32x4_t a = {0, 0, 0, 0};
-    for (int k = 0; k < segs; ++k, part += n) a += *reinterpret_cast<const f32x4_t*>(part);
-    *reinterpret_cast<f32x4_t*>((of_a ? p.da : p.db) + g * n + at) = a;
+    *reinterpret_cast<f32x4_t*>((of_a ? p.da : p.db) + g * n + at) = lora_sum_parts(part, n, segs);
   }
 }
 

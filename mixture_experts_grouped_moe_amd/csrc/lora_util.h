@@ -54,6 +54,20 @@ __device__ __forceinline__ uint32_t lora_div(uint32_t s, uint32_t magic, int32_t
   return (uint32_t)(((uint64_t)s * magic) >> shift);
 }
 
+// The parts of four ranks of a place, added in order.
+__device__ __forceinline__ f32x4_t lora_sum_parts(const float* at, int64_t step, int parts) {
+  f32x4_t h = {0, 0, 0, 0};
+  int k = 0;
+  for (; k + 4 <= parts; k += 4, at += 4 * step) {
+    f32x4_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const f32x4_t*>(at + j * step);
+    h = (((h + v[0]) + v[1]) + v[2]) + v[3];
+  }
+  for (; k < parts; ++k, at += step) h += *reinterpret_cast<const f32x4_t*>(at);
+  return h;
+}
+
 // Rank r in the kernels: padded to 8, 16, 32, 64 or 128.
 template <class F>
 inline hipError_t lora_rank(int r, F f) {

@@ -163,7 +163,7 @@ struct LoraParams {
   int64_t w_g, w_ld;
   float* part;       // h in parts of K, [splits][places][R]
   uint16_t* packed;  // h as the large `up` takes it, [places][2][R] bf16
-  int32_t splits, n_splits, run_blocks;
+  int32_t splits, n_splits, run_tiles;
   float* h;  // [S][R], or null
   uint16_t* c;
   int64_t c_ld;
