@@ -21,6 +21,8 @@ projections of the batch (group = adapter; or adapter * E + expert):
 """
 
 import ctypes
+import functools
+import struct
 
 import torch
 
@@ -83,31 +85,57 @@ class MoeLoraBackwardArgs(ctypes.Structure):
     ]
 
 
+# Calls on small inputs are bound by the host: the argument structs are packed as
+# bytes (a ctypes structure takes 2 us more), and sizes of workspaces are kept.
+_CODES = {_i64: "q", _i32: "i", _f32: "f", _vp: "P"}
+
+
+def _packer(mirror):
+    """mirror(*values) as bytes, the native layout of its fields."""
+    form = struct.Struct("@" + "".join(_CODES[t] for _, t in mirror._fields_))
+    assert form.size <= ctypes.sizeof(mirror) < form.size + 8
+    tail = bytes(ctypes.sizeof(mirror) - form.size)
+    return form.pack if not tail else lambda *values: form.pack(*values) + tail
+
+
+_pack_norm, _pack_norm_backward = _packer(MoeRmsnormArgs), _packer(MoeRmsnormBackwardArgs)
+_pack_lora, _pack_lora_backward = _packer(MoeLoraArgs), _packer(MoeLoraBackwardArgs)
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
 def _bind():
+    args = ctypes.c_char_p
     sig = {
         "moe_dropout": (_i32, [_vp, _i64, _i64, _i64, _f32, _vp, _vp, _i64, _vp]),
-        "moe_rmsnorm": (_i32, [ctypes.POINTER(MoeRmsnormArgs), _vp]),
-        "moe_rmsnorm_backward": (_i32, [ctypes.POINTER(MoeRmsnormBackwardArgs), _vp]),
+        "moe_rmsnorm": (_i32, [args, _vp]),
+        "moe_rmsnorm_backward": (_i32, [args, _vp]),
         "moe_rmsnorm_backward_workspace_bytes": (_i64, [_i64, _i64]),
-        "moe_lora": (_i32, [ctypes.POINTER(MoeLoraArgs), _vp]),
-        "moe_lora_backward": (_i32, [ctypes.POINTER(MoeLoraBackwardArgs), _vp]),
+        "moe_lora": (_i32, [args, _vp]),
+        "moe_lora_backward": (_i32, [args, _vp]),
         "moe_lora_block_m": (_i32, [_i64, _i32]),
         "moe_lora_workspace_bytes": (_i64, [_i64, _i32, _i32, _i64, _i64, _i32, _i64]),
         "moe_lora_backward_workspace_bytes": (_i64, [_i64, _i32, _i32, _i64, _i64, _i32, _i64]),
     }
-    for name, (res, args) in sig.items():
+    for name, (res, types) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
-        fn.argtypes = args
+        fn.argtypes = types
 
 
 _bind()
 
+_norm_backward_bytes = functools.lru_cache(maxsize=4096)(lib.moe_rmsnorm_backward_workspace_bytes)
+_lora_bytes = functools.lru_cache(maxsize=4096)(lib.moe_lora_workspace_bytes)
+_lora_backward_bytes = functools.lru_cache(maxsize=4096)(lib.moe_lora_backward_workspace_bytes)
+
 
 def _rng(rng):
-    """The address of a dropout's {seed, offset}; None without one."""
+    """The address of a dropout's {seed, offset}; 0 without one."""
     if rng is None:
-        return None
+        return 0
     _flat(rng, "rng", torch.int64, (2,))
     return rng.data_ptr()
 
@@ -117,6 +145,18 @@ def _wide(t, name):
     if not isinstance(t, torch.Tensor) or t.dtype not in _WIDE:
         raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
     return _WIDE[t.dtype]
+
+
+def _workspace(workspace, need, like):
+    """The address and size of the caller's workspace, or of a new one."""
+    if workspace is None:
+        if need <= 0:
+            return 0, 0, None  # (the call says what is wrong with the sizes)
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1)
+        _same_device(like, workspace)
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 @_on_stream
@@ -155,7 +195,7 @@ def moe_rmsnorm(x, weight, residual=None, eps=1e-6, p=0.0, rng=None, quant=None,
     T, n, xld = _mat(x, "x", torch.bfloat16)
     kind, wd = _QUANTS[quant], _wide(weight, "weight")
     _flat(weight, "weight", weight.dtype, (n,))
-    rd, rld, res_p = MOE_BF16, 0, None
+    rd, rld, res_p = MOE_BF16, 0, 0
     if residual is not None:
         rd = _wide(residual, "residual")
         rld, res_p = _mat(residual, "residual", residual.dtype, T, n)[2], residual.data_ptr()
@@ -192,10 +232,9 @@ def moe_rmsnorm(x, weight, residual=None, eps=1e-6, p=0.0, rng=None, quant=None,
                 _flat(s, "scales", torch.float32, (T,))
     rng_p = _rng(rng)
     _same_device(x, weight, residual, rng, y, v, q, s)
-    _check(lib.moe_rmsnorm(ctypes.byref(MoeRmsnormArgs(
-        T, n, x.data_ptr(), xld, p, rng_p, res_p, rld, rd, v.data_ptr() if v is not None else None, vld,
-        weight.data_ptr(), wd, eps, y.data_ptr() if y is not None else None, yld, kind,
-        q.data_ptr() if kind else None, qld, s.data_ptr() if kind else None, sld)), _stream(x)))
+    _check(lib.moe_rmsnorm(_pack_norm(
+        T, n, x.data_ptr(), xld, p, rng_p, res_p, rld, rd, _ptr(v), vld, weight.data_ptr(), wd, eps, _ptr(y), yld, kind,
+        _ptr(q), qld, _ptr(s), sld), _stream(x)))
     return y, v, q, s
 
 
@@ -242,21 +281,14 @@ def moe_rmsnorm_backward(dy, sum, weight, dsum=None, eps=1e-6, p=0.0, rng=None, 
             drld = _mat(dres, "dresidual", sum.dtype, T, n)[2]
         if dw is not None:
             _flat(dw, "dweight", torch.float32, (n,))
-    ws_p, ws_n = None, 0
+    ws_p = ws_n = 0
     if dw is not None:
-        if workspace is None:
-            workspace = torch.empty(max(moe_rmsnorm_backward_workspace_bytes(T, n), 0), dtype=torch.uint8,
-                                    device=dy.device)
-        else:
-            _need(workspace, "workspace", torch.uint8, 1)
-        ws_p, ws_n = workspace.data_ptr(), workspace.numel()
+        ws_p, ws_n, workspace = _workspace(workspace, _norm_backward_bytes(T, n) if workspace is None else 0, dy)
     rng_p = _rng(rng)
-    _same_device(dy, sum, weight, dsum, rng, dx, dres, dw, workspace)
-    _check(lib.moe_rmsnorm_backward(ctypes.byref(MoeRmsnormBackwardArgs(
-        T, n, dy.data_ptr(), gld, dsum.data_ptr() if dsum is not None else None, dsld, sum.data_ptr(), vld, sd,
-        weight.data_ptr(), wd, eps, p, rng_p, dres.data_ptr() if dres is not None else None, drld,
-        dx.data_ptr() if dx is not None else None, dxld, dw.data_ptr() if dw is not None else None, ws_p, ws_n)),
-        _stream(dy)))
+    _same_device(dy, sum, weight, dsum, rng, dx, dres, dw)
+    _check(lib.moe_rmsnorm_backward(_pack_norm_backward(
+        T, n, dy.data_ptr(), gld, _ptr(dsum), dsld, sum.data_ptr(), vld, sd, weight.data_ptr(), wd, eps, p, rng_p,
+        _ptr(dres), drld, _ptr(dx), dxld, _ptr(dw), ws_p, ws_n), _stream(dy)))
     return result
 
 
@@ -299,31 +331,18 @@ def _lora_args(x, a, b, routing, scale, row_div, S, N):
     x_ld = _mat(x, "x", torch.bfloat16, -(-S // div), K)[2]
     ids, groups = routing[0], routing[1]
     for t, name in ((ids, "sorted_slot_ids"), (groups, "group_ids")):
-        _need(t, name, torch.int32, 1)
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
+            _need(t, name, torch.int32, 1)
     blocks = groups.numel()
     bm = ids.numel() // blocks if blocks else moe_lora_block_m(S, G)
     if bm * blocks != ids.numel():
         raise ValueError("the routing's arrays do not belong together")
-    scale_p = None
     if scale is not None:
         _flat(scale, "scale", torch.float32, (G,))
-        scale_p = scale.data_ptr()
     _same_device(x, a, b, ids, groups, scale)
     sizes = S, G, R, K, N
-    return sizes, (x.data_ptr(), x_ld, div, a.data_ptr(), a_g, a_ld, b.data_ptr(), b_g, b_ld, scale_p, ids.data_ptr(),
+    return sizes, (x.data_ptr(), x_ld, div, a.data_ptr(), a_g, a_ld, b.data_ptr(), b_g, b_ld, _ptr(scale), ids.data_ptr(),
                    groups.data_ptr(), bm, blocks)
-
-
-def _workspace(workspace, need, like):
-    """The address and size of the caller's workspace, or of a new one."""
-    if workspace is None:
-        if need < 0:
-            return None, 0, None  # (the call says what is wrong with the sizes)
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-    else:
-        _need(workspace, "workspace", torch.uint8, 1)
-        _same_device(like, workspace)
-    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 @_on_stream
@@ -342,11 +361,9 @@ def moe_lora(c, x, a, b, routing, scale=None, row_div=1, keep_h=False, workspace
     S, N, c_ld = _mat(c, "c", torch.bfloat16)
     sizes, args = _lora_args(x, a, b, routing, scale, row_div, S, N)
     h = torch.empty((S, sizes[2]), dtype=torch.float32, device=c.device) if keep_h else None
-    need = 0 if workspace is not None else lib.moe_lora_workspace_bytes(*sizes, *args[-2:])
-    ws_p, ws_n, ws = _workspace(workspace, need, c)
+    ws_p, ws_n, ws = _workspace(workspace, _lora_bytes(*sizes, *args[-2:]) if workspace is None else 0, c)
     _same_device(c, x)
-    _check(lib.moe_lora(ctypes.byref(MoeLoraArgs(*sizes, *args, c.data_ptr(), c_ld, h.data_ptr() if keep_h else None,
-                                                 ws_p, ws_n)), _stream(c)))
+    _check(lib.moe_lora(_pack_lora(*sizes, *args, c.data_ptr(), c_ld, _ptr(h), ws_p, ws_n), _stream(c)))
     return (c, h) if keep_h else c
 
 
@@ -364,11 +381,9 @@ def moe_lora_backward(dy, x, a, b, routing, h, scale=None, row_div=1, dx=None, w
     S, N, dy_ld = _mat(dy, "dy", torch.bfloat16)
     sizes, args = _lora_args(x, a, b, routing, scale, row_div, S, N)
     _, G, R, K, _ = sizes
-    h_p = da_p = db_p = dx_p = da = db = None
-    dx_ld = 0
+    da = db = None
     if weights:
         _flat(h, "h", torch.float32, (S, R))
-        h_p = h.data_ptr()
         if out is None:
             da = torch.empty((G, R, K), dtype=torch.float32, device=dy.device)
             db = torch.empty((G, N, R), dtype=torch.float32, device=dy.device)
@@ -376,12 +391,11 @@ def moe_lora_backward(dy, x, a, b, routing, h, scale=None, row_div=1, dx=None, w
             da, db = out
             _flat(da, "da", torch.float32, (G, R, K))
             _flat(db, "db", torch.float32, (G, N, R))
-        da_p, db_p = da.data_ptr(), db.data_ptr()
-    if dx is not None:
-        dx_ld, dx_p = _mat(dx, "dx", torch.bfloat16, S, K)[2], dx.data_ptr()
-    need = 0 if workspace is not None else lib.moe_lora_backward_workspace_bytes(*sizes, *args[-2:])
-    ws_p, ws_n, ws = _workspace(workspace, need, dy)
-    _same_device(dy, x, h if weights else None, dx, da, db)
-    _check(lib.moe_lora_backward(ctypes.byref(MoeLoraBackwardArgs(
-        *sizes, dy.data_ptr(), dy_ld, *args, h_p, dx_p, dx_ld, da_p, db_p, ws_p, ws_n)), _stream(dy)))
+    else:
+        h = None
+    dx_ld = _mat(dx, "dx", torch.bfloat16, S, K)[2] if dx is not None else 0
+    ws_p, ws_n, ws = _workspace(workspace, _lora_backward_bytes(*sizes, *args[-2:]) if workspace is None else 0, dy)
+    _same_device(dy, x, h, dx, da, db)
+    _check(lib.moe_lora_backward(_pack_lora_backward(
+        *sizes, dy.data_ptr(), dy_ld, *args, _ptr(h), _ptr(dx), dx_ld, _ptr(da), _ptr(db), ws_p, ws_n), _stream(dy)))
     return da, db

@@ -335,6 +335,12 @@ moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream) {
   char* base = static_cast<char*>(args->workspace);
   p.splits = z.splits;
   p.h = args->h;
+  p.w2 = static_cast<const uint16_t*>(a.b);
+  p.w2_g = a.b_stride_g;
+  p.w2_ld = a.b_ld;
+  p.c = static_cast<uint16_t*>(args->c);
+  p.c_ld = args->c_ld;
+  if (z.both) return hip_status(moe::launch_lora_both(p, (hipStream_t)stream), "moe_lora launch");
   p.part = reinterpret_cast<float*>(base);
   if (!z.few && z.splits == 1) p.packed = reinterpret_cast<uint16_t*>(base + z.packed);
   st = hip_status(moe::launch_lora_down(p, (hipStream_t)stream), "moe_lora launch");
@@ -344,11 +350,6 @@ moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream) {
     st = hip_status(moe::launch_lora_join(p, false, (hipStream_t)stream), "moe_lora launch");
     if (st != MOE_OK) return st;
   }
-  p.w = static_cast<const uint16_t*>(a.b);
-  p.w_g = a.b_stride_g;
-  p.w_ld = a.b_ld;
-  p.c = static_cast<uint16_t*>(args->c);
-  p.c_ld = args->c_ld;
   return hip_status(z.few ? moe::launch_lora_up_few(p, (hipStream_t)stream)
                           : moe::launch_lora_up(p, false, (hipStream_t)stream),
                     "moe_lora launch");
@@ -429,9 +430,9 @@ moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t st
   if (err == hipSuccess) err = moe::launch_lora_join(p, true, on);
   if (err == hipSuccess && args->dx != nullptr) {
     p.N = (int32_t)a.K;
-    p.w = static_cast<const uint16_t*>(a.a);
-    p.w_g = a.a_stride_g;
-    p.w_ld = a.a_ld;
+    p.w2 = static_cast<const uint16_t*>(a.a);
+    p.w2_g = a.a_stride_g;
+    p.w2_ld = a.a_ld;
     p.c = static_cast<uint16_t*>(args->dx);
     p.c_ld = args->dx_ld;
     err = moe::launch_lora_up(p, true, on);

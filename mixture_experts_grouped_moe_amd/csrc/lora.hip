@@ -32,38 +32,26 @@ __device__ __forceinline__ void lora_put_packed(uint16_t* packed, int64_t pos, i
 // D rows are ranks, columns slots: a lane then holds 4 consecutive ranks of a
 // slot, one 16-byte store. The waves take K in turn, whole cache lines of x at a
 // time, operands straight from memory in MFMA layout, the next ones on their way
-// during the products, and add their sums through LDS. Loads are not masked: a
-// place without a slot reads the block's first row, a rank past R the last one,
-// and their rows and columns of D are not stored.
-template <int RT, int MT>
-__global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
+// during the products, and add their sums through LDS, into wave 0's. Loads are
+// not masked: a place without a slot reads the block's first row, a rank past R
+// the last one, and their rows and columns of D are not stored. `slot`: of each
+// tile's place m16; part `sp` of `splits` of K.
+template <int W, int RT, int MT>
+__device__ __forceinline__ void lora_down(const LoraParams& p, int g, const uint32_t (&slot)[MT],
+                                          const bool (&live)[MT], uint32_t spare, int sp, int splits,
+                                          f32x4_t (&red)[W / 2][RT * MT][64], f32x4_t (&acc)[RT][MT]) {
   constexpr int U = RT + MT <= 2 ? 4 : RT >= 4 ? 1 : 2;  // steps of 32 columns of a turn
   constexpr int kTurn = 32 * U;
-  __shared__ f32x4_t red[2][RT * MT][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
-  const int b = p.block0 + blockIdx.x / p.splits, sp = blockIdx.x % p.splits;
-  const int g = p.groups[b];
-  const int row0 = blockIdx.y * MT * 16;
-  const int32_t* ids = p.sorted + (int64_t)b * p.bm;
-  const uint32_t first = (uint32_t)ids[0];
-  uint32_t slot[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) slot[m] = (uint32_t)ids[min(row0 + 16 * m + m16, p.bm - 1)];
-  if ((uint32_t)g >= (uint32_t)p.G) return;
   const uint16_t* xr[MT];
-  bool live[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    live[m] = row0 + 16 * m + m16 < p.bm && slot[m] < (uint32_t)p.S;
-    const uint32_t s = live[m] ? slot[m] : first < (uint32_t)p.S ? first : 0;
-    xr[m] = p.x + (int64_t)lora_div(s, p.div_magic, p.div_shift) * p.x_ld + 8 * q;
-  }
+  for (int m = 0; m < MT; ++m)
+    xr[m] = p.x + (int64_t)lora_div(live[m] ? slot[m] : spare, p.div_magic, p.div_shift) * p.x_ld + 8 * q;
   const uint16_t* wr[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t)
     wr[t] = p.w + (int64_t)g * p.w_g + (int64_t)min(16 * t + m16, p.R - 1) * p.w_ld + 8 * q;
-  f32x4_t acc[RT][MT];
-#pragma unroll
+  #pragma unroll
   for (int t = 0; t < RT; ++t)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0, 0, 0, 0};
@@ -88,19 +76,19 @@ __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[t][m] = lora_mfma(v.w[u][t], v.x[u][m], acc[t][m]);
   };
-  const int turns = p.K / kTurn, per = (turns + p.splits - 1) / p.splits;
+  const int turns = p.K / kTurn, per = (turns + splits - 1) / splits;
   const int end = min(turns, (sp + 1) * per);
   Turn v, next;
   int i = sp * per + wave;
   if (i < end) load(v, i);
-  for (; i + 4 < end; i += 8) {
-    load(next, i + 4);
+  for (; i + W < end; i += 2 * W) {
+    load(next, i + W);
     add(v);
-    if (i + 8 < end) load(v, i + 8);
+    if (i + 2 * W < end) load(v, i + 2 * W);
     add(next);
   }
   if (i < end) add(v);
-  if (kTurn * turns < p.K && sp == p.splits - 1 && wave == 0) {  // the columns behind the last whole turn
+  if (kTurn * turns < p.K && sp == splits - 1 && wave == 0) {  // the columns behind the last whole turn
     Turn z = {};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -115,7 +103,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
   }
   // the waves' sums: the upper half's into the lower half's, and so on
 #pragma unroll
-  for (int half = 2; half > 0; half /= 2) {
+  for (int half = W / 2; half > 0; half /= 2) {
     if (wave >= half && wave < 2 * half)
 #pragma unroll
       for (int t = 0; t < RT; ++t)
@@ -129,6 +117,26 @@ __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
         for (int m = 0; m < MT; ++m) acc[t][m] += red[wave][t * MT + m][lane];
     if (half > 1) __syncthreads();
   }
+}
+
+template <int RT, int MT>
+__global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
+  __shared__ f32x4_t red[2][RT * MT][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
+  const int b = p.block0 + blockIdx.x / p.splits, sp = blockIdx.x % p.splits;
+  const int g = p.groups[b];
+  const int row0 = blockIdx.y * MT * 16;
+  const int32_t* ids = p.sorted + (int64_t)b * p.bm;
+  const uint32_t first = (uint32_t)ids[0];
+  uint32_t slot[MT];
+  bool live[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) slot[m] = (uint32_t)ids[min(row0 + 16 * m + m16, p.bm - 1)];
+  if ((uint32_t)g >= (uint32_t)p.G) return;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) live[m] = row0 + 16 * m + m16 < p.bm && slot[m] < (uint32_t)p.S;
+  f32x4_t acc[RT][MT];
+  lora_down<4, RT, MT>(p, g, slot, live, first < (uint32_t)p.S ? first : 0, sp, p.splits, red, acc);
   if (wave > 0) return;
   const float scale = p.packed != nullptr && p.scale != nullptr ? p.scale[g] : 1.0f;
 #pragma unroll
@@ -173,33 +181,31 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraParams p, b
 // D rows are columns of C, D columns slots. Row i of tile j stands for column
 // 32 (j / 2) + 8 (i / 4) + 4 (j % 2) + i % 4 of a 64-column piece, so that a lane
 // holds twice 8 consecutive columns of one slot: one tile of 16 slots then
-// spreads over four times the waves that `up` would use. h enters as there. A
-// wave's first piece of C and B is on its way while the parts of h are summed.
+// spreads over four times the waves that `up` would use. h enters as there.
+// Loads are not masked, as in `down`. (The first piece of C and B is on its way
+// while h is made.)
 template <int RC>
-__global__ __launch_bounds__(kLoraThreads) void lora_up_few_kernel(LoraParams p) {
-  constexpr int F = RC < 4 ? 1 : RC / 4, P = RC < 4 ? 1 : 2;
-  constexpr int kRank = RC < 4 ? 16 : 8 * RC, kLd = kRank + 8;  // of a slot's row of h in LDS
-  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][kLd];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
-  const int b = p.block0 + blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
-  const int g = p.groups[b];
-  if ((uint32_t)g >= (uint32_t)p.G) return;
-  const int row0 = blockIdx.y * 16, rows = min(16, p.bm - row0);
-  const int64_t pos0 = (int64_t)b * p.bm + row0;
-  const int32_t* ids = p.sorted + pos0;
-  const int pieces = p.R / 8;
-  const uint32_t slot = (uint32_t)ids[min(m16, rows - 1)], first = (uint32_t)p.sorted[(int64_t)b * p.bm];
-  const bool live = m16 < rows && slot < (uint32_t)p.S;
-  uint16_t* cr = p.c + (int64_t)(live ? slot : first < (uint32_t)p.S ? first : 0) * p.c_ld;
-  const uint16_t* wr = p.w + (int64_t)g * p.w_g;
-  const int chunks = (p.N + 63) / 64, per = (chunks + p.n_splits - 1) / p.n_splits;
-  const int end = min(chunks, (sp + 1) * per);
-  u32x4_t cv[2], wv[4][F];
-  auto load = [&](int i) {
-    const int n0 = 64 * i;
+struct LoraFew {
+  static constexpr int F = RC < 4 ? 1 : RC / 4, P = RC < 4 ? 1 : 2;
+  static constexpr int kRank = RC < 4 ? 16 : 8 * RC, kLd = kRank + 8;  // of a slot's row of h in LDS
+  u32x4_t c[2], w[4][F];
+  uint16_t* row;
+  const uint16_t* matrix;
+  int lane, q, m16;
+  bool live;
+
+  __device__ __forceinline__ LoraFew(const LoraParams& p, int g, uint32_t slot, bool live_, uint32_t spare)
+      : live(live_) {
+    lane = threadIdx.x % 64;
+    q = lane / 16;
+    m16 = lane % 16;
+    row = p.c + (int64_t)(live ? slot : spare) * p.c_ld;
+    matrix = p.w2 + (int64_t)g * p.w2_g;
+  }
+  __device__ __forceinline__ void load(const LoraParams& p, int i) {
+    const int n0 = 64 * i, pieces = p.R / 8;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      cv[e] = *reinterpret_cast<const u32x4_t*>(cr + min(n0 + 32 * e + 8 * q, p.N - 8));
+    for (int e = 0; e < 2; ++e) c[e] = *reinterpret_cast<const u32x4_t*>(row + min(n0 + 32 * e + 8 * q, p.N - 8));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = min(n0 + 32 * (j / 2) + 8 * (m16 / 4) + 4 * (j % 2) + m16 % 4, p.N - 1);
@@ -207,64 +213,125 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_few_kernel(LoraParams p)
       for (int f = 0; f < F; ++f) {
         const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
         const bool in = piece < pieces && (RC != 1 || q < 2);
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(wr + (int64_t)n * p.w_ld + (in ? 8 * piece : 0));
-        wv[j][f] = in ? v : u32x4_t{0, 0, 0, 0};
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(matrix + (int64_t)n * p.w2_ld + (in ? 8 * piece : 0));
+        w[j][f] = in ? v : u32x4_t{0, 0, 0, 0};
       }
     }
-  };
-  int i = sp * per + wave;
-  if (i < end) load(i);
+  }
+  // Four ranks of a place to LDS.
+  __device__ __forceinline__ static void put(uint16_t (&hs)[2][16][kLd], int place, int r, f32x4_t h) {
+    uint32_t hi[2], lo[2];
+    lora_split(h[0], h[1], hi[0], lo[0]);
+    lora_split(h[2], h[3], hi[1], lo[1]);
+    *reinterpret_cast<u32x2_t*>(&hs[0][place][r]) = u32x2_t{hi[0], hi[1]};
+    *reinterpret_cast<u32x2_t*>(&hs[1][place][r]) = u32x2_t{lo[0], lo[1]};
+  }
+  // Adds the pieces i, i + step, ... below end, the first of which is loaded.
+  __device__ __forceinline__ void add(const LoraParams& p, uint16_t (&hs)[2][16][kLd], int i, int step, int end) {
+    u32x4_t h[F][P];
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0, part = RC >= 4 ? k : RC == 2 ? q / 2 : q % 2;
+        h[f][k] = *reinterpret_cast<const u32x4_t*>(&hs[part][m16][8 * piece]);
+        if (RC == 1 && q >= 2) h[f][k] = u32x4_t{0, 0, 0, 0};
+      }
+    for (; i < end; i += step) {
+      const int n0 = 64 * i;
+      f32x4_t d[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[j] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+          for (int k = 0; k < P; ++k) d[j] = lora_mfma(w[j][f], h[f][k], d[j]);
+      }
+      const u32x4_t now[2] = {c[0], c[1]};
+      if (i + step < end) load(p, i + step);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        u32x4_t o;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          o[v] = lora_pack(__uint_as_float(now[e][v] << 16) + d[2 * e + v / 2][2 * (v % 2)],
+                           __uint_as_float(now[e][v] & 0xffff0000u) + d[2 * e + v / 2][2 * (v % 2) + 1]);
+        const int n = n0 + 32 * e + 8 * q;
+        if (live && n < p.N) *reinterpret_cast<u32x4_t*>(row + n) = o;
+      }
+    }
+  }
+};
 
-  // h: four ranks a thread
+// From the parts of h.
+template <int RC>
+__global__ __launch_bounds__(kLoraThreads) void lora_up_few_kernel(LoraParams p) {
+  using Few = LoraFew<RC>;
+  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][Few::kLd];
+  const int wave = threadIdx.x / 64, m16 = threadIdx.x % 16;
+  const int b = p.block0 + blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
+  const int g = p.groups[b];
+  const int row0 = blockIdx.y * 16, rows = min(16, p.bm - row0);
+  const int64_t pos0 = (int64_t)b * p.bm + row0;
+  const int32_t* ids = p.sorted + pos0;
+  const uint32_t slot = (uint32_t)ids[min(m16, rows - 1)], first = (uint32_t)p.sorted[(int64_t)b * p.bm];
+  if ((uint32_t)g >= (uint32_t)p.G) return;
+  Few few(p, g, slot, m16 < rows && slot < (uint32_t)p.S, first < (uint32_t)p.S ? first : 0);
+  const int chunks = (p.N + 63) / 64, per = (chunks + p.n_splits - 1) / p.n_splits;
+  const int end = min(chunks, (sp + 1) * per), i = sp * per + wave;
+  if (i < end) few.load(p, i);
   const float scale = p.scale != nullptr ? p.scale[g] : 1.0f;
-  for (int t = threadIdx.x; t < 16 * (kRank / 4); t += kLoraThreads) {
-    const int row = t / (kRank / 4), r = t % (kRank / 4) * 4;
+  for (int t = threadIdx.x; t < 16 * (Few::kRank / 4); t += kLoraThreads) {  // four ranks a thread
+    const int row = t / (Few::kRank / 4), r = t % (Few::kRank / 4) * 4;
     const uint32_t s = row < rows ? (uint32_t)ids[row] : 0xFFFFFFFFu;
     f32x4_t h = {0, 0, 0, 0};
     if (s < (uint32_t)p.S && r < p.R) {
       h = lora_sum_parts(p.part + (pos0 + row) * p.R + r, (int64_t)p.max_blocks * p.bm * p.R, p.splits);
       if (p.h != nullptr && sp == 0) *reinterpret_cast<f32x4_t*>(p.h + (int64_t)s * p.R + r) = h;
     }
-    uint32_t hi[2], lo[2];
-    lora_split(h[0] * scale, h[1] * scale, hi[0], lo[0]);
-    lora_split(h[2] * scale, h[3] * scale, hi[1], lo[1]);
-    *reinterpret_cast<u32x2_t*>(&hs[0][row][r]) = u32x2_t{hi[0], hi[1]};
-    *reinterpret_cast<u32x2_t*>(&hs[1][row][r]) = u32x2_t{lo[0], lo[1]};
+    Few::put(hs, row, r, h * scale);
   }
   __syncthreads();
-  u32x4_t hv[F][P];
-#pragma unroll
-  for (int f = 0; f < F; ++f)
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0, part = RC >= 4 ? k : RC == 2 ? q / 2 : q % 2;
-      hv[f][k] = *reinterpret_cast<const u32x4_t*>(&hs[part][m16][8 * piece]);
-      if (RC == 1 && q >= 2) hv[f][k] = u32x4_t{0, 0, 0, 0};
-    }
+  few.add(p, hs, i, 4, end);
+}
 
-  for (; i < end; i += 4) {
-    const int n0 = 64 * i;
-    f32x4_t d[4];
+// Both products in one launch: every workgroup of a tile forms its h, by 8 waves
+// over K, and adds to its part of N.
+template <int RC>
+__global__ __launch_bounds__(512) void lora_both_kernel(LoraParams p) {
+  using Few = LoraFew<RC>;
+  constexpr int RT = (RC + 1) / 2;
+  __shared__ f32x4_t red[4][RT][64];
+  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][Few::kLd];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
+  const int b = p.block0 + blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
+  const int g = p.groups[b];
+  const int row0 = blockIdx.y * 16, rows = min(16, p.bm - row0);
+  const int32_t* ids = p.sorted + (int64_t)b * p.bm + row0;
+  const uint32_t slot[1] = {(uint32_t)ids[min(m16, rows - 1)]}, first = (uint32_t)p.sorted[(int64_t)b * p.bm];
+  if ((uint32_t)g >= (uint32_t)p.G) return;
+  const bool live[1] = {m16 < rows && slot[0] < (uint32_t)p.S};
+  const uint32_t spare = first < (uint32_t)p.S ? first : 0;
+  Few few(p, g, slot[0], live[0], spare);
+  const int chunks = (p.N + 63) / 64, per = (chunks + p.n_splits - 1) / p.n_splits;
+  const int end = min(chunks, (sp + 1) * per), i = sp * per + wave;
+  if (i < end) few.load(p, i);
+  f32x4_t acc[RT][1];
+  lora_down<8, RT, 1>(p, g, slot, live, spare, 0, 1, red, acc);
+  if (wave == 0) {
+    const float scale = p.scale != nullptr ? p.scale[g] : 1.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      d[j] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int f = 0; f < F; ++f)
-#pragma unroll
-        for (int k = 0; k < P; ++k) d[j] = lora_mfma(wv[j][f], hv[f][k], d[j]);
-    }
-    const u32x4_t cn[2] = {cv[0], cv[1]};
-    if (i + 4 < end) load(i + 4);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      u32x4_t o;
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        o[w] = lora_pack(__uint_as_float(cn[e][w] << 16) + d[2 * e + w / 2][2 * (w % 2)],
-                         __uint_as_float(cn[e][w] & 0xffff0000u) + d[2 * e + w / 2][2 * (w % 2) + 1]);
-      if (live && n0 + 32 * e + 8 * q < p.N) *reinterpret_cast<u32x4_t*>(cr + n0 + 32 * e + 8 * q) = o;
+    for (int t = 0; t < RT; ++t) {
+      const int r = 16 * t + 4 * q;
+      const bool in = live[0] && r < p.R;
+      if (in && p.h != nullptr && sp == 0)
+        *reinterpret_cast<f32x4_t*>(p.h + (int64_t)slot[0] * p.R + r) = acc[t][0];
+      Few::put(hs, m16, r, in ? acc[t][0] * scale : f32x4_t{0, 0, 0, 0});
     }
   }
+  __syncthreads();
+  few.add(p, hs, i, 8, end);
 }
 
 // --------------------------------------------------------------------- up
@@ -341,7 +408,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
   auto matrix = [&](int group) {
     if (group != have && (uint32_t)group < (uint32_t)p.G) {
       have = group;
-      const uint16_t* wr = p.w + (int64_t)have * p.w_g;
+      const uint16_t* wr = p.w2 + (int64_t)have * p.w2_g;
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
@@ -350,8 +417,8 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const int rank = here ? 8 * piece : 0;
-          w[j] = *reinterpret_cast<const u32x4_t*>(TURNED ? wr + (int64_t)(rank + j) * p.w_ld + col
-                                                          : wr + (int64_t)(col + j) * p.w_ld + rank);
+          w[j] = *reinterpret_cast<const u32x4_t*>(TURNED ? wr + (int64_t)(rank + j) * p.w2_ld + col
+                                                          : wr + (int64_t)(col + j) * p.w2_ld + rank);
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -427,9 +494,20 @@ int lora_k_splits(int64_t max_blocks, int64_t k) {
   return (int)(n < 32 ? n : 32);
 }
 
+// Whether both products go in one launch: with few slots and up to 64 KB of A,
+// which every workgroup of a tile reads. (28 slots of 16 groups, K = 2048, rank
+// 16: 6.4 us, 6.5 in two launches, and 8 us of the host's time in place of 12;
+// one slot of 2048: 5.8 and 6.3; K = 2880, rank 16: 10.2 and 8.0 us, K = 7168,
+// rank 8: 11.5 and 7.5.)
+static bool lora_both(int64_t max_blocks, int bm, int R, int64_t K) {
+  return lora_few(max_blocks, bm) && R <= 32 && K * R <= 32768;
+}
+
 // Of moe_lora's workspace: the parts of h, then packed (neither where it is not used).
 LoraSizes lora_sizes(int32_t R, int64_t K, int32_t bm, int64_t max_blocks) {
   LoraSizes z{};
+  z.both = lora_both(max_blocks, bm, R, K);
+  if (z.both) return z;
   z.few = lora_few(max_blocks, bm);
   z.splits = lora_k_splits(max_blocks, K);
   const int64_t h = max_blocks * bm * R * 4;
@@ -509,15 +587,29 @@ hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream)
   });
 }
 
-hipError_t launch_lora_up_few(const LoraParams& p0, hipStream_t stream) {
-  LoraParams p = p0;
+// The grid of the kernels for few slots: parts of N of at least `least` columns.
+template <class F>
+static hipError_t lora_few_grid(LoraParams p, int least, F launch) {
   const int y = p.bm <= 16 ? 1 : p.bm / 16;
-  const int64_t tiles = (int64_t)p.max_blocks * y, most = (p.N + 255) / 256;
+  const int64_t tiles = (int64_t)p.max_blocks * y, most = (p.N + least - 1) / least;
   const int64_t want = (512 + tiles - 1) / (tiles > 0 ? tiles : 1);
   p.n_splits = (int32_t)(want < most ? want : most);
+  return lora_blocks(p, p.n_splits, [&](const LoraParams& q, uint32_t grid) { launch(q, dim3(grid, y)); });
+}
+
+hipError_t launch_lora_up_few(const LoraParams& p, hipStream_t stream) {
   return lora_rank(p.R, [&](auto rank) {
-    return lora_blocks(p, p.n_splits, [&](const LoraParams& q, uint32_t grid) {
-      hipLaunchKernelGGL(lora_up_few_kernel<decltype(rank)::value>, dim3(grid, y), dim3(kLoraThreads), 0, stream, q);
+    return lora_few_grid(p, 256, [&](const LoraParams& q, dim3 grid) {
+      hipLaunchKernelGGL(lora_up_few_kernel<decltype(rank)::value>, grid, dim3(kLoraThreads), 0, stream, q);
+    });
+  });
+}
+
+hipError_t launch_lora_both(const LoraParams& p, hipStream_t stream) {
+  return lora_rank(p.R, [&](auto rank) {
+    constexpr int RC = decltype(rank)::value < 4 ? decltype(rank)::value : 4;  // (ranks up to 32)
+    return lora_few_grid(p, 512, [&](const LoraParams& q, dim3 grid) {
+      hipLaunchKernelGGL(lora_both_kernel<RC>, grid, dim3(512), 0, stream, q);
     });
   });
 }

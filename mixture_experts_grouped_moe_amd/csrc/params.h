@@ -159,8 +159,10 @@ struct LoraParams {
   int64_t x_ld;
   uint32_t div_magic;  // of the division of slots by x_row_div
   int32_t div_shift;
-  const uint16_t* w;  // A, then B
+  const uint16_t* w;  // A
   int64_t w_g, w_ld;
+  const uint16_t* w2;  // B (dx: A)
+  int64_t w2_g, w2_ld;
   float* part;       // h in parts of K, [splits][places][R]
   uint16_t* packed;  // h as the large `up` takes it, [places][2][R] bf16
   int32_t splits, n_splits, run_tiles;
@@ -232,6 +234,7 @@ hipError_t launch_norm(const NormParams& p, const Dropout& d, hipStream_t stream
 hipError_t launch_norm_backward(const NormParams& p, const Dropout& d, hipStream_t stream);
 int64_t norm_backward_workspace_bytes(int64_t rows, int64_t n);
 struct LoraSizes {
+  bool both;       // both products in one launch, without a workspace
   bool few;        // the small `up`, which reads the parts
   int32_t splits;  // parts of K
   int64_t packed, bytes;  // offset into the workspace and its size
@@ -241,6 +244,7 @@ hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream);
 hipError_t launch_lora_join(const LoraParams& p, bool over, hipStream_t stream);
 hipError_t launch_lora_up(const LoraParams& p, bool turned, hipStream_t stream);
 hipError_t launch_lora_up_few(const LoraParams& p, hipStream_t stream);
+hipError_t launch_lora_both(const LoraParams& p, hipStream_t stream);
 struct LoraGradSizes {
   int32_t n_parts, seg_blocks, max_segs, max_parts;
   int64_t dh, packed, table, da_part, db_part, bytes;  // offsets into the workspace and its size

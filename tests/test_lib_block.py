@@ -53,6 +53,16 @@ def test_struct_mirrors(tmp_path):
     assert [l for l in said if l] == want
 
 
+def test_packed_structs_are_the_mirrors():
+    """The binding packs its arguments as bytes: the mirrors' bytes."""
+    for pack, mirror in ((moe.block._pack_norm, moe.block.MoeRmsnormArgs),
+                         (moe.block._pack_norm_backward, moe.block.MoeRmsnormBackwardArgs),
+                         (moe.block._pack_lora, moe.block.MoeLoraArgs),
+                         (moe.block._pack_lora_backward, moe.block.MoeLoraBackwardArgs)):
+        values = [i + 1 if t is not ctypes.c_float else i + 0.5 for i, (_, t) in enumerate(mirror._fields_)]
+        assert pack(*values) == bytes(mirror(*values))
+
+
 def refused(st):
     return st in (INVALID, UNSUPPORTED)
 
@@ -65,14 +75,14 @@ def _norm(**kw):
     d = dict(rows=4, n=64, x=P, x_ld=64, p=0.5, rng=2 * P, residual=3 * P, residual_ld=64, residual_dtype=FP32,
              sum=4 * P, sum_ld=64, weight=5 * P, weight_dtype=BF16, eps=1e-6, y=6 * P, y_ld=64, quant=1, q=7 * P,
              q_ld=64, scales=8 * P, scales_ld=2)
-    return L.moe_rmsnorm(ctypes.byref(moe.block.MoeRmsnormArgs(**{**d, **kw})), None)
+    return L.moe_rmsnorm(bytes(moe.block.MoeRmsnormArgs(**{**d, **kw})), None)
 
 
 def _norm_bwd(**kw):
     d = dict(rows=4, n=64, dy=P, dy_ld=64, dsum=2 * P, dsum_ld=64, sum=3 * P, sum_ld=64, sum_dtype=FP32, weight=4 * P,
              weight_dtype=BF16, eps=1e-6, p=0.5, rng=5 * P, dresidual=6 * P, dresidual_ld=64, dx=7 * P, dx_ld=64,
              dweight=8 * P, workspace=9 * P, workspace_bytes=1 << 24)
-    return L.moe_rmsnorm_backward(ctypes.byref(moe.block.MoeRmsnormBackwardArgs(**{**d, **kw})), None)
+    return L.moe_rmsnorm_backward(bytes(moe.block.MoeRmsnormBackwardArgs(**{**d, **kw})), None)
 
 
 def test_dropout_rejects(no_device):
@@ -168,13 +178,13 @@ _LORA = dict(num_slots=20, num_groups=3, rank=16, k=64, n=48, x=20 * P, x_ld=64,
 
 def _lora(**kw):
     d = dict(_LORA, c=26 * P, c_ld=48, h=27 * P, workspace=28 * P, workspace_bytes=1 << 30)
-    return L.moe_lora(ctypes.byref(moe.block.MoeLoraArgs(**{**d, **kw})), None)
+    return L.moe_lora(bytes(moe.block.MoeLoraArgs(**{**d, **kw})), None)
 
 
 def _lora_bwd(**kw):
     d = dict(_LORA, dy=29 * P, dy_ld=48, h=27 * P, dx=30 * P, dx_ld=64, da=31 * P, db=32 * P, workspace=28 * P,
              workspace_bytes=1 << 30)
-    return L.moe_lora_backward(ctypes.byref(moe.block.MoeLoraBackwardArgs(**{**d, **kw})), None)
+    return L.moe_lora_backward(bytes(moe.block.MoeLoraBackwardArgs(**{**d, **kw})), None)
 
 
 def _lora_bytes(f, S=20, G=3, R=16, K=64, N=48, bm=16, mb=4):
@@ -194,16 +204,18 @@ def test_lora_rejects(no_device):
                     dict(x_ld=68), dict(a_ld=60), dict(a_ld=72), dict(a_stride_g=1016), dict(b_ld=8), dict(b_stride_g=760),
                     dict(a_stride_g=1028), dict(scale=23 * P + 2), dict(sorted_slot_ids=None), dict(group_ids=None),
                     dict(group_ids=25 * P + 2), dict(block_m=24), dict(block_m=128), dict(max_blocks=3),
-                    dict(max_blocks=1 << 27), dict(workspace=None), dict(workspace=28 * P + 8), dict(h=27 * P + 8),
+                    dict(max_blocks=1 << 27), dict(workspace=28 * P + 8), dict(h=27 * P + 8),
                     dict(x_ld=1 << 60), dict(a_stride_g=1 << 60)):
             assert call(**bad) == INVALID, bad
         assert call(num_groups=1025, max_blocks=30) == UNSUPPORTED
         assert call(rank=136, a_stride_g=1 << 14, b_ld=136, b_stride_g=1 << 14) == UNSUPPORTED
-    assert not refused(_lora(h=None))
+    assert not refused(_lora(h=None)) and not refused(_lora(workspace=None, workspace_bytes=0))   # one launch, no workspace
+    wide = dict(rank=64, a_stride_g=4096, b_ld=64, b_stride_g=3072)
+    assert not refused(_lora(**wide)) and _lora(**wide, workspace=None) == INVALID
+    assert _lora(**wide, workspace_bytes=_lora_bytes(moe.moe_lora_workspace_bytes, R=64) - 1) == INVALID
     assert _lora(c=None) == INVALID and _lora(c_ld=40) == INVALID and _lora(c=26 * P + 8) == INVALID
-    assert _lora(workspace_bytes=_lora_bytes(moe.moe_lora_workspace_bytes) - 1) == INVALID
     assert not refused(_lora_bwd(dx=None)) and not refused(_lora_bwd(da=None, db=None, h=None))
-    for bad in (dict(dy=None), dict(dy_ld=40), dict(dx_ld=56), dict(da=None), dict(db=None), dict(h=None),
+    for bad in (dict(workspace=None), dict(dy=None), dict(dy_ld=40), dict(dx_ld=56), dict(da=None), dict(db=None), dict(h=None),
                 dict(dx=None, da=None, db=None), dict(da=31 * P + 8),
                 dict(workspace_bytes=_lora_bytes(moe.moe_lora_backward_workspace_bytes) - 1)):
         assert _lora_bwd(**bad) == INVALID, bad
@@ -225,7 +237,7 @@ def test_lora_sizes():
 
 def test_lora_overlaps_are_rejected(no_device):
     shared = ["x", "a", "b", "scale", "sorted_slot_ids", "group_ids"]
-    _overlaps(_lora, ["c", "h", "workspace"], shared)
+    _overlaps(lambda **kw: _lora(rank=64, a_stride_g=4096, b_ld=64, b_stride_g=3072, **kw), ["c", "h", "workspace"], shared)
     _overlaps(_lora_bwd, ["dx", "da", "db", "workspace"], shared + ["dy", "h"])
 
 
