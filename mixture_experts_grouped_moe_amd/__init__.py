@@ -604,7 +604,7 @@ _warned_padding = False
 
 
 def moe_w4a16_layer(x, topk_ids, topk_w, w1, s1, w2, s2, b1=None, b2=None, num_tokens=None,
-                    pad_token_dim=False, stream=None):
+                    pad_token_dim=False, stream=None, adapter=None):
     """The W4A16 MXFP4 expert layer: align -> gate+up GEMM with SwiGLU ->
     down GEMM -> top-k combine. Returns y bf16 [num_tokens, H]. w1 / w2 are
     rows-layout codes with scales s1 / s2, or PackedWeights (s1 / s2 None).
@@ -616,6 +616,9 @@ def moe_w4a16_layer(x, topk_ids, topk_w, w1, s1, w2, s2, b1=None, b2=None, num_t
     y are formed. Padding is honoured only where moe_padding_supported() says
     it is exact (bf16 activations x MXFP4 weights); elsewhere it is ignored
     with a warning.
+
+    adapter: (a [E, R, I], b [E, H, R], scale fp32 [E] or None), low-rank
+    adapters of the experts' down projections, added to its output by moe_lora.
     """
     global _warned_padding
     T = x.shape[0] if num_tokens is None else int(num_tokens)
@@ -637,21 +640,25 @@ def moe_w4a16_layer(x, topk_ids, topk_w, w1, s1, w2, s2, b1=None, b2=None, num_t
                          epilogue="swiglu", stream=stream)
     c2 = moe_grouped_gemm(h, w2, "e2m1x2", routing, Tr, k, E, a_row_div=1, w_scale=s2, bias=b2,
                           stream=stream)
+    if adapter is not None:
+        moe_lora(c2, h, adapter[0], adapter[1], routing, scale=adapter[2], stream=stream)
     return moe_combine(c2, topk_w, k, num_tokens=T, stream=stream)
 
 
-def moe_relu2_layer(x, topk_ids, topk_w, w1, w2, b1=None, b2=None, num_tokens=None, stream=None):
+def moe_relu2_layer(x, topk_ids, topk_w, w1, w2, b1=None, b2=None, num_tokens=None, stream=None, adapter=None):
     """The non-gated squared-ReLU expert layer (the Nemotron decode shape):
     align -> up GEMM with h = max(pre, 0)^2 -> down GEMM -> top-k combine, bf16
     weights (rows layout [E, N, H] and [E, H, N], or PackedWeights). Token
-    counts up to moe_decode_max_tokens() run the decode GEMM. Returns y bf16
-    [num_tokens, H]."""
+    counts up to moe_decode_max_tokens() run the decode GEMM. adapter: as in
+    moe_w4a16_layer. Returns y bf16 [num_tokens, H]."""
     T = x.shape[0] if num_tokens is None else int(num_tokens)
     k = topk_ids.shape[1]
     E = w1.num_experts if isinstance(w1, PackedWeights) else w1.shape[0]
     routing = moe_align(topk_ids, E, moe_gemm_block_m("bf16", T), num_tokens=T, stream=stream)
     h = moe_grouped_gemm(x, w1, "bf16", routing, T, k, E, a_row_div=k, bias=b1, epilogue="relu2", stream=stream)
     c2 = moe_grouped_gemm(h, w2, "bf16", routing, T, k, E, a_row_div=1, bias=b2, stream=stream)
+    if adapter is not None:
+        moe_lora(c2, h, adapter[0], adapter[1], routing, scale=adapter[2], stream=stream)
     return moe_combine(c2, topk_w, k, num_tokens=T, stream=stream)
 
 
