@@ -45,7 +45,7 @@ extern "C" {
 
 /* y[r][i] = bf16( keep(r, i) * x[r][i] / (1 - threshold / 65536) ).
  * x, y (device) bf16 [rows][n], row strides x_ld, y_ld (elements).
- * Requirements: rows >= 0; n a positive multiple of 8; rows * n < 2^60; strides
+ * Requirements: rows >= 0; n a positive multiple of 8, below 2^31; rows * n < 2^60; strides
  * >= n and multiples of 8; x, y 16-byte aligned, rng 8-byte; 0 <= p <= 1; rng
  * may be NULL when threshold is 0. y may be x (the same pointer and stride) and
  * must not overlap it otherwise, nor rng. */
@@ -99,7 +99,7 @@ typedef struct {
   int64_t scales_ld;       /* MXFP8 only */
 } moe_rmsnorm_args;
 
-/* Requirements: 0 <= rows < 2^31; n a positive multiple of 8 (32 for MXFP8), at
+/* Requirements: 0 <= rows < 2^31 - 1; n a positive multiple of 8 (32 for MXFP8), at
  * most 16384; y or a quant; eps >= 0 and finite; 0 <= p <= 1. Strides cover a row
  * and are multiples of 8. x, residual, sum, weight, y 16-byte aligned; rng and q
  * 8-byte, per-token scales 4-byte. Strides and pointers of what is
@@ -157,7 +157,8 @@ int64_t moe_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t n);
  *   h[s] = A[g] x[row]                            (fp32; stored when h != NULL)
  *   C[s] = bf16( C[s] + scale[g] * B[g] h[s] )    (scale NULL: 1)
  * C is what the shared projection wrote (moe_grouped_gemm, for one). Rows of C
- * and h of slots in no block are neither read nor written. Products of bf16
+ * and h of slots in no block are left as they were, and nothing that is in them
+ * or in rows of x that no block names reaches a result. Products of bf16
  * values are exact, sums fp32; the second product takes h as two bf16 terms
  * (2^-16 relative), so an infinite value of B gives infinities or NaN. The
  * order of the sums depends on the sizes alone: repeated calls give equal bits.
@@ -189,7 +190,7 @@ typedef struct {
   float* h;                /* (device) fp32 [num_slots][rank], contiguous, or NULL */
   void* workspace;         /* (device, 16-byte aligned) not kept between calls; calls that may run
                               at the same time (other streams, graphs replayed side by side) need one each */
-  int64_t workspace_bytes; /* >= moe_lora_workspace_bytes(...) */
+  int64_t workspace_bytes; /* >= moe_lora_workspace_bytes(...); where that is 0, workspace may be NULL */
 } moe_lora_args;
 
 /* Requirements: 0 <= num_slots <= 2^31 - 2^16; 1 <= num_groups <= 1024; rank a
@@ -220,8 +221,9 @@ int64_t moe_lora_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t 
  * where x_row_div > 1, moe_combine_routed adds the rows of a token. dy passes
  * through to the shared projection unchanged. da and db are written for every
  * group, zeros for one without slots; both NULL: not computed (h and x are then
- * not read). The second products take dh, and the weights' gradients dh and h,
- * as two bf16 terms (2^-16 relative). Rows of dx of slots in no block are left. */
+ * not read). The second product takes dh as two bf16 terms (2^-16 relative), the
+ * weights' gradients dh and h as three (all of fp32's bits). Rows of dx of slots
+ * in no block are left as they were. */
 typedef struct {
   int64_t num_slots;
   int32_t num_groups;
@@ -249,7 +251,7 @@ typedef struct {
   int64_t dx_ld;
   float* da;               /* (device) fp32, contiguous, or NULL */
   float* db;
-  void* workspace;
+  void* workspace;         /* as in the forward pass */
   int64_t workspace_bytes; /* >= moe_lora_backward_workspace_bytes(...) */
 } moe_lora_backward_args;
 
@@ -259,6 +261,7 @@ typedef struct {
  * dx, da, db and workspace must not overlap each other or an input. */
 moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t stream);
 
+/* Bytes of its workspace; -1 on bad sizes. */
 int64_t moe_lora_backward_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t rank, int64_t k, int64_t n,
                                           int32_t block_m, int64_t max_blocks);
 

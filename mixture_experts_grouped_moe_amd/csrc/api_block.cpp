@@ -57,7 +57,7 @@ moe_status check_rows(const char* name, const void* p, int64_t ld, int64_t rows,
 // What the norm and its gradient check alike.
 moe_status check_norm(int64_t rows, int64_t n, int64_t multiple, int32_t dtype, const void* weight,
                       int32_t weight_dtype, float eps, float p, const uint64_t* rng) {
-  if (rows < 0 || rows >= INT32_MAX) return fail(MOE_ERR_INVALID_ARGUMENT, "rows must be in [0, 2^31)");
+  if (rows < 0 || rows >= INT32_MAX) return fail(MOE_ERR_INVALID_ARGUMENT, "rows must be in [0, 2^31 - 1)");
   if (n < multiple || n % multiple != 0)
     return fail(MOE_ERR_INVALID_ARGUMENT, "n must be a positive multiple of %lld", (long long)multiple);
   if (n > kNormMaxWidth) return fail(MOE_ERR_UNSUPPORTED, "n %lld > %lld", (long long)n, (long long)kNormMaxWidth);

@@ -10,7 +10,14 @@
 // block list; as `up` takes it, it is scaled and in two bf16 terms ("packed",
 // [place][hi, lo][R]), which `down` writes itself where K is not split, `join`
 // from the parts where it is; with few slots a small `up` reads the parts, two
-// launches in all.
+// launches in all, or one (`both`).
+//
+// Measured (kernel times): 8192 slots of 8 groups, K = 7168, N = 4096, rank 32:
+// `down` 31 us (3.8 TB/s: a group's A is read again by each block, beside the
+// rows), `join` 4.9, `up` 33 (5.6 TB/s). 32768 slots of 128 groups, four to a row
+// of 2880, N = 5760, rank 16: `down` 37 (5.3 TB/s), `up` 143 (730 MB, 5.1 TB/s;
+// the rows alone read and written back reach 4.7). 28 slots of 16 groups, K =
+// 2048, N = 1856, rank 16: 6.7, latency: ids, then rows and A, then the stores.
 #include <type_traits>
 
 #include "lora_util.h"
@@ -488,7 +495,7 @@ static bool lora_few(int64_t max_blocks, int bm) { return max_blocks * (bm < 16 
 // 75 at 3, 70 at 4, 79 at 1; 7 slots of 7 groups, rank 128: 15 us at 28 parts, 25
 // at 8.)
 int lora_k_splits(int64_t max_blocks, int64_t k) {
-  const int64_t want = (256 + max_blocks - 1) / (max_blocks > 0 ? max_blocks : 1);
+  const int64_t want = (kLoraCUs + max_blocks - 1) / (max_blocks > 0 ? max_blocks : 1);
   const int64_t most = k / 256 > 1 ? k / 256 : 1;
   const int64_t n = want < most ? want : most;
   return (int)(n < 32 ? n : 32);
@@ -561,14 +568,15 @@ hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream)
   p.n_splits = (p.N + 511) / 512;
   const int per = p.bm <= 16 ? 1 : p.bm / 16;
   const int64_t all = (int64_t)p.max_blocks * per * p.n_splits;  // tiles of 16 slots and 512 columns
-  // About 3072 workgroups: many more than run at once, so that they end together
-  // (32768 slots of 128 groups, 5760 columns: 180 us for the whole call, 184 at
-  // 1536), of whole blocks, whose slots are one group's (187 with 9 tiles in place
+  // About 12 workgroups a CU: many more than run at once, so that they end together
+  // (32768 slots of 128 groups, 5760 columns: 180 us for the whole call, 184 at 6
+  // a CU), of whole blocks, whose slots are one group's (187 with 9 tiles in place
   // of 8). With fewer tiles 4 a workgroup, which reads its columns of B for them,
   // or what gives 512 workgroups (gradients of 1333 slots: 28.5 us, 31.6 at 4
   // tiles; 4096 slots of rank 64: 35.8 us at 4, 39 at 2).
-  const int64_t share = all / 3072;
-  p.run_tiles = (int32_t)(share >= 8 ? share / per * per : share > 4 ? share : all / 512 > 4 ? 4 : all / 512 > 1 ? all / 512 : 1);
+  const int64_t share = all / (12 * kLoraCUs);
+  const int64_t few = all / (2 * kLoraCUs) < 4 ? all / (2 * kLoraCUs) : 4;
+  p.run_tiles = (int32_t)(share >= 8 ? share / per * per : share > 4 ? share : few > 1 ? few : 1);
   return lora_rank(p.R, [&](auto rank) {
     constexpr int RC = decltype(rank)::value;
     // launches of whole blocks and whole runs
@@ -592,7 +600,7 @@ template <class F>
 static hipError_t lora_few_grid(LoraParams p, int least, F launch) {
   const int y = p.bm <= 16 ? 1 : p.bm / 16;
   const int64_t tiles = (int64_t)p.max_blocks * y, most = (p.N + least - 1) / least;
-  const int64_t want = (512 + tiles - 1) / (tiles > 0 ? tiles : 1);
+  const int64_t want = (2 * kLoraCUs + tiles - 1) / (tiles > 0 ? tiles : 1);
   p.n_splits = (int32_t)(want < most ? want : most);
   return lora_blocks(p, p.n_splits, [&](const LoraParams& q, uint32_t grid) { launch(q, dim3(grid, y)); });
 }

@@ -7,6 +7,7 @@
 namespace moe {
 
 constexpr int kLoraThreads = 256;  // four waves
+constexpr int kLoraCUs = 256;
 
 typedef __bf16 lora_bf16x8 __attribute__((ext_vector_type(8)));
 

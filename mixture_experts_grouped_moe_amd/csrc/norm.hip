@@ -7,9 +7,11 @@
 // columns each, neighbouring threads on neighbouring pieces), so the sum of
 // squares, the row's largest magnitude and all outputs come from one pass over
 // memory; workgroups take rows in turn with the next row's loads in flight.
-// 4096 x 7168 with MXFP8: 50 us, 5.3 TB/s (a large copy reaches 5.1); 7 rows of
-// 2688: 3.7 us; gradient of 16384 x 7168: 166 us, 5.65 TB/s. One row a
-// workgroup without the loads ahead: 55 and 204 us.
+// 4096 x 7168 with MXFP8: 49 us, 5.4 TB/s (a large copy reaches 5.1); 6554 x 2880
+// of an fp32 stream with dropout: 38 us, 5.9 TB/s; 7 rows of 2688: 3.7 to 4.4 us,
+// latency; gradient of 16384 x 7168: 166 us, 5.65 TB/s, and 5 for dweight's last
+// sums; of 333 x 2880: 7.6 and 3.5 us. One row a workgroup without the loads
+// ahead: 55 us the first, 204 the last but one.
 #include <type_traits>
 
 #include "dropout_util.h"
@@ -506,7 +508,8 @@ hipError_t launch_norm_backward(const NormParams& p, const Dropout& d, hipStream
   }
   if (p.dw == nullptr) return hipSuccess;
   const int n = p.pieces * 8;
-  hipLaunchKernelGGL(norm_dweight_kernel, dim3((n + kNormFinCols - 1) / kNormFinCols), dim3(1024), 0, stream, p.partial, (int32_t)parts, n, p.dw);
+  hipLaunchKernelGGL(norm_dweight_kernel, dim3((n + kNormFinCols - 1) / kNormFinCols), dim3(1024), 0, stream, p.partial,
+                     (int32_t)parts, n, p.dw);
   return hipGetLastError();
 }
 

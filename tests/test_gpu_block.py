@@ -177,3 +177,35 @@ def test_layers_with_adapters(tokens):
     plain = moe.moe_relu2_layer(x, ids, w, w1, w2)
     assert torch.equal(moe.moe_relu2_layer(x, ids, w, w1, w2, adapter=(a, torch.zeros_like(b), None)), plain)
     assert not torch.equal(moe.moe_relu2_layer(x, ids, w, w1, w2, adapter=(a, b, scale)), plain)
+
+
+def test_steps_side_by_side():
+    # two steps on two streams at once, and their graphs replayed at once, each
+    # with the workspaces that it allocated: the bits of one after the other
+    ds = [inputs(), inputs()]
+    ds[1]["x"] = normal((T, H), 21, "x")
+    ds[1]["logits"] = normal((T, E), 21, "z", "fp32")
+    want = [step(d)[0] for d in ds]
+    streams, graphs, kept = [torch.cuda.Stream() for _ in ds], [], []
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step(ds[i])[0]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(g[n], w[n]) for n in w)
+    for d in ds:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            kept.append(step(d)[0])
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for g, w in zip(kept, want):
+            assert all(torch.equal(g[n], w[n]) for n in w)
+            for n in w:
+                g[n].zero_()

@@ -210,7 +210,7 @@ def test_lora_rejects(no_device):
         assert call(num_groups=1025, max_blocks=30) == UNSUPPORTED
         assert call(rank=136, a_stride_g=1 << 14, b_ld=136, b_stride_g=1 << 14) == UNSUPPORTED
     assert not refused(_lora(h=None)) and not refused(_lora(workspace=None, workspace_bytes=0))   # one launch, no workspace
-    wide = dict(rank=64, a_stride_g=4096, b_ld=64, b_stride_g=3072)
+    wide = dict(rank=64, a_stride_g=4096, b_ld=64, b_stride_g=3200)
     assert not refused(_lora(**wide)) and _lora(**wide, workspace=None) == INVALID
     assert _lora(**wide, workspace_bytes=_lora_bytes(moe.moe_lora_workspace_bytes, R=64) - 1) == INVALID
     assert _lora(c=None) == INVALID and _lora(c_ld=40) == INVALID and _lora(c=26 * P + 8) == INVALID
@@ -237,7 +237,7 @@ def test_lora_sizes():
 
 def test_lora_overlaps_are_rejected(no_device):
     shared = ["x", "a", "b", "scale", "sorted_slot_ids", "group_ids"]
-    _overlaps(lambda **kw: _lora(rank=64, a_stride_g=4096, b_ld=64, b_stride_g=3072, **kw), ["c", "h", "workspace"], shared)
+    _overlaps(lambda **kw: _lora(rank=64, a_stride_g=4096, b_ld=64, b_stride_g=3200, **kw), ["c", "h", "workspace"], shared)
     _overlaps(_lora_bwd, ["dx", "da", "db", "workspace"], shared + ["dy", "h"])
 
 
