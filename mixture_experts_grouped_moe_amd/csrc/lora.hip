@@ -14,7 +14,7 @@
 //
 // Measured (kernel times): 8192 slots of 8 groups, K = 7168, N = 4096, rank 32:
 // `down` 31 us (3.8 TB/s: a group's A is read again by each block, beside the
-// rows), `join` 4.9, `up` 33 (5.6 TB/s). 32768 slots of 128 groups, four to a row
+// rows), `join` 4.9, `up` 33 (3.9 TB/s). 32768 slots of 128 groups, four to a row
 // of 2880, N = 5760, rank 16: `down` 37 (5.3 TB/s), `up` 143 (730 MB, 5.1 TB/s;
 // the rows alone read and written back reach 4.7). 28 slots of 16 groups, K =
 // 2048, N = 1856, rank 16: 6.7, latency: ids, then rows and A, then the stores.
