@@ -377,7 +377,7 @@ moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t st
       misaligned(args->workspace, 16))
     return fail(MOE_ERR_INVALID_ARGUMENT, "h, da, db and workspace must be 16-byte aligned");
   const moe::LoraGradSizes z = moe::lora_grad_sizes(a.G, a.R, a.K, a.N, a.block_m, a.max_blocks);
-  if (args->workspace_bytes < z.bytes || args->workspace == nullptr)
+  if (args->workspace_bytes < z.bytes || (z.bytes > 0 && args->workspace == nullptr))
     return fail(MOE_ERR_INVALID_ARGUMENT, "workspace of %lld bytes, %lld needed", (long long)args->workspace_bytes,
                 (long long)z.bytes);
   const Range dy = span(args->dy, a.S, args->dy_ld, a.N, 2), h = {args->h, a.S * a.R * 4};
@@ -412,7 +412,8 @@ moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t st
   q.b_g = a.b_stride_g;
   q.b_ld = a.b_ld;
   q.dh = reinterpret_cast<float*>(base + z.dh);
-  q.table = reinterpret_cast<int32_t*>(base + z.table);
+  if (z.seg_blocks > 1) q.table = reinterpret_cast<int32_t*>(base + z.table);
+  if (z.direct) q.parts = z.n_parts;
   q.seg_blocks = z.seg_blocks;
   q.max_segs = z.max_segs;
   q.max_parts = z.max_parts;
@@ -423,11 +424,11 @@ moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t st
   p.max_blocks = q.max_blocks;
   p.part = q.dh;
   p.splits = z.n_parts;
-  if (args->dx != nullptr) p.packed = reinterpret_cast<uint16_t*>(base + z.packed);
+  if (args->dx != nullptr && !z.direct) p.packed = reinterpret_cast<uint16_t*>(base + z.packed);
   const hipStream_t on = (hipStream_t)stream;
-  hipError_t err = moe::launch_lora_grad_table(q, on);
+  hipError_t err = z.seg_blocks > 1 ? moe::launch_lora_grad_table(q, on) : hipSuccess;
   if (err == hipSuccess) err = moe::launch_lora_grad_dy(q, on);
-  if (err == hipSuccess) err = moe::launch_lora_join(p, true, on);
+  if (err == hipSuccess && !z.direct) err = moe::launch_lora_join(p, true, on);
   if (err == hipSuccess && args->dx != nullptr) {
     p.N = (int32_t)a.K;
     p.w2 = static_cast<const uint16_t*>(a.a);

@@ -351,10 +351,11 @@ __global__ __launch_bounds__(512) void lora_both_kernel(LoraParams p) {
 // with no product: 4.7 TB/s so, 4.1 to 4.4 in 64-byte pieces of 16 rows). h
 // enters as hi + lo: for ranks up to 16 both lie in one MFMA's k (RC = 2: hi hi
 // lo lo, RC = 1: hi lo and two zeros, in pieces of 8), beyond, each piece of 32
-// ranks of B meets hi and lo in turn. TURNED: the matrix is [R][N] (dx, whose
+// ranks of B meets hi and lo in turn. PARTS: h comes from its parts, added, scaled
+// and split by every wave. TURNED: the matrix is [R][N] (dx, whose
 // matrix is A itself): a lane reads its 8 columns of each of 8 ranks and turns
 // the 8 x 8 around in registers.
-template <int RC, bool TURNED>
+template <int RC, bool TURNED, bool PARTS>
 __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
   constexpr int F = RC < 4 ? 1 : RC / 4, P = RC < 4 ? 1 : 2;
   constexpr int NT = 8, kCols = 16 * NT;
@@ -399,6 +400,36 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
       v.c[r] = *reinterpret_cast<const u32x4_t*>(at);
     }
     const int64_t pos = (int64_t)((t0 + t) >> shift) * p.bm + min(row + m16, p.bm - 1);
+    if constexpr (PARTS) {
+      const float scale = p.scale != nullptr ? p.scale[v.group] : 1.0f;
+      const int64_t step = (int64_t)p.max_blocks * p.bm * p.R;
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
+        const bool here = piece < pieces && (RC != 1 || q < 2);
+        const float* at = p.part + pos * p.R + (here ? 8 * piece : 0);
+        const f32x4_t a = lora_sum_parts(at, step, p.splits) * scale;
+        const f32x4_t b = lora_sum_parts(at + 4, step, p.splits) * scale;
+        u32x4_t hi, lo;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t w[2];
+          lora_split(a[2 * e], a[2 * e + 1], w[0], w[1]);
+          hi[e] = w[0];
+          lo[e] = w[1];
+          lora_split(b[2 * e], b[2 * e + 1], w[0], w[1]);
+          hi[2 + e] = w[0];
+          lo[2 + e] = w[1];
+        }
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const bool low = RC >= 4 ? k == 1 : RC == 2 ? q >= 2 : q == 1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v.h[f][k][e] = !here ? 0 : low ? lo[e] : hi[e];
+        }
+      }
+      return;
+    }
     const uint16_t* at = p.packed + pos * (2 * p.R);
 #pragma unroll
     for (int f = 0; f < F; ++f)
@@ -586,7 +617,9 @@ hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream)
     for (int64_t r = 0; r < runs; r += most) {
       q.block0 = (int32_t)(r * p.run_tiles / per);
       const int64_t n = runs - r < most ? runs - r : most;
-      auto kernel = turned ? lora_up_kernel<RC, true> : lora_up_kernel<RC, false>;
+      auto kernel = !turned               ? lora_up_kernel<RC, false, false>
+                    : q.packed != nullptr ? lora_up_kernel<RC, true, false>
+                                          : lora_up_kernel<RC, true, true>;
       hipLaunchKernelGGL(kernel, dim3((uint32_t)(n * p.n_splits)), dim3(kLoraThreads), 0, stream, q);
       const hipError_t err = hipGetLastError();
       if (err != hipSuccess) return err;

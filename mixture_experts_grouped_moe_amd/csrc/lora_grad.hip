@@ -10,8 +10,8 @@
 // Measured (kernel times): 32768 slots of 128 groups, K = 2880 (a row serves four),
 // N = 5760, rank 16: the table 9 us, dy 106 (383 MB read and 69 written, 4.3 TB/s;
 // gathered rows of this width are read at 4.5 to 4.9), h's join 7.2, dx 71 (5.4
-// TB/s), x 32 (173 MB moved, 5.4 TB/s), the gradients' join 4.9. 1333 slots of 3 groups, 2688
-// x 1856, rank 8: six launches of 3.2 to 6.9 us each, all latency.
+// TB/s), x 32 (172 MB moved, 5.4 TB/s), the gradients' join 4.9. 1333 slots of 3 groups,
+// 2688 x 1856, rank 8: four launches of 3.5 to 7 us each, all latency.
 #include <type_traits>
 
 #include "lora_util.h"
@@ -28,7 +28,7 @@ constexpr int kLgJoinInts = 3;  // group of several segments, its first partial 
 
 // ------------------------------------------------------------------ table
 
-// The segments, one workgroup: max_segs entries of kLgSegInts, then for the join
+// The segments where they hold several blocks, one workgroup: max_segs entries of kLgSegInts, then for the join
 // an entry of kLgJoinInts for each group of several. Segments hold seg_blocks
 // blocks (a group's last one fewer, and no places behind its last slot); a group
 // without blocks has an empty one, which writes its zeros. Longest segments
@@ -151,6 +151,38 @@ __global__ __launch_bounds__(1024) void lora_table_kernel(LoraGradParams p) {
   }
 }
 
+// Where every block is a segment (max_blocks <= 256: lora_grad_sizes), workgroups
+// find theirs themselves: segment i is block i, its partial slot i too where the
+// group has another block beside it, and those past max_blocks stand for groups
+// without blocks. (1333 slots of 3 groups, 2688 x 1856, rank 8: 24.9 us for the
+// whole call, 28.2 with the table; 700 slots of one, 4096 x 4096, rank 64: 44.0 and
+// 46.4.) False: no segment.
+__device__ __forceinline__ bool lora_segment(const LoraGradParams& p, int i, int& g, int& slot, int64_t& pos0,
+                                             int64_t& pos1) {
+  if (p.table != nullptr) {
+    const int32_t* e = p.table + (int64_t)i * kLgSegInts;
+    g = e[0];
+    slot = e[3];
+    pos0 = e[1];
+    pos1 = e[2];
+    return g >= 0;
+  }
+  slot = -1;
+  pos0 = pos1 = 0;
+  if (i >= p.max_blocks) {
+    g = i - p.max_blocks;
+    return g < p.G && !__syncthreads_or((int)threadIdx.x < p.max_blocks && p.groups[threadIdx.x] == g);
+  }
+  g = p.groups[i];
+  const int before = i > 0 ? p.groups[i - 1] : -1, after = i + 1 < p.max_blocks ? p.groups[i + 1] : -1;
+  const int lane = threadIdx.x % 64;
+  pos0 = (int64_t)i * p.bm;
+  const uint64_t live = __ballot(lane < p.bm && (uint32_t)p.sorted[pos0 + min(lane, p.bm - 1)] < (uint32_t)p.S);
+  pos1 = pos0 + (live != 0 ? 64 - __builtin_clzll(live) : 0);
+  if (before == g || after == g) slot = i;
+  return (uint32_t)g < (uint32_t)p.G;
+}
+
 // ------------------------------------------------------------- x and dy
 
 // A slot's row of the tile lies by 16-byte units, exchanged so that both reads
@@ -183,14 +215,14 @@ __global__ __launch_bounds__(kLgThreads, RT == 1 ? 4 : 2) void lora_wide_kernel(
   __shared__ __attribute__((aligned(16))) uint16_t narrows[2][3][RT * 16][kNarrowLd];
   __shared__ f32x4_t red[OF_X || NP == 1 ? 1 : NP][2 * RT][64];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, q = lane / 16, m16 = lane % 16;
-  const int32_t* e = p.table + (int64_t)blockIdx.y * kLgSegInts;
-  const int g = e[0], slot = e[3];
-  const int64_t pos0 = e[1], pos1 = e[2];
-  if (g < 0) return;  // past the last segment
+  int g, slot;
+  int64_t pos0, pos1;
+  if (!lora_segment(p, blockIdx.y, g, slot, pos0, pos1)) return;
   const int c0 = blockIdx.x * kLgCols, width = OF_X ? p.K : p.N;
   const uint16_t* big = OF_X ? p.x : p.dy;
   const int64_t ld = OF_X ? p.x_ld : p.dy_ld;
   const float scale = p.scale != nullptr ? p.scale[g] : 1.0f;
+  const float narrow_scale = OF_X && p.parts == 0 ? 1.0f : scale;  // (a joined dh is scaled)
   const bool weights = p.da != nullptr;
   f32x4_t acc[RT][NC];
 #pragma unroll
@@ -241,7 +273,11 @@ __global__ __launch_bounds__(kLgThreads, RT == 1 ? 4 : 2) void lora_wide_kernel(
     const float* from = OF_X ? p.dh + (pos0 + min(at + nslot, places - 1)) * p.R
                              : p.h + (int64_t)(narrow ? ids.narrow : spare) * p.R;
 #pragma unroll
-    for (int i = 0; i < NH; ++i) o.h[i] = *reinterpret_cast<const f32x4_t*>(from + min(4 * nr + 64 * i, p.R - 4));
+    for (int i = 0; i < NH; ++i) {
+      const float* at_r = from + min(4 * nr + 64 * i, p.R - 4);
+      o.h[i] = OF_X && p.parts > 1 ? lora_sum_parts(at_r, (int64_t)p.max_blocks * p.bm * p.R, p.parts)
+                                   : *reinterpret_cast<const f32x4_t*>(at_r);
+    }
   };
   constexpr int kRowB = kLgCols * 2;
   auto put_dh = [&](int pos, int tile, f32x4_t d) {  // tile = 2 * rank tile + slot tile
@@ -265,7 +301,7 @@ __global__ __launch_bounds__(kLgThreads, RT == 1 ? 4 : 2) void lora_wide_kernel(
       for (int i = 0; i < NH; ++i) {
         const int r = 4 * nr + 64 * i;
         if (r >= RT * 16) continue;
-        const f32x4_t h = (o.live & 2) && r < p.R ? (OF_X ? o.h[i] : o.h[i] * scale) : f32x4_t{0, 0, 0, 0};
+        const f32x4_t h = (o.live & 2) && r < p.R ? o.h[i] * narrow_scale : f32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t term[3];
@@ -399,8 +435,23 @@ __global__ __launch_bounds__(kLgThreads, RT == 1 ? 4 : 2) void lora_wide_kernel(
 
 // The partial sums of groups of several segments, added in order.
 __global__ __launch_bounds__(kLoraThreads) void lora_grad_join_kernel(LoraGradParams p) {
-  const int32_t* e = p.table + p.max_segs * kLgSegInts + (int64_t)blockIdx.y * kLgJoinInts;
-  const int g = e[0], slot = e[1], segs = e[2];
+  int g, slot, segs;
+  if (p.table != nullptr) {
+    const int32_t* e = p.table + p.max_segs * kLgSegInts + (int64_t)blockIdx.y * kLgJoinInts;
+    g = e[0], slot = e[1], segs = e[2];
+  } else {  // a group's first block adds for its blocks (max_blocks <= kLoraThreads)
+    __shared__ int stop;
+    slot = blockIdx.y;
+    if (slot + 1 >= p.max_blocks) return;
+    g = p.groups[slot];
+    if ((uint32_t)g >= (uint32_t)p.G || p.groups[slot + 1] != g || (slot > 0 && p.groups[slot - 1] == g)) return;
+    const int i = threadIdx.x;
+    if (i == 0) stop = p.max_blocks;
+    __syncthreads();
+    if (i > slot && i < p.max_blocks && p.groups[i] != g) atomicMin(&stop, i);
+    __syncthreads();
+    segs = stop - slot;
+  }
   const int64_t na = (int64_t)p.R * p.K, nb = (int64_t)p.R * p.N;
   for (int64_t i = ((int64_t)blockIdx.x * kLoraThreads + threadIdx.x) * 4; segs > 0 && i < na + nb;
        i += (int64_t)gridDim.x * kLoraThreads * 4) {
@@ -423,17 +474,22 @@ LoraGradSizes lora_grad_sizes(int32_t G, int32_t R, int64_t K, int64_t N, int32_
   const int64_t per = (max_blocks + want - 1) / want;
   z.seg_blocks = (int32_t)(per > 1 ? per : 1);
   z.max_segs = (int32_t)(max_blocks / z.seg_blocks + G);
-  // (a group of s > 1 segments has more than (s - 1) seg_blocks blocks, so s <= 2 blocks / seg_blocks)
-  z.max_parts = (int32_t)(2 * (max_blocks / z.seg_blocks));
+  // (where a block is a segment, its number is its partial slot; else a group of s > 1 segments has more than
+  // (s - 1) seg_blocks blocks, so s <= 2 blocks / seg_blocks)
+  z.max_parts = (int32_t)(z.seg_blocks == 1 ? max_blocks : 2 * (max_blocks / z.seg_blocks));
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t was = at;
     at += (bytes + 255) / 256 * 256;
     return was;
   };
+  // the join of dh's parts left to the readers, a launch less, where parts and ranks are few (1333 slots of 3 groups,
+  // 2688 x 1856, rank 8, 4 parts: 23.7 us for the whole call, 24.9 with the join; rank 16 at 4 parts 17.6 and 19.2, 8
+  // parts 20.9 and 20.8, 14 parts 28.5 and 25.3; rank 64 at 6 parts 31.4 and 30.4)
+  z.direct = z.seg_blocks == 1 && z.n_parts * R <= 128;
   z.dh = take(z.n_parts * max_blocks * bm * R * 4);
-  z.packed = take(max_blocks * bm * R * 4);
-  z.table = take(((int64_t)z.max_segs * kLgSegInts + z.max_parts / 2 * kLgJoinInts) * 4);
+  z.packed = take(z.direct ? 0 : max_blocks * bm * R * 4);
+  z.table = take(z.seg_blocks == 1 ? 0 : ((int64_t)z.max_segs * kLgSegInts + z.max_parts / 2 * kLgJoinInts) * 4);
   z.da_part = take((int64_t)z.max_parts * R * K * 4);
   z.db_part = take((int64_t)z.max_parts * R * N * 4);
   z.bytes = at;
@@ -463,8 +519,8 @@ hipError_t launch_lora_grad_join(const LoraGradParams& p, hipStream_t stream) {
   if (p.max_parts == 0) return hipSuccess;
   const int64_t quads = (int64_t)p.R * (p.K + p.N) / 4;
   const int64_t want = (quads + kLoraThreads - 1) / kLoraThreads;
-  hipLaunchKernelGGL(lora_grad_join_kernel, dim3((uint32_t)(want < 1024 ? want : 1024), p.max_parts / 2),
-                     dim3(kLoraThreads), 0, stream, p);
+  const uint32_t groups = p.table != nullptr ? p.max_parts / 2 : p.max_parts;
+  hipLaunchKernelGGL(lora_grad_join_kernel, dim3((uint32_t)(want < 1024 ? want : 1024), groups), dim3(kLoraThreads), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -186,10 +186,11 @@ struct LoraGradParams {
   const uint16_t* b;
   int64_t b_g, b_ld;
   const float* h;
-  float* dh;  // [parts of N][places][R]; joined, the first holds dh
+  float* dh;  // [parts of N][places][R]; joined, the first holds scale times their sum
+  int32_t parts;  // of dh, for the pass over x to add and scale; 0: joined
   float* da;  // or null, as db
   float* db;
-  int32_t* table;
+  int32_t* table;  // null: every block is a segment
   int32_t seg_blocks, max_segs, max_parts;
   float* da_part;
   float* db_part;
@@ -247,6 +248,7 @@ hipError_t launch_lora_up_few(const LoraParams& p, hipStream_t stream);
 hipError_t launch_lora_both(const LoraParams& p, hipStream_t stream);
 struct LoraGradSizes {
   int32_t n_parts, seg_blocks, max_segs, max_parts;
+  bool direct;  // `up` and the pass over x take the parts of dh
   int64_t dh, packed, table, da_part, db_part, bytes;  // offsets into the workspace and its size
 };
 LoraGradSizes lora_grad_sizes(int32_t G, int32_t R, int64_t K, int64_t N, int32_t bm, int64_t max_blocks);
