@@ -135,6 +135,13 @@ def test_lora_long_lists(S, G, R):
     Case(S, G, R, 520, 264, 1, None, seed=S, scale=False).run()
 
 
+@pytest.mark.parametrize("S,G,R,K,N,bm", [(20000, 3, 16, 136, 264, None), (9000, 40, 128, 72, 136, 16),
+                                          (6000, 1, 8, 264, 72, 8), (3000, 2, 32, 72, 4104, 16)])
+def test_lora_segments_of_several_blocks(S, G, R, K, N, bm):
+    """Lists of more blocks than the gradients have segments for."""
+    Case(S, G, R, K, N, 2, bm, seed=S + R).run()
+
+
 def test_lora_without_slots():
     moe = _moe()
     case = Case(0, 3, 16, 64, 48)
