@@ -71,7 +71,8 @@ typedef enum {
  *     scales = X + 127, q = E4M3 nearest to u / 2^X, ties to even, saturated at
  *     448; a block holding a NaN or infinity becomes scales 0xFF, q 0x7F
  *   quant PER_TOKEN: scales[r] = max(max|u| / 448, 2^-126), q = E4M3 nearest to
- *     u / scales[r]; a row holding a NaN or infinity becomes scales NaN, q 0x7F
+ *     the fp32 quotient u / scales[r], ties to even; a row holding a NaN or
+ *     infinity becomes scales NaN, q 0x7F
  * The statistics and the 8-bit forms come from the unrounded v and u. A row
  * whose sum of squares passes fp32's range gives what that formula gives in
  * fp32. */

@@ -1,0 +1,59 @@
+"""GPU tests of moe_rmsnorm and moe_rmsnorm_backward at inputs whose sums and
+statistics are exact in fp32, so that the outputs have one right value and no
+tolerance: rows of ones and minus ones have mean v^2 = 1 and, with eps = 0,
+1 / sqrt = 1.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from helpers import need_gpu
+from oracle import formats, quant
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _moe():
+    import mixture_experts_grouped_moe_amd as moe
+    return moe
+
+
+def e4m3_borders():
+    """The midpoints between neighbouring E4M3 magnitudes."""
+    v = formats.e4m3_to_f64(np.arange(127, dtype=np.uint8))   # 0 ... 448
+    return (v[1:] + v[:-1]) / 2
+
+
+# largest magnitudes: ordinary ones, scales next to the smallest and below it, and fp32's largest
+TOPS = [1.0, 1.2345, 447.9, 3.3e-5, 1.7e19, 448 * 1.75 * 2.0 ** -126, 448 * 2.0 ** -126, 2.0 ** -121, 3.4e38]
+
+
+@pytest.mark.parametrize("top", TOPS)
+@pytest.mark.parametrize("n", [1536, 6144])   # a row in two waves and in eight
+def test_per_token_codes_at_the_borders(top, n):
+    """u is the weight: those next to a border between two codes, times the
+    row's scale. A code is the nearest to the fp32 quotient u / scale, ties to
+    even."""
+    top = np.float32(top)
+    scale = max(np.float32(top / np.float32(448)), np.float32(2.0 ** -126))
+    at = (e4m3_borders() * np.float64(scale)).astype(np.float32)
+    step = np.arange(-5, 6)[:, None]
+    w = (at.view(np.int32)[None, :] + step).view(np.float32).reshape(-1)
+    w = w[np.isfinite(w) & (np.abs(w) <= top)][:n - 1]
+    w = np.concatenate([[top], w, np.zeros(n - 1 - w.size, np.float32)]).astype(np.float32)
+    sign = np.where(np.arange(n) % 3 == 1, -1.0, 1.0)
+    x = torch.from_numpy(np.stack([np.ones(n), sign])).to(torch.bfloat16).cuda()
+    _, _, q, s = _moe().moe_rmsnorm(x, torch.from_numpy(w).cuda(), eps=0.0, quant="per_token", keep_y=False)
+    assert (s.cpu().numpy() == scale).all()
+    quotient = np.stack([w, w * sign.astype(np.float32)]) / scale
+    assert quotient.dtype == np.float32
+    want = formats.e4m3_to_f64(quant.e4m3_round(quotient))
+    got = formats.e4m3_to_f64(q.cpu().numpy())
+    off = got != want
+    assert not off.any(), f"{off.sum()} of {off.size} codes, e.g. u / scale {quotient[off][:4]}"
