@@ -160,8 +160,8 @@ int64_t moe_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t n);
  * C is what the shared projection wrote (moe_grouped_gemm, for one). Rows of C
  * and h of slots in no block are left as they were, and nothing that is in them
  * or in rows of x that no block names reaches a result. Products of bf16
- * values are exact, sums fp32; the second product takes h as two bf16 terms
- * (2^-16 relative), so an infinite value of B gives infinities or NaN. The
+ * values are exact, sums fp32; the second product takes h as three bf16 terms
+ * (all of fp32's bits), so an infinite value of B gives infinities or NaN. The
  * order of the sums depends on the sizes alone: repeated calls give equal bits.
  *
  * With groups = experts, moe_grouped_gemm's block list serves the adapters too
@@ -222,8 +222,7 @@ int64_t moe_lora_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t 
  * where x_row_div > 1, moe_combine_routed adds the rows of a token. dy passes
  * through to the shared projection unchanged. da and db are written for every
  * group, zeros for one without slots; both NULL: not computed (h and x are then
- * not read). The second product takes dh as two bf16 terms (2^-16 relative), the
- * weights' gradients dh and h as three (all of fp32's bits). Rows of dx of slots
+ * not read). The products take dh and h as three bf16 terms (all of fp32's bits). Rows of dx of slots
  * in no block are left as they were. */
 typedef struct {
   int64_t num_slots;

@@ -332,7 +332,6 @@ moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream) {
   p.w_g = a.a_stride_g;
   p.w_ld = a.a_ld;
   const moe::LoraSizes z = moe::lora_sizes(a.R, a.K, a.block_m, a.max_blocks);
-  char* base = static_cast<char*>(args->workspace);
   p.splits = z.splits;
   p.h = args->h;
   p.w2 = static_cast<const uint16_t*>(a.b);
@@ -341,14 +340,14 @@ moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream) {
   p.c = static_cast<uint16_t*>(args->c);
   p.c_ld = args->c_ld;
   if (z.both) return hip_status(moe::launch_lora_both(p, (hipStream_t)stream), "moe_lora launch");
-  p.part = reinterpret_cast<float*>(base);
-  if (!z.few && z.splits == 1) p.packed = reinterpret_cast<uint16_t*>(base + z.packed);
+  p.part = static_cast<float*>(args->workspace);
+  p.scaled = !z.few && z.splits == 1;
   st = hip_status(moe::launch_lora_down(p, (hipStream_t)stream), "moe_lora launch");
   if (st != MOE_OK) return st;
   if (!z.few && z.splits > 1) {
-    p.packed = reinterpret_cast<uint16_t*>(base + z.packed);
-    st = hip_status(moe::launch_lora_join(p, false, (hipStream_t)stream), "moe_lora launch");
+    st = hip_status(moe::launch_lora_join(p, (hipStream_t)stream), "moe_lora launch");
     if (st != MOE_OK) return st;
+    p.scaled = true;
   }
   return hip_status(z.few ? moe::launch_lora_up_few(p, (hipStream_t)stream)
                           : moe::launch_lora_up(p, false, (hipStream_t)stream),
@@ -424,11 +423,11 @@ moe_status moe_lora_backward(const moe_lora_backward_args* args, moe_stream_t st
   p.max_blocks = q.max_blocks;
   p.part = q.dh;
   p.splits = z.n_parts;
-  if (args->dx != nullptr && !z.direct) p.packed = reinterpret_cast<uint16_t*>(base + z.packed);
+  p.scaled = !z.direct;
   const hipStream_t on = (hipStream_t)stream;
   hipError_t err = z.seg_blocks > 1 ? moe::launch_lora_grad_table(q, on) : hipSuccess;
   if (err == hipSuccess) err = moe::launch_lora_grad_dy(q, on);
-  if (err == hipSuccess && !z.direct) err = moe::launch_lora_join(p, true, on);
+  if (err == hipSuccess && !z.direct) err = moe::launch_lora_join(p, on);
   if (err == hipSuccess && args->dx != nullptr) {
     p.N = (int32_t)a.K;
     p.w2 = static_cast<const uint16_t*>(a.a);

@@ -7,10 +7,10 @@
 // shared by its blocks through the caches; the products are 2 R flops a byte.
 // Every output column needs the whole of h = A x, so `down` forms h, a block of
 // slots and a part of K a workgroup, and `up` adds B h. h lies by place in the
-// block list; as `up` takes it, it is scaled and in two bf16 terms ("packed",
-// [place][hi, lo][R]), which `down` writes itself where K is not split, `join`
-// from the parts where it is; with few slots a small `up` reads the parts, two
-// launches in all, or one (`both`).
+// block list; `up` takes it scaled, as `down` writes it where K is not split and
+// `join` leaves it over the first part where it is; with few slots a small `up`
+// reads the parts, two launches in all, or one (`both`). The second product
+// takes h as three bf16 terms, all of its bits (lora_split).
 //
 // Measured (kernel times): 8192 slots of 8 groups, K = 7168, N = 4096, rank 32:
 // `down` 31 us (3.8 TB/s: a group's A is read again by each block, beside the
@@ -23,16 +23,6 @@
 #include "lora_util.h"
 
 namespace moe {
-
-// h as `up` takes it, four ranks of a place.
-__device__ __forceinline__ void lora_put_packed(uint16_t* packed, int64_t pos, int R, int r, f32x4_t h, float scale) {
-  uint32_t hi[2], lo[2];
-  lora_split(h[0] * scale, h[1] * scale, hi[0], lo[0]);
-  lora_split(h[2] * scale, h[3] * scale, hi[1], lo[1]);
-  uint16_t* to = packed + pos * (2 * R) + r;
-  *reinterpret_cast<u32x2_t*>(to) = u32x2_t{hi[0], hi[1]};
-  *reinterpret_cast<u32x2_t*>(to + R) = u32x2_t{lo[0], lo[1]};
-}
 
 // ------------------------------------------------------------------- down
 
@@ -145,7 +135,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
   f32x4_t acc[RT][MT];
   lora_down<4, RT, MT>(p, g, slot, live, first < (uint32_t)p.S ? first : 0, sp, p.splits, red, acc);
   if (wave > 0) return;
-  const float scale = p.packed != nullptr && p.scale != nullptr ? p.scale[g] : 1.0f;
+  const float scale = p.scaled && p.scale != nullptr ? p.scale[g] : 1.0f;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (!live[m]) continue;
@@ -154,19 +144,14 @@ __global__ __launch_bounds__(kLoraThreads) void lora_down_kernel(LoraParams p) {
     for (int t = 0; t < RT; ++t) {
       const int r = 16 * t + 4 * q;
       if (r >= p.R) continue;
-      if (p.packed != nullptr) {
-        lora_put_packed(p.packed, pos, p.R, r, acc[t][m], scale);
-        if (p.h != nullptr) *reinterpret_cast<f32x4_t*>(p.h + (int64_t)slot[m] * p.R + r) = acc[t][m];
-      } else {
-        *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)sp * p.max_blocks * p.bm + pos) * p.R + r) = acc[t][m];
-      }
+      *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)sp * p.max_blocks * p.bm + pos) * p.R + r) = acc[t][m] * scale;
+      if (p.scaled && p.h != nullptr) *reinterpret_cast<f32x4_t*>(p.h + (int64_t)slot[m] * p.R + r) = acc[t][m];
     }
   }
 }
 
-// Several parts -> h where it is wanted, and packed. (`over`: the scaled sum over
-// the first part, the backward pass's dh.)
-__global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraParams p, bool over) {
+// Several parts -> h where it is wanted, and scaled over the first part.
+__global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraParams p) {
   const int64_t places = (int64_t)p.max_blocks * p.bm, n = places * (p.R / 4);
   for (int64_t i = (int64_t)blockIdx.x * kLoraThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kLoraThreads) {
     const int64_t pos = i / (p.R / 4);
@@ -177,8 +162,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraParams p, b
     const float scale = p.scale != nullptr ? p.scale[g] : 1.0f;
     float* at = p.part + pos * p.R + r;
     const f32x4_t h = lora_sum_parts(at, places * p.R, p.splits);
-    if (p.packed != nullptr) lora_put_packed(p.packed, pos, p.R, r, h, scale);
-    if (over) *reinterpret_cast<f32x4_t*>(at) = h * scale;
+    *reinterpret_cast<f32x4_t*>(at) = h * scale;
     if (p.h != nullptr) *reinterpret_cast<f32x4_t*>(p.h + (int64_t)s * p.R + r) = h;
   }
 }
@@ -193,7 +177,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraParams p, b
 // while h is made.)
 template <int RC>
 struct LoraFew {
-  static constexpr int F = RC < 4 ? 1 : RC / 4, P = RC < 4 ? 1 : 2;
+  static constexpr int F = RC < 4 ? 1 : RC / 4, P = RC < 4 ? RC : 3;
   static constexpr int kRank = RC < 4 ? 16 : 8 * RC, kLd = kRank + 8;  // of a slot's row of h in LDS
   u32x4_t c[2], w[4][F];
   uint16_t* row;
@@ -219,30 +203,31 @@ struct LoraFew {
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
-        const bool in = piece < pieces && (RC != 1 || q < 2);
+        const bool in = piece < pieces && (RC != 1 || q < 3);
         const u32x4_t v = *reinterpret_cast<const u32x4_t*>(matrix + (int64_t)n * p.w2_ld + (in ? 8 * piece : 0));
         w[j][f] = in ? v : u32x4_t{0, 0, 0, 0};
       }
     }
   }
   // Four ranks of a place to LDS.
-  __device__ __forceinline__ static void put(uint16_t (&hs)[2][16][kLd], int place, int r, f32x4_t h) {
-    uint32_t hi[2], lo[2];
-    lora_split(h[0], h[1], hi[0], lo[0]);
-    lora_split(h[2], h[3], hi[1], lo[1]);
-    *reinterpret_cast<u32x2_t*>(&hs[0][place][r]) = u32x2_t{hi[0], hi[1]};
-    *reinterpret_cast<u32x2_t*>(&hs[1][place][r]) = u32x2_t{lo[0], lo[1]};
+  __device__ __forceinline__ static void put(uint16_t (&hs)[3][16][kLd], int place, int r, f32x4_t h) {
+    uint32_t a[3], b[3];
+    lora_split(h[0], h[1], a);
+    lora_split(h[2], h[3], b);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x2_t*>(&hs[k][place][r]) = u32x2_t{a[k], b[k]};
   }
   // Adds the pieces i, i + step, ... below end, the first of which is loaded.
-  __device__ __forceinline__ void add(const LoraParams& p, uint16_t (&hs)[2][16][kLd], int i, int step, int end) {
+  __device__ __forceinline__ void add(const LoraParams& p, uint16_t (&hs)[3][16][kLd], int i, int step, int end) {
     u32x4_t h[F][P];
 #pragma unroll
     for (int f = 0; f < F; ++f)
 #pragma unroll
       for (int k = 0; k < P; ++k) {
-        const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0, part = RC >= 4 ? k : RC == 2 ? q / 2 : q % 2;
-        h[f][k] = *reinterpret_cast<const u32x4_t*>(&hs[part][m16][8 * piece]);
-        if (RC == 1 && q >= 2) h[f][k] = u32x4_t{0, 0, 0, 0};
+        const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
+        const int term = RC >= 4 ? 2 - k : RC == 2 ? (k == 0 ? 2 : q / 2) : min(q, 2);
+        h[f][k] = *reinterpret_cast<const u32x4_t*>(&hs[term][m16][8 * piece]);
+        if ((RC == 1 && q == 3) || (RC == 2 && k == 0 && q >= 2)) h[f][k] = u32x4_t{0, 0, 0, 0};
       }
     for (; i < end; i += step) {
       const int n0 = 64 * i;
@@ -275,7 +260,7 @@ struct LoraFew {
 template <int RC>
 __global__ __launch_bounds__(kLoraThreads) void lora_up_few_kernel(LoraParams p) {
   using Few = LoraFew<RC>;
-  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][Few::kLd];
+  __shared__ __attribute__((aligned(16))) uint16_t hs[3][16][Few::kLd];
   const int wave = threadIdx.x / 64, m16 = threadIdx.x % 16;
   const int b = p.block0 + blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
   const int g = p.groups[b];
@@ -310,7 +295,7 @@ __global__ __launch_bounds__(512) void lora_both_kernel(LoraParams p) {
   using Few = LoraFew<RC>;
   constexpr int RT = (RC + 1) / 2;
   __shared__ f32x4_t red[4][RT][64];
-  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][Few::kLd];
+  __shared__ __attribute__((aligned(16))) uint16_t hs[3][16][Few::kLd];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
   const int b = p.block0 + blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
   const int g = p.groups[b];
@@ -343,21 +328,28 @@ __global__ __launch_bounds__(512) void lora_both_kernel(LoraParams p) {
 
 // --------------------------------------------------------------------- up
 
+// Waves per SIMD: three up to rank 16 (32768 slots of 128 groups, 5760 columns:
+// 188 us for the whole call, 208 at two; with the parts' sums its registers do not
+// suffice), two up to 64 (8192 slots of 8 groups, 4096 columns, rank 32: 69 us, 78
+// at three).
+constexpr int lora_up_waves(int RC, bool parts) { return RC == 1 || (RC == 2 && !parts) ? 3 : RC <= 8 ? 2 : 1; }
+
 // A wave keeps 16 NT columns of a group's B in registers and takes the run's
 // slots 16 at a time, ids two tiles ahead, C and h one ahead. D rows are slots,
 // columns those of C: column m of tile j stands for column NT m + j, so that a
 // lane holds NT consecutive columns of 4 slots and an access of C is 256
 // contiguous bytes of 4 rows (28672 gathered rows of 5760, read and written back
-// with no product: 4.7 TB/s so, 4.1 to 4.4 in 64-byte pieces of 16 rows). h
-// enters as hi + lo: for ranks up to 16 both lie in one MFMA's k (RC = 2: hi hi
-// lo lo, RC = 1: hi lo and two zeros, in pieces of 8), beyond, each piece of 32
-// ranks of B meets hi and lo in turn. PARTS: h comes from its parts, added, scaled
-// and split by every wave. TURNED: the matrix is [R][N] (dx, whose
+// with no product: 4.7 TB/s so, 4.1 to 4.4 in 64-byte pieces of 16 rows). Every
+// wave splits h: each piece of 32 ranks of B meets the three terms in turn, the
+// smallest first; up to 16 ranks an MFMA's k of 32 holds several (RC = 2: the
+// third term and zeros, then the first and the second; RC = 1: all three and
+// zeros, in pieces of 8). PARTS: h comes from its parts, added and scaled by every
+// wave. TURNED: the matrix is [R][N] (dx, whose
 // matrix is A itself): a lane reads its 8 columns of each of 8 ranks and turns
 // the 8 x 8 around in registers.
 template <int RC, bool TURNED, bool PARTS>
-__global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
-  constexpr int F = RC < 4 ? 1 : RC / 4, P = RC < 4 ? 1 : 2;
+__global__ __launch_bounds__(kLoraThreads, lora_up_waves(RC, PARTS)) void lora_up_kernel(LoraParams p) {
+  constexpr int F = RC < 4 ? 1 : RC / 4, P = RC < 4 ? RC : 3;
   constexpr int NT = 8, kCols = 16 * NT;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
   const int run = blockIdx.x / p.n_splits, n0 = (blockIdx.x % p.n_splits * 4 + wave) * kCols;
@@ -372,12 +364,14 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
   // column past N the last ones; what comes of them is not stored. (A tile of a
   // block without a group is passed over.)
   const int col = n0 + NT * m16 < p.N ? n0 + NT * m16 : p.N - NT;
+  uint16_t* c0 = p.c + col;
   struct Ids {
     int slot[4], first, group;
   };
   struct Tile {
-    u32x4_t c[4], h[F][P];
-    uint16_t* to[4];
+    u32x4_t c[4];
+    f32x4_t h[F][2];  // 8 ranks of place m16
+    int to[4];  // the rows' slots; -1: not stored
     int group;
   };
   auto load_ids = [&](Ids& v, int t) {
@@ -395,51 +389,26 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const bool live = row + 4 * q < p.bm && (uint32_t)ids.slot[r] < (uint32_t)p.S;
-      uint16_t* at = p.c + (int64_t)(live ? ids.slot[r] : first) * p.c_ld + col;
-      v.to[r] = live && in ? at : nullptr;
-      v.c[r] = *reinterpret_cast<const u32x4_t*>(at);
+      v.to[r] = live && in ? ids.slot[r] : -1;
+      v.c[r] = *reinterpret_cast<const u32x4_t*>(c0 + (int64_t)(live ? ids.slot[r] : first) * p.c_ld);
     }
     const int64_t pos = (int64_t)((t0 + t) >> shift) * p.bm + min(row + m16, p.bm - 1);
-    if constexpr (PARTS) {
-      const float scale = p.scale != nullptr ? p.scale[v.group] : 1.0f;
-      const int64_t step = (int64_t)p.max_blocks * p.bm * p.R;
+    const float scale = PARTS && p.scale != nullptr ? p.scale[v.group] : 1.0f;
 #pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
-        const bool here = piece < pieces && (RC != 1 || q < 2);
-        const float* at = p.part + pos * p.R + (here ? 8 * piece : 0);
-        const f32x4_t a = lora_sum_parts(at, step, p.splits) * scale;
-        const f32x4_t b = lora_sum_parts(at + 4, step, p.splits) * scale;
-        u32x4_t hi, lo;
+    for (int f = 0; f < F; ++f) {
+      const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
+      const bool here = piece < pieces;
+      const float* at = p.part + pos * p.R + (here ? 8 * piece : 0);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t w[2];
-          lora_split(a[2 * e], a[2 * e + 1], w[0], w[1]);
-          hi[e] = w[0];
-          lo[e] = w[1];
-          lora_split(b[2 * e], b[2 * e + 1], w[0], w[1]);
-          hi[2 + e] = w[0];
-          lo[2 + e] = w[1];
-        }
-#pragma unroll
-        for (int k = 0; k < P; ++k) {
-          const bool low = RC >= 4 ? k == 1 : RC == 2 ? q >= 2 : q == 1;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v.h[f][k][e] = !here ? 0 : low ? lo[e] : hi[e];
-        }
+      for (int e = 0; e < 2; ++e) {
+        f32x4_t h;
+        if constexpr (PARTS)
+          h = lora_sum_parts(at + 4 * e, (int64_t)p.max_blocks * p.bm * p.R, p.splits) * scale;
+        else
+          h = *reinterpret_cast<const f32x4_t*>(at + 4 * e);
+        v.h[f][e] = here ? h : f32x4_t{0, 0, 0, 0};
       }
-      return;
     }
-    const uint16_t* at = p.packed + pos * (2 * p.R);
-#pragma unroll
-    for (int f = 0; f < F; ++f)
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const int piece = RC >= 4 ? 4 * f + q : q;  // (RC < 4: hi and lo pieces follow each other)
-        const bool here = RC >= 4 ? piece < pieces : q < 2 * RC;
-        const u32x4_t h = *reinterpret_cast<const u32x4_t*>(at + (here ? k * p.R + 8 * piece : 0));
-        v.h[f][k] = here ? h : u32x4_t{0, 0, 0, 0};
-      }
   };
   u32x4_t wv[NT][F];
   int have = -1;  // the group whose B is here
@@ -450,7 +419,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int piece = RC >= 4 ? 4 * f + q : RC == 2 ? q % 2 : 0;
-        const bool here = piece < pieces && (RC != 1 || q < 2);
+        const bool here = piece < pieces && (RC != 1 || q < 3);
         u32x4_t w[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -474,12 +443,31 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
     if ((uint32_t)v.group >= (uint32_t)p.G) return;
     f32x4_t d[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      d[j] = f32x4_t{0, 0, 0, 0};
+    for (int j = 0; j < NT; ++j) d[j] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int f = 0; f < F; ++f)
+    for (int f = 0; f < F; ++f) {
+      u32x4_t t[3], h[P];
 #pragma unroll
-        for (int k = 0; k < P; ++k) d[j] = lora_mfma(v.h[f][k], wv[j][f], d[j]);
+      for (int e = 0; e < 4; ++e) {
+        uint32_t w[3];
+        lora_split(v.h[f][e / 2][2 * (e % 2)], v.h[f][e / 2][2 * (e % 2) + 1], w);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) t[k][e] = w[k];
+      }
+      const u32x4_t none = {0, 0, 0, 0};
+      if constexpr (RC >= 4) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) h[k] = t[2 - k];
+      } else if constexpr (RC == 2) {
+        h[0] = q < 2 ? t[2] : none;
+        h[1] = q < 2 ? t[0] : t[1];
+      } else {
+        h[0] = q == 0 ? t[0] : q == 1 ? t[1] : q == 2 ? t[2] : none;
+      }
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) d[j] = lora_mfma(h[k], wv[j][f], d[j]);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -488,7 +476,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_kernel(LoraParams p) {
       for (int w = 0; w < 4; ++w)
         o[w] = lora_pack(__uint_as_float(v.c[r][w] << 16) + d[2 * w][r],
                          __uint_as_float(v.c[r][w] & 0xffff0000u) + d[2 * w + 1][r]);
-      if (v.to[r] != nullptr) *reinterpret_cast<u32x4_t*>(v.to[r]) = o;
+      if (v.to[r] >= 0) *reinterpret_cast<u32x4_t*>(c0 + (int64_t)v.to[r] * p.c_ld) = o;
     }
   };
   Ids ids;
@@ -541,16 +529,13 @@ static bool lora_both(int64_t max_blocks, int bm, int R, int64_t K) {
   return lora_few(max_blocks, bm) && R <= 32 && K * R <= 32768;
 }
 
-// Of moe_lora's workspace: the parts of h, then packed (neither where it is not used).
 LoraSizes lora_sizes(int32_t R, int64_t K, int32_t bm, int64_t max_blocks) {
   LoraSizes z{};
   z.both = lora_both(max_blocks, bm, R, K);
   if (z.both) return z;
   z.few = lora_few(max_blocks, bm);
   z.splits = lora_k_splits(max_blocks, K);
-  const int64_t h = max_blocks * bm * R * 4;
-  z.packed = z.few || z.splits > 1 ? z.splits * h : 0;
-  z.bytes = z.packed + (z.few ? 0 : h);
+  z.bytes = z.splits * max_blocks * bm * R * 4;
   return z;
 }
 
@@ -586,11 +571,10 @@ hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream) {
   });
 }
 
-hipError_t launch_lora_join(const LoraParams& p, bool over, hipStream_t stream) {
+hipError_t launch_lora_join(const LoraParams& p, hipStream_t stream) {
   const int64_t want = ((int64_t)p.max_blocks * p.bm * (p.R / 4) + kLoraThreads - 1) / kLoraThreads;
   if (want == 0) return hipSuccess;
-  hipLaunchKernelGGL(lora_join_kernel, dim3((uint32_t)(want < 4096 ? want : 4096)), dim3(kLoraThreads), 0, stream, p,
-                     over);
+  hipLaunchKernelGGL(lora_join_kernel, dim3((uint32_t)(want < 4096 ? want : 4096)), dim3(kLoraThreads), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -617,9 +601,9 @@ hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream)
     for (int64_t r = 0; r < runs; r += most) {
       q.block0 = (int32_t)(r * p.run_tiles / per);
       const int64_t n = runs - r < most ? runs - r : most;
-      auto kernel = !turned               ? lora_up_kernel<RC, false, false>
-                    : q.packed != nullptr ? lora_up_kernel<RC, true, false>
-                                          : lora_up_kernel<RC, true, true>;
+      auto kernel = !turned    ? lora_up_kernel<RC, false, false>
+                    : q.scaled ? lora_up_kernel<RC, true, false>
+                               : lora_up_kernel<RC, true, true>;
       hipLaunchKernelGGL(kernel, dim3((uint32_t)(n * p.n_splits)), dim3(kLoraThreads), 0, stream, q);
       const hipError_t err = hipGetLastError();
       if (err != hipSuccess) return err;

@@ -305,7 +305,7 @@ __global__ __launch_bounds__(kLgThreads, RT == 1 ? 4 : 2) void lora_wide_kernel(
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t term[3];
-          lora_split3(h[2 * k], h[2 * k + 1], term);
+          lora_split(h[2 * k], h[2 * k + 1], term);
 #pragma unroll
           for (int j = 0; j < 3; ++j) {
             narrow[j][r + 2 * k][nslot] = (uint16_t)term[j];
@@ -488,7 +488,6 @@ LoraGradSizes lora_grad_sizes(int32_t G, int32_t R, int64_t K, int64_t N, int32_
   // parts 20.9 and 20.8, 14 parts 28.5 and 25.3; rank 64 at 6 parts 31.4 and 30.4)
   z.direct = z.seg_blocks == 1 && z.n_parts * R <= 128;
   z.dh = take(z.n_parts * max_blocks * bm * R * 4);
-  z.packed = take(z.direct ? 0 : max_blocks * bm * R * 4);
   z.table = take(z.seg_blocks == 1 ? 0 : ((int64_t)z.max_segs * kLgSegInts + z.max_parts / 2 * kLgJoinInts) * 4);
   z.da_part = take((int64_t)z.max_parts * R * K * 4);
   z.db_part = take((int64_t)z.max_parts * R * N * 4);

@@ -28,26 +28,22 @@ __device__ __forceinline__ uint32_t lora_pack(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// f = hi + lo to 2^-16 of f for two floats, both terms bf16 pairs. hi is rounded
-// to nearest, or towards zero where that would pass bf16's range; an infinite or
-// NaN f is hi alone.
-__device__ __forceinline__ void lora_split(float f0, float f1, uint32_t& hi, uint32_t& lo) {
-  constexpr float kMost = 0x1.FEp127f;  // bf16's largest
-  const float m0 = fabsf(f0) < INFINITY ? fminf(fmaxf(f0, -kMost), kMost) : f0;
-  const float m1 = fabsf(f1) < INFINITY ? fminf(fmaxf(f1, -kMost), kMost) : f1;
-  hi = lora_pack(m0, m1);
-  const float r0 = f0 - __uint_as_float(hi << 16), r1 = f1 - __uint_as_float(hi & 0xffff0000u);
-  lo = lora_pack(fabsf(f0) < INFINITY ? r0 : 0.0f, fabsf(f1) < INFINITY ? r1 : 0.0f);
-}
-
-// f as three bf16 terms, all of its 24 bits (to what bf16's smallest holds).
-__device__ __forceinline__ void lora_split3(float f0, float f1, uint32_t (&t)[3]) {
-  uint32_t lo;
-  lora_split(f0, f1, t[0], lo);
-  const float r0 = fabsf(f0) < INFINITY ? f0 - __uint_as_float(t[0] << 16) : 0.0f;
-  const float r1 = fabsf(f1) < INFINITY ? f1 - __uint_as_float(t[0] & 0xffff0000u) : 0.0f;
-  t[1] = lo;
-  t[2] = lora_pack(r0 - __uint_as_float(lo << 16), r1 - __uint_as_float(lo & 0xffff0000u));
+// f = t[0] + t[1] + t[2] for two floats, the terms bf16 pairs, each the upper half
+// of what the ones before it leave: 8 of a float's 24 bits at a time, so that all
+// are there (to what bf16's smallest holds), and none passes bf16's range. An
+// infinite f is the first term alone. (Two terms lose the products' last bits,
+// which show where they cancel what they are added to.)
+__device__ __forceinline__ void lora_split(float f0, float f1, uint32_t (&t)[3]) {
+  uint32_t a = __float_as_uint(f0), b = __float_as_uint(f1);
+  t[0] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+  f0 = fabsf(f0) == INFINITY ? 0.0f : f0 - __uint_as_float(a & 0xffff0000u);
+  f1 = fabsf(f1) == INFINITY ? 0.0f : f1 - __uint_as_float(b & 0xffff0000u);
+  a = __float_as_uint(f0);
+  b = __float_as_uint(f1);
+  t[1] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+  f0 -= __uint_as_float(a & 0xffff0000u);
+  f1 -= __uint_as_float(b & 0xffff0000u);
+  t[2] = __builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
 }
 
 // floor(s / d) for s < 2^31 (lora_set_division).

@@ -163,8 +163,8 @@ struct LoraParams {
   int64_t w_g, w_ld;
   const uint16_t* w2;  // B (dx: A)
   int64_t w2_g, w2_ld;
-  float* part;       // h in parts of K, [splits][places][R]
-  uint16_t* packed;  // h as the large `up` takes it, [places][2][R] bf16
+  float* part;  // h in parts of K, [splits][places][R]
+  bool scaled;  // the first part holds scale times the whole of h
   int32_t splits, n_splits, run_tiles;
   float* h;  // [S][R], or null
   uint16_t* c;
@@ -238,18 +238,18 @@ struct LoraSizes {
   bool both;       // both products in one launch, without a workspace
   bool few;        // the small `up`, which reads the parts
   int32_t splits;  // parts of K
-  int64_t packed, bytes;  // offset into the workspace and its size
+  int64_t bytes;   // of the workspace: the parts of h
 };
 LoraSizes lora_sizes(int32_t R, int64_t K, int32_t bm, int64_t max_blocks);
 hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream);
-hipError_t launch_lora_join(const LoraParams& p, bool over, hipStream_t stream);
+hipError_t launch_lora_join(const LoraParams& p, hipStream_t stream);
 hipError_t launch_lora_up(const LoraParams& p, bool turned, hipStream_t stream);
 hipError_t launch_lora_up_few(const LoraParams& p, hipStream_t stream);
 hipError_t launch_lora_both(const LoraParams& p, hipStream_t stream);
 struct LoraGradSizes {
   int32_t n_parts, seg_blocks, max_segs, max_parts;
   bool direct;  // `up` and the pass over x take the parts of dh
-  int64_t dh, packed, table, da_part, db_part, bytes;  // offsets into the workspace and its size
+  int64_t dh, table, da_part, db_part, bytes;  // offsets into the workspace and its size
 };
 LoraGradSizes lora_grad_sizes(int32_t G, int32_t R, int64_t K, int64_t N, int32_t bm, int64_t max_blocks);
 hipError_t launch_lora_grad_table(const LoraGradParams& p, hipStream_t stream);
