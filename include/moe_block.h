@@ -201,7 +201,9 @@ typedef struct {
  * max_blocks >= moe_align_max_blocks(num_slots, num_groups, block_m) and
  * max_blocks * block_m < 2^31. A block whose group id lies outside
  * [0, num_groups) and a slot id outside [0, num_slots) are skipped; no slot may
- * stand in the list twice. c, h and workspace must not overlap each other or an
+ * stand in the list twice, so num_slots is at most the number that the list was
+ * aligned for, which its padding places hold, however many rows c, x and h have
+ * behind those. c, h and workspace must not overlap each other or an
  * input. */
 moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream);
 

@@ -21,7 +21,7 @@ __all__ = [
     "moe_align", "moe_grouped_gemm", "moe_grouped_gemm_prepare", "moe_combine", "moe_wgrad",
     "moe_quantize_mxfp8", "moe_block_mapping", "moe_grouped_gemm_per_token",
     "moe_grouped_gemm_per_token_prepare",
-    "moe_pack_weights", "moe_packed_sizes", "PackedWeights", "MOE_LAYOUT_ROWS", "MOE_LAYOUT_KBLOCK",
+    "moe_pack_weights", "moe_packed_sizes", "PackedWeights", "Routing", "MOE_LAYOUT_ROWS", "MOE_LAYOUT_KBLOCK",
     "moe_w4a16_layer", "moe_relu2_layer", "moe_decode_layer", "moe_decode_layer_prepare",
     "moe_decode_layer_fits",
     "LIB_PATH",
@@ -240,12 +240,18 @@ def moe_pack_weights(w, w_dtype, w_scale=None, stream=None):
 
 
 
+class Routing(tuple):
+    """moe_align's (sorted_token_ids, expert_ids, num_tokens_post_pad), with the
+    number of slots that they were made for (num_slots): a padding place holds
+    it, so it is no slot of theirs in a buffer of more rows either."""
+
+
 def moe_align(topk_ids, num_experts, block_m, num_tokens=None, out=None, stream=None):
     """Sort slots by expert and pad each expert to block_m.
 
     topk_ids: int32 [T, top_k] on the device. Returns (sorted_token_ids,
-    expert_ids, num_tokens_post_pad) as int32 device tensors; `out` may give
-    preallocated ones. num_tokens (default T) routes only the first rows.
+    expert_ids, num_tokens_post_pad) as int32 device tensors, a Routing; `out`
+    may give preallocated ones. num_tokens (default T) routes only the first rows.
     """
     _need(topk_ids, "topk_ids", torch.int32, 2)
     if not topk_ids.is_contiguous():
@@ -267,7 +273,9 @@ def moe_align(topk_ids, num_experts, block_m, num_tokens=None, out=None, stream=
     _check(lib.moe_align(_ptr(topk_ids), T, k, int(num_experts), int(block_m),
                          _ptr(sorted_ids), _ptr(expert_ids), _ptr(post_pad), max_blocks,
                          _stream(stream)))
-    return sorted_ids, expert_ids, post_pad
+    routing = Routing((sorted_ids, expert_ids, post_pad))
+    routing.num_slots = T * k
+    return routing
 
 
 def _weight_args(g, w, w_dtype, w_scale, bias, K):

@@ -319,6 +319,20 @@ def _adapters(t, name):
     return G, r, c, sg if G > 1 else r * ld, ld
 
 
+def _lora_slots(routing, num_slots, rows, name):
+    """The number of slots: num_slots, or what the list was made for (the rows
+    of C or dy where it does not say), at most `rows`."""
+    made = getattr(routing, "num_slots", None)
+    if num_slots is None:
+        return rows if made is None or made > rows else made
+    S = int(num_slots)
+    if S < 0 or S > rows:
+        raise ValueError(f"num_slots must be in [0, {rows}], the rows of {name}, got {S}")
+    if made is not None and S > made:
+        raise ValueError(f"num_slots {S} exceeds the {made} slots that the routing was made for")
+    return S
+
+
 def _lora_args(x, a, b, routing, scale, row_div, S, N):
     """The arguments that both adapter entry points share: (sizes, fields, G, R, K)."""
     G, R, K, a_g, a_ld = _adapters(a, "a")
@@ -346,19 +360,23 @@ def _lora_args(x, a, b, routing, scale, row_div, S, N):
 
 
 @_on_stream
-def moe_lora(c, x, a, b, routing, scale=None, row_div=1, keep_h=False, workspace=None):
+def moe_lora(c, x, a, b, routing, scale=None, row_div=1, keep_h=False, workspace=None, num_slots=None):
     """Adds low-rank adapters to a shared projection's output, in place:
     c[s] += scale[g] * b[g] @ (a[g] @ x[s // row_div]) for the slots s of every
     group g.
 
-    c: bf16 [S, N], the projection's output; x: bf16 [S / row_div, K], its
+    c: bf16 [at least S, N], the projection's output; x: bf16 [S / row_div, K], its
     input; a: bf16 [G, R, K], b: bf16 [G, N, R] (8 <= R <= 128, a multiple of 8;
     rows and matrices may be strided); scale: fp32 [G]; routing: moe_align's
     over the slots' group ids, at block size 8, 16, 32 or 64
     (moe_lora_block_m(S, G); with groups = experts, the grouped GEMM's own).
-    Slots in no group keep their rows. Returns c; with keep_h (c, h), h fp32
-    [S, R] = a @ x of the routed slots for moe_lora_backward."""
-    S, N, c_ld = _mat(c, "c", torch.bfloat16)
+    Slots in no group keep their rows, and so do rows of c behind the slots. S
+    is what moe_align made the routing for; num_slots takes fewer of them, or
+    says it for a list of one's own, whose padding must hold no number below
+    it (default: the rows of c). Returns c; with keep_h (c, h), h fp32 [S, R] =
+    a @ x of the routed slots for moe_lora_backward."""
+    rows, N, c_ld = _mat(c, "c", torch.bfloat16)
+    S = _lora_slots(routing, num_slots, rows, "c")
     sizes, args = _lora_args(x, a, b, routing, scale, row_div, S, N)
     h = torch.empty((S, sizes[2]), dtype=torch.float32, device=c.device) if keep_h else None
     ws_p, ws_n, ws = _workspace(workspace, _lora_bytes(*sizes, *args[-2:]) if workspace is None else 0, c)
@@ -369,16 +387,17 @@ def moe_lora(c, x, a, b, routing, scale=None, row_div=1, keep_h=False, workspace
 
 @_on_stream
 def moe_lora_backward(dy, x, a, b, routing, h, scale=None, row_div=1, dx=None, weights=True, out=None,
-                      workspace=None):
-    """Gradients of moe_lora from dy (bf16 [S, N], the gradient of c after the
-    addition) and the h that the forward pass kept.
+                      workspace=None, num_slots=None):
+    """Gradients of moe_lora from dy (bf16 [at least S, N], the gradient of c
+    after the addition) and the h that the forward pass kept.
 
     Returns (da fp32 [G, R, K], db fp32 [G, N, R]), zeros for groups without
-    slots; (None, None) with weights=False. dx (bf16 [S, K], the shared
+    slots; (None, None) with weights=False. dx (bf16 [at least S, K], the shared
     projection's gradient of its input, a row per slot) gets the adapters' part
     added in place. The other arguments as in the forward pass; `out` may give
     da and db."""
-    S, N, dy_ld = _mat(dy, "dy", torch.bfloat16)
+    rows, N, dy_ld = _mat(dy, "dy", torch.bfloat16)
+    S = _lora_slots(routing, num_slots, rows, "dy")
     sizes, args = _lora_args(x, a, b, routing, scale, row_div, S, N)
     _, G, R, K, _ = sizes
     da = db = None
