@@ -115,7 +115,8 @@ moe_status moe_rmsnorm(const moe_rmsnorm_args* args, moe_stream_t stream);
  *   d = dsum[r] + s (g - v s^2 mean_i(g[i] v[i]))    (dsum NULL: 0)
  *   dresidual[r] = d       (sum_dtype; NULL: not stored)
  *   dx[r] = bf16(drop(d))  (NULL: not stored)
- *   dweight = sum_r dy[r] v s   (fp32 [n], one fixed order; NULL: not computed) */
+ *   dweight = sum_r dy[r] v s   (fp32 [n]; NULL: not computed. A workgroup's rows are
+ *   added in 32 bits, their sums in 64, in one fixed order) */
 typedef struct {
   int64_t rows;
   int64_t n;

@@ -401,7 +401,7 @@ __global__ __launch_bounds__(THREADS, kNormBwdWaves) void norm_backward_kernel(N
     }
   }
   if (p.dw == nullptr) return;
-  if constexpr (kRows > 1) {  // the row groups' terms, added in order
+  if constexpr (kRows > 1) {  // the row groups' terms, added in order, in 64 bits
     __shared__ f32x4_t terms[kRows][LANES * V * 2];
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -414,26 +414,33 @@ __global__ __launch_bounds__(THREADS, kNormBwdWaves) void norm_backward_kernel(N
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        double a[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = acc[j][4 * h + e];
         for (int i = 1; i < kRows; ++i) {
           const f32x4_t t = terms[i][(2 * j + h) * LANES + lane];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[j][4 * h + e] += t[e];
+          for (int e = 0; e < 4; ++e) a[e] += t[e];
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][4 * h + e] = (float)a[e];
+      }
   }
   norm_store<LANES, V, true>(p.partial, blockIdx.x, (int64_t)p.pieces * 8, lane, p.pieces, acc);
 }
 
-// dweight[c] = the sum of the partial rows: 64 strands of rows a workgroup, 8
-// loads of a strand in flight, the strands added in order.
+// dweight[c] = the sum of the partial rows, in 64 bits: 64 strands of rows a
+// workgroup, 8 loads of a strand in flight, the strands added in order.
 __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* __restrict__ partial, int32_t parts, int32_t n,
                                                             float* __restrict__ dw) {
   constexpr int kStrands = 64, kAhead = 8;
-  __shared__ f32x4_t s[kStrands][kNormFinCols / 4];
+  typedef double f64x4_t __attribute__((ext_vector_type(4)));
+  __shared__ f64x4_t s[kStrands][kNormFinCols / 4];
   const int c = threadIdx.x % (kNormFinCols / 4), k = threadIdx.x / (kNormFinCols / 4);
   const int col = blockIdx.x * kNormFinCols + 4 * c;
   const f32x4_t* p = reinterpret_cast<const f32x4_t*>(partial + col);
-  f32x4_t a = {0, 0, 0, 0};
+  f64x4_t a = {0, 0, 0, 0};
   if (col < n) {
     for (int i = k; i < parts; i += kStrands * kAhead) {
       f32x4_t v[kAhead];
@@ -443,7 +450,9 @@ __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* __restr
         v[j] = r < parts ? p[(int64_t)r * (n / 4)] : f32x4_t{0, 0, 0, 0};
       }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) a += v[j];
+      for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] += v[j][e];
     }
   }
   s[k][c] = a;
@@ -456,7 +465,7 @@ __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* __restr
   if (k == 0 && col < n) {
     for (int i = 1; i < 8; ++i) a += s[i][c];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dw[col + i] = a[i];
+    for (int i = 0; i < 4; ++i) dw[col + i] = (float)a[i];
   }
 }
 

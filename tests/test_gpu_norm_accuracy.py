@@ -55,5 +55,26 @@ def test_per_token_codes_at_the_borders(top, n):
     assert quotient.dtype == np.float32
     want = formats.e4m3_to_f64(quant.e4m3_round(quotient))
     got = formats.e4m3_to_f64(q.cpu().numpy())
-    off = got != want
-    assert not off.any(), f"{off.sum()} of {off.size} codes, e.g. u / scale {quotient[off][:4]}"
+    off = int((got != want).sum())
+    assert off == 0, f"{off} of {got.size} codes, e.g. u / scale {quotient[got != want][:4]}"
+
+
+# rows that are workgroups' own (a partial row each), and one workgroup for all
+# rows, whose row groups' terms it adds (16 and 4 of them). Within one of several
+# workgroups rows are added in 32 bits.
+@pytest.mark.parametrize("T,n", [(300, 1040), (500, 2056), (250, 16384), (16, 64), (4, 512)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_dweight_of_rows_that_cancel(T, n, dtype):
+    """dweight = sum of dy (v / sqrt = +-1): two rows of 2^15 cancel, one at each
+    end, and what is between them is 2^-10 times whole numbers, which 32 bits
+    lose beside 2^15."""
+    rng = np.random.default_rng(T + n)
+    sign = rng.choice([-1.0, 1.0], size=(T, n))
+    dy = rng.integers(-3, 4, size=(T, n)) * 2.0 ** -10
+    dy[0], dy[-1] = 2.0 ** 15, -(2.0 ** 15) * sign[0] * sign[-1]
+    moe = _moe()
+    to = lambda a, t: torch.from_numpy(a.astype(np.float32)).to(t).cuda()  # noqa: E731
+    w = torch.ones(n, device="cuda")
+    _, _, dw = moe.moe_rmsnorm_backward(to(dy, torch.bfloat16), to(sign, dtype), w, eps=0.0)
+    off = int((dw.cpu().double().numpy() != (dy * sign).sum(axis=0)).sum())
+    assert off == 0, f"{off} of {n}"
