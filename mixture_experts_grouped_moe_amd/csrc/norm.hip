@@ -372,7 +372,7 @@ __global__ __launch_bounds__(THREADS, kNormBwdWaves) void norm_backward_kernel(N
     }
     norm_reduce2<LANES>(s, t, red[turn]);
     const float r = norm_rstd(s, p.n, p.eps);
-    const float c = r * r * (t / p.n);
+    const float c = r * (r * (t / p.n));  // (r r would pass fp32's range where rows are below 2^-64)
     float v[V][8];
 #pragma unroll
     for (int j = 0; j < V; ++j) {

@@ -78,3 +78,22 @@ def test_dweight_of_rows_that_cancel(T, n, dtype):
     _, _, dw = moe.moe_rmsnorm_backward(to(dy, torch.bfloat16), to(sign, dtype), w, eps=0.0)
     off = int((dw.cpu().double().numpy() != (dy * sign).sum(axis=0)).sum())
     assert off == 0, f"{off} of {n}"
+
+
+@pytest.mark.parametrize("power", [-74, -66, -63, 30, 55])
+@pytest.mark.parametrize("n", [64, 1040, 9216])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradient_of_small_and_large_rows(power, n, dtype):
+    """With eps = 0 the gradient of rows 2^power times as large is 2^-power
+    times as large, and dweight is the same; rows of +-1 lose nothing to fp32's
+    subnormal numbers in the sums."""
+    rng, moe = np.random.default_rng(n), _moe()
+    v = torch.from_numpy(rng.choice([-1.0, 1.0], size=(5, n))).to(dtype).cuda()
+    dy = torch.from_numpy(rng.standard_normal((5, n))).to(torch.bfloat16).cuda()
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(n)).float().cuda()
+    dx, dres, dw = moe.moe_rmsnorm_backward(dy, v, w, eps=0.0)
+    got = moe.moe_rmsnorm_backward(dy, v * 2.0 ** power, w, eps=0.0)
+    assert torch.isfinite(dres).all()
+    for a, b in zip(got, (dx, dres, dw)):
+        b = b if b is dw else (b.double() * 2.0 ** -power).to(b.dtype)
+        assert int((a != b).sum()) == 0
