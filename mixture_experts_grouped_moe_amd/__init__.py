@@ -611,6 +611,15 @@ def moe_wgrad(x, grad, routing, num_tokens, top_k, num_experts, out=None, stream
 _warned_padding = False
 
 
+def _layer_adapter(adapter):
+    """A layer's (a, b, scale), or None."""
+    if adapter is None:
+        return None
+    if not isinstance(adapter, (tuple, list)) or len(adapter) != 3:
+        raise ValueError("adapter must be (a, b, scale), scale a tensor or None")
+    return adapter
+
+
 def moe_w4a16_layer(x, topk_ids, topk_w, w1, s1, w2, s2, b1=None, b2=None, num_tokens=None,
                     pad_token_dim=False, stream=None, adapter=None):
     """The W4A16 MXFP4 expert layer: align -> gate+up GEMM with SwiGLU ->
@@ -629,6 +638,7 @@ def moe_w4a16_layer(x, topk_ids, topk_w, w1, s1, w2, s2, b1=None, b2=None, num_t
     adapters of the experts' down projections, added to its output by moe_lora.
     """
     global _warned_padding
+    adapter = _layer_adapter(adapter)
     T = x.shape[0] if num_tokens is None else int(num_tokens)
     Tr = T
     if pad_token_dim:
@@ -661,6 +671,7 @@ def moe_relu2_layer(x, topk_ids, topk_w, w1, w2, b1=None, b2=None, num_tokens=No
     weights (rows layout [E, N, H] and [E, H, N], or PackedWeights). Token
     counts up to moe_decode_max_tokens() run the decode GEMM. adapter: as in
     moe_w4a16_layer. Returns y bf16 [num_tokens, H]."""
+    adapter = _layer_adapter(adapter)
     T = x.shape[0] if num_tokens is None else int(num_tokens)
     k = topk_ids.shape[1]
     E = w1.num_experts if isinstance(w1, PackedWeights) else w1.shape[0]

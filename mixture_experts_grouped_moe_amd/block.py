@@ -192,8 +192,11 @@ def moe_rmsnorm(x, weight, residual=None, eps=1e-6, p=0.0, rng=None, quant=None,
     where it would be x); q uint8 E4M3 codes [T, n] with scales uint8 E8M0
     [T, n / 32] or fp32 [T] (None without quant). `out` may give the four, None
     for what is not wanted; its sum may be residual."""
+    kind = _QUANTS.get(quant)
+    if kind is None:
+        raise ValueError(f'quant must be None, "none", "mxfp8" or "per_token", got {quant!r}')
     T, n, xld = _mat(x, "x", torch.bfloat16)
-    kind, wd = _QUANTS[quant], _wide(weight, "weight")
+    wd = _wide(weight, "weight")
     _flat(weight, "weight", weight.dtype, (n,))
     rd, rld, res_p = MOE_BF16, 0, 0
     if residual is not None:
