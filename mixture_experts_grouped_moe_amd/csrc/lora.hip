@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_up_few_kernel(LoraParams p)
   using Few = LoraFew<RC>;
   __shared__ __attribute__((aligned(16))) uint16_t hs[3][16][Few::kLd];
   const int wave = threadIdx.x / 64, m16 = threadIdx.x % 16;
-  const int b = p.block0 + blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
+  const int b = blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
   const int g = p.groups[b];
   const int row0 = blockIdx.y * 16, rows = min(16, p.bm - row0);
   const int64_t pos0 = (int64_t)b * p.bm + row0;
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(512) void lora_both_kernel(LoraParams p) {
   __shared__ f32x4_t red[4][RT][64];
   __shared__ __attribute__((aligned(16))) uint16_t hs[3][16][Few::kLd];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, m16 = lane % 16;
-  const int b = p.block0 + blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
+  const int b = blockIdx.x / p.n_splits, sp = blockIdx.x % p.n_splits;
   const int g = p.groups[b];
   const int row0 = blockIdx.y * 16, rows = min(16, p.bm - row0);
   const int32_t* ids = p.sorted + (int64_t)b * p.bm + row0;
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(kLoraThreads, lora_up_waves(RC, PARTS)) void lora_u
   const int run = blockIdx.x / p.n_splits, n0 = (blockIdx.x % p.n_splits * 4 + wave) * kCols;
   if (n0 >= p.N) return;
   const int shift = p.bm <= 16 ? 0 : p.bm / 32;  // log2 of a block's tiles (1, 2 or 4)
-  const int t0 = (p.block0 << shift) + run * p.run_tiles;  // below 2^31 (as max_blocks * bm)
+  const int t0 = run * p.run_tiles;                  // below 2^31 (as max_blocks * bm)
   const int tiles = min(p.run_tiles, (p.max_blocks << shift) - t0);
   const bool in = n0 + NT * m16 < p.N;
   const int pieces = p.R / 8;
@@ -539,31 +539,25 @@ LoraSizes lora_sizes(int32_t R, int64_t K, int32_t bm, int64_t max_blocks) {
   return z;
 }
 
-// Launches over all blocks, at most kLoraMaxGrid workgroups at a time (a grid
-// holds fewer than 2^32 threads).
-constexpr int64_t kLoraMaxGrid = 1 << 21;
-
-template <class F>
-static hipError_t lora_blocks(LoraParams p, int per_block, F launch) {
-  const int64_t per = kLoraMaxGrid / per_block > 0 ? kLoraMaxGrid / per_block : 1;
-  for (int64_t b = 0; b < p.max_blocks; b += per) {
-    p.block0 = (int32_t)b;
-    launch(p, (uint32_t)((p.max_blocks - b < per ? p.max_blocks - b : per) * per_block));
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
-  return hipSuccess;
-}
-
 hipError_t launch_lora_down(const LoraParams& p, hipStream_t stream) {
   return lora_rank(p.R, [&](auto rank) {
     constexpr int RT = (decltype(rank)::value + 1) / 2, MOST = RT == 8 ? 2 : 4;
     auto go = [&](auto mt) {
       constexpr int MT = decltype(mt)::value;
       const int y = p.bm <= 16 * MT ? 1 : p.bm / (16 * MT);
-      return lora_blocks(p, p.splits, [&](const LoraParams& q, uint32_t grid) {
-        hipLaunchKernelGGL((lora_down_kernel<RT, MT>), dim3(grid, y), dim3(kLoraThreads), 0, stream, q);
-      });
+      // (a grid holds fewer than 2^32 threads)
+      constexpr int64_t kMost = 1 << 21;
+      const int64_t blocks = kMost / p.splits;
+      LoraParams q = p;
+      for (int64_t b = 0; b < p.max_blocks; b += blocks) {
+        q.block0 = (int32_t)b;
+        const int64_t n = p.max_blocks - b < blocks ? p.max_blocks - b : blocks;
+        hipLaunchKernelGGL((lora_down_kernel<RT, MT>), dim3((uint32_t)(n * p.splits), y), dim3(kLoraThreads), 0, stream,
+                           q);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+      }
+      return hipSuccess;
     };
     if (p.bm <= 16) return go(std::integral_constant<int, 1>{});
     if (p.bm == 32) return go(std::integral_constant<int, 2>{});
@@ -582,7 +576,8 @@ hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream)
   LoraParams p = p0;
   p.n_splits = (p.N + 511) / 512;
   const int per = p.bm <= 16 ? 1 : p.bm / 16;
-  const int64_t all = (int64_t)p.max_blocks * per * p.n_splits;  // tiles of 16 slots and 512 columns
+  const int64_t tiles = (int64_t)p.max_blocks * per, all = tiles * p.n_splits;  // of 16 slots; and 512 columns
+  if (all == 0) return hipSuccess;
   // About 12 workgroups a CU: many more than run at once, so that they end together
   // (32768 slots of 128 groups, 5760 columns: 180 us for the whole call, 184 at 6
   // a CU), of whole blocks, whose slots are one group's (187 with 9 tiles in place
@@ -591,35 +586,31 @@ hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream)
   // tiles; 4096 slots of rank 64: 35.8 us at 4, 39 at 2).
   const int64_t share = all / (12 * kLoraCUs);
   const int64_t few = all / (2 * kLoraCUs) < 4 ? all / (2 * kLoraCUs) : 4;
-  p.run_tiles = (int32_t)(share >= 8 ? share / per * per : share > 4 ? share : few > 1 ? few : 1);
+  const int64_t run = share >= 8 ? share / per * per : share > 4 ? share : few > 1 ? few : 1;
+  p.run_tiles = (int32_t)(run < tiles ? run : tiles);
+  // (below 2^16 workgroups: 5 tiles for each of those 12 a CU where runs are short,
+  // and a run that is not whole for each of at most 2^15 parts of the columns)
+  const int64_t grid = (tiles + p.run_tiles - 1) / p.run_tiles * p.n_splits;
   return lora_rank(p.R, [&](auto rank) {
     constexpr int RC = decltype(rank)::value;
-    // launches of whole blocks and whole runs
-    LoraParams q = p;
-    const int64_t runs = ((int64_t)p.max_blocks * per + p.run_tiles - 1) / p.run_tiles;
-    const int64_t most = kLoraMaxGrid / p.n_splits / per * per > 0 ? kLoraMaxGrid / p.n_splits / per * per : per;
-    for (int64_t r = 0; r < runs; r += most) {
-      q.block0 = (int32_t)(r * p.run_tiles / per);
-      const int64_t n = runs - r < most ? runs - r : most;
-      auto kernel = !turned    ? lora_up_kernel<RC, false, false>
-                    : q.scaled ? lora_up_kernel<RC, true, false>
-                               : lora_up_kernel<RC, true, true>;
-      hipLaunchKernelGGL(kernel, dim3((uint32_t)(n * p.n_splits)), dim3(kLoraThreads), 0, stream, q);
-      const hipError_t err = hipGetLastError();
-      if (err != hipSuccess) return err;
-    }
-    return hipSuccess;
+    auto kernel = !turned    ? lora_up_kernel<RC, false, false>
+                  : p.scaled ? lora_up_kernel<RC, true, false>
+                             : lora_up_kernel<RC, true, true>;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(kLoraThreads), 0, stream, p);
+    return hipGetLastError();
   });
 }
 
-// The grid of the kernels for few slots: parts of N of at least `least` columns.
+// The grid of the kernels for few slots: parts of N of at least `least` columns,
+// below 1024 workgroups (lora_few: 64 tiles at most).
 template <class F>
 static hipError_t lora_few_grid(LoraParams p, int least, F launch) {
   const int y = p.bm <= 16 ? 1 : p.bm / 16;
   const int64_t tiles = (int64_t)p.max_blocks * y, most = (p.N + least - 1) / least;
   const int64_t want = (2 * kLoraCUs + tiles - 1) / (tiles > 0 ? tiles : 1);
   p.n_splits = (int32_t)(want < most ? want : most);
-  return lora_blocks(p, p.n_splits, [&](const LoraParams& q, uint32_t grid) { launch(q, dim3(grid, y)); });
+  launch(p, dim3(p.max_blocks * p.n_splits, y));
+  return hipGetLastError();
 }
 
 hipError_t launch_lora_up_few(const LoraParams& p, hipStream_t stream) {

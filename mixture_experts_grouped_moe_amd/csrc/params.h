@@ -151,7 +151,7 @@ struct NormParams {
 struct LoraParams {
   int32_t S, G, R, K, N;
   int32_t bm, max_blocks;
-  int32_t block0;  // the launch's first block
+  int32_t block0;  // of a launch of `down`: its first block
   const int32_t* sorted;
   const int32_t* groups;
   const float* scale;
