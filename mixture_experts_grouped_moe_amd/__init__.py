@@ -251,7 +251,8 @@ def moe_align(topk_ids, num_experts, block_m, num_tokens=None, out=None, stream=
 
     topk_ids: int32 [T, top_k] on the device. Returns (sorted_token_ids,
     expert_ids, num_tokens_post_pad) as int32 device tensors, a Routing; `out`
-    may give preallocated ones. num_tokens (default T) routes only the first rows.
+    may give preallocated ones (an earlier Routing, which then stands for the new
+    slots). num_tokens (default T) routes only the first rows.
     """
     _need(topk_ids, "topk_ids", torch.int32, 2)
     if not topk_ids.is_contiguous():
@@ -273,7 +274,7 @@ def moe_align(topk_ids, num_experts, block_m, num_tokens=None, out=None, stream=
     _check(lib.moe_align(_ptr(topk_ids), T, k, int(num_experts), int(block_m),
                          _ptr(sorted_ids), _ptr(expert_ids), _ptr(post_pad), max_blocks,
                          _stream(stream)))
-    routing = Routing((sorted_ids, expert_ids, post_pad))
+    routing = out if isinstance(out, Routing) else Routing((sorted_ids, expert_ids, post_pad))
     routing.num_slots = T * k
     return routing
 

@@ -100,3 +100,20 @@ def test_align_says_what_it_was_made_for():
     out = tuple(torch.empty_like(t) for t in routing)
     again = moe.moe_align(ids, 4, 16, num_tokens=5, out=out)
     assert again.num_slots == 10 and all(a is b for a, b in zip(again, out))
+
+
+def test_align_into_an_earlier_routing():
+    """A list aligned again for fewer slots into the same Routing: its padding holds the new number."""
+    moe = _moe()
+    case = Case(60, 3, 16, 64, 48, 1, 16, seed=2, free=0.0)
+    ids = case.ids[:, None].contiguous().cuda()
+    routing = moe.moe_align(ids, 3, 16)
+    assert moe.moe_align(ids, 3, 16, num_tokens=37, out=routing) is routing and routing.num_slots == 37
+    c = case.c.clone()
+    moe.moe_lora(c, case.x, case.a, case.b, routing, case.scale)
+    want = moe.moe_lora(case.c[:37].clone(), case.x[:37], case.a, case.b, moe.moe_align(ids[:37], 3, 16), case.scale)
+    # (the longer list may split K otherwise: two sums of K + R + 4 = 84 roundings of
+    # magnitudes below 32 in all, 2^-12, and a half step of bf16 each)
+    d = (c[:37].float() - want.float()).abs()
+    assert (d <= 2.0 ** -7 * want.float().abs() + 2.0 ** -12).all()
+    assert torch.equal(c[37:], case.c[37:])
