@@ -166,7 +166,9 @@ int64_t moe_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t n);
  * order of the sums depends on the sizes alone: repeated calls give equal bits.
  *
  * With groups = experts, moe_grouped_gemm's block list serves the adapters too
- * (block_m 8 and 64 are its block sizes). */
+ * (block_m 8 and 64 are its block sizes). An adapter of each expert for several
+ * requests is a group = adapter * experts + expert: 1024 groups at most, so 8 such
+ * adapters of 128 experts and 4 of 256; more of them take several lists and calls. */
 typedef struct {
   int64_t num_slots;
   int32_t num_groups;
@@ -225,7 +227,7 @@ int64_t moe_lora_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t 
  * where x_row_div > 1, moe_combine_routed adds the rows of a token. dy passes
  * through to the shared projection unchanged. da and db are written for every
  * group, zeros for one without slots; both NULL: not computed (h and x are then
- * not read). The products take dh and h as three bf16 terms (all of fp32's bits). Rows of dx of slots
+ * not read, but x is checked all the same). The products take dh and h as three bf16 terms (all of fp32's bits). Rows of dx of slots
  * in no block are left as they were. */
 typedef struct {
   int64_t num_slots;

@@ -10,7 +10,8 @@ MXFP8 activations, with dropout of the layer's output:
     dx, dres, dweight = moe_rmsnorm_backward(dy, r, weight, dsum=dr, p=p, rng=rng)
 
 Adapters of many requests beside a projection, one block list for all
-projections of the batch (group = adapter; or adapter * E + expert):
+projections of the batch (group = adapter; or adapter * E + expert; up to 1024
+groups a list):
 
     routing = moe_align(adapter_of_slot, G, moe_lora_block_m(S, G))
     c = moe_grouped_gemm(...)                                  # or any shared projection

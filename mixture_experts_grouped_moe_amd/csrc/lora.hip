@@ -14,10 +14,10 @@
 //
 // Measured (kernel times): 8192 slots of 8 groups, K = 7168, N = 4096, rank 32:
 // `down` 31 us (3.8 TB/s: a group's A is read again by each block, beside the
-// rows), `join` 4.9, `up` 33 (3.9 TB/s). 32768 slots of 128 groups, four to a row
-// of 2880, N = 5760, rank 16: `down` 37 (5.3 TB/s), `up` 143 (730 MB, 5.1 TB/s;
-// the rows alone read and written back reach 4.7). 28 slots of 16 groups, K =
-// 2048, N = 1856, rank 16: 6.7, latency: ids, then rows and A, then the stores.
+// rows), `join` 4.8, `up` 34 (3.7 TB/s). 32768 slots of 128 groups, four to a row
+// of 2880, N = 5760, rank 16: `down` 36 (5.5 TB/s), `up` 156 (730 MB, 4.7 TB/s, what
+// the rows alone read and written back reach). 28 slots of 16 groups, K = 2048,
+// N = 1856, rank 16: 6.8, latency: ids, then rows and A, then the stores.
 #include <type_traits>
 
 #include "lora_util.h"
@@ -505,13 +505,13 @@ __global__ __launch_bounds__(kLoraThreads, lora_up_waves(RC, PARTS)) void lora_u
 // ------------------------------------------------------------------ launch
 
 // Whether the small `up` serves: up to 64 tiles of 16 slots. (28 slots of 16
-// groups, 1856 columns, rank 16: 6.6 us for the whole call, 8.2 through `up`;
-// 256 slots of 32 groups, 7168 columns: 13.1, and 16.3 us with `join` and `up`.)
+// groups, 1856 columns, rank 16: 6.5 us for the whole call, 9.5 through `up`;
+// 256 slots of 32 groups, 7168 columns: 13.2, and 14.9 us with `join` and `up`.)
 static bool lora_few(int64_t max_blocks, int bm) { return max_blocks * (bm < 16 ? 1 : bm / 16) <= 64; }
 
 // Parts of K: a workgroup for each CU, at least 256 columns and at most 32 parts.
-// (8192 slots, 8 groups, K = 7168, rank 32: 68 us for the whole call at 2 parts,
-// 75 at 3, 70 at 4, 79 at 1; 7 slots of 7 groups, rank 128: 15 us at 28 parts, 25
+// (8192 slots, 8 groups, K = 7168, rank 32: 69 us for the whole call at 2 parts,
+// 76 at 3, 70 at 4, 79 at 1; 7 slots of 7 groups, rank 128: 15 us at 28 parts, 25
 // at 8.)
 int lora_k_splits(int64_t max_blocks, int64_t k) {
   const int64_t want = (kLoraCUs + max_blocks - 1) / (max_blocks > 0 ? max_blocks : 1);
@@ -524,7 +524,9 @@ int lora_k_splits(int64_t max_blocks, int64_t k) {
 // which every workgroup of a tile reads. (28 slots of 16 groups, K = 2048, rank
 // 16: 6.4 us, 6.5 in two launches, and 8 us of the host's time in place of 12;
 // one slot of 2048: 5.8 and 6.3; K = 2880, rank 16: 10.2 and 8.0 us, K = 7168,
-// rank 8: 11.5 and 7.5.)
+// rank 8: 11.5 and 7.5. Past the border, at K R = 36864 to 46080 and ranks 8 to 32,
+// one launch saves up to 1.0 us or costs up to 0.5 for one slot, saves up to 0.6 or
+// costs up to 2.2 for 28 slots of 16 groups, and costs 0.2 to 5.4 for 200 of 8.)
 static bool lora_both(int64_t max_blocks, int bm, int R, int64_t K) {
   return lora_few(max_blocks, bm) && R <= 32 && K * R <= 32768;
 }
@@ -579,11 +581,11 @@ hipError_t launch_lora_up(const LoraParams& p0, bool turned, hipStream_t stream)
   const int64_t tiles = (int64_t)p.max_blocks * per, all = tiles * p.n_splits;  // of 16 slots; and 512 columns
   if (all == 0) return hipSuccess;
   // About 12 workgroups a CU: many more than run at once, so that they end together
-  // (32768 slots of 128 groups, 5760 columns: 180 us for the whole call, 184 at 6
-  // a CU), of whole blocks, whose slots are one group's (187 with 9 tiles in place
+  // (32768 slots of 128 groups, 5760 columns: 188 us for the whole call, 190 at 6
+  // a CU), of whole blocks, whose slots are one group's (190 with 9 tiles in place
   // of 8). With fewer tiles 4 a workgroup, which reads its columns of B for them,
-  // or what gives 512 workgroups (gradients of 1333 slots: 28.5 us, 31.6 at 4
-  // tiles; 4096 slots of rank 64: 35.8 us at 4, 39 at 2).
+  // or what gives 512 workgroups (gradients of 1333 slots: 23.6 us, 27.0 at 4
+  // tiles; 4096 slots of rank 64: 36 us at 4, 40 at 2).
   const int64_t share = all / (12 * kLoraCUs);
   const int64_t few = all / (2 * kLoraCUs) < 4 ? all / (2 * kLoraCUs) : 4;
   const int64_t run = share >= 8 ? share / per * per : share > 4 ? share : few > 1 ? few : 1;

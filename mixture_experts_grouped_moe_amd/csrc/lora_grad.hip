@@ -8,10 +8,11 @@
 // every time); a group of one segment writes its gradient directly.
 //
 // Measured (kernel times): 32768 slots of 128 groups, K = 2880 (a row serves four),
-// N = 5760, rank 16: the table 9 us, dy 106 (383 MB read and 69 written, 4.3 TB/s;
-// gathered rows of this width are read at 4.5 to 4.9), h's join 7.2, dx 71 (5.4
-// TB/s), x 32 (172 MB moved, 5.4 TB/s), the gradients' join 4.9. 1333 slots of 3 groups,
-// 2688 x 1856, rank 8: four launches of 3.5 to 7 us each, all latency.
+// N = 5760, rank 16: the table 9 us, dy 104 (383 MB read and 69 written, 4.3 TB/s;
+// gathered rows of this width are read at 4.5 to 4.9), h's join 6.8, dx 80 (4.8
+// TB/s), x 32 (172 MB moved, 5.4 TB/s), the gradients' join 5.0. 1333 slots of 3 groups,
+// 2688 x 1856, rank 8: four launches of 4 to 7 us each, all latency (dx and x,
+// which both wait for dy alone, run one after the other).
 #include <type_traits>
 
 #include "lora_util.h"
