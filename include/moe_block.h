@@ -206,8 +206,7 @@ typedef struct {
  * [0, num_groups) and a slot id outside [0, num_slots) are skipped; no slot may
  * stand in the list twice, so num_slots is at most the number that the list was
  * aligned for, which its padding places hold, however many rows c, x and h have
- * behind those. c, h and workspace must not overlap each other or an
- * input. */
+ * behind those. c, h and workspace must not overlap each other or an input. */
 moe_status moe_lora(const moe_lora_args* args, moe_stream_t stream);
 
 /* The block size that suits num_slots slots over num_groups groups: 16, or 64
@@ -227,8 +226,9 @@ int64_t moe_lora_workspace_bytes(int64_t num_slots, int32_t num_groups, int32_t 
  * where x_row_div > 1, moe_combine_routed adds the rows of a token. dy passes
  * through to the shared projection unchanged. da and db are written for every
  * group, zeros for one without slots; both NULL: not computed (h and x are then
- * not read, but x is checked all the same). The products take dh and h as three bf16 terms (all of fp32's bits). Rows of dx of slots
- * in no block are left as they were. */
+ * not read, but x is checked all the same). The products take dh and h as three
+ * bf16 terms (all of fp32's bits). Rows of dx of slots in no block are left as
+ * they were. */
 typedef struct {
   int64_t num_slots;
   int32_t num_groups;

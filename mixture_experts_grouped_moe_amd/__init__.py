@@ -660,9 +660,9 @@ def moe_w4a16_layer(x, topk_ids, topk_w, w1, s1, w2, s2, b1=None, b2=None, num_t
     c2 = moe_grouped_gemm(h, w2, "e2m1x2", routing, Tr, k, E, a_row_div=1, w_scale=s2, bias=b2,
                           stream=stream)
     if adapter is not None:
-        if Tr != T:  # moe_lora's sums are split by the length of its list: the real rows' own keeps their bits
-            routing = moe_align(topk_ids, E, moe_gemm_block_m("e2m1x2", T), num_tokens=T, stream=stream)
-        moe_lora(c2, h, adapter[0], adapter[1], routing, scale=adapter[2], stream=stream)
+        # moe_lora's sums are split by the length of its list: the real rows' own keeps their bits
+        real = routing if Tr == T else moe_align(topk_ids, E, moe_gemm_block_m("e2m1x2", T), num_tokens=T, stream=stream)
+        moe_lora(c2, h, adapter[0], adapter[1], real, scale=adapter[2], stream=stream)
     return moe_combine(c2, topk_w, k, num_tokens=T, stream=stream)
 
 

@@ -7,11 +7,11 @@
 // columns each, neighbouring threads on neighbouring pieces), so the sum of
 // squares, the row's largest magnitude and all outputs come from one pass over
 // memory; workgroups take rows in turn with the next row's loads in flight.
-// 4096 x 7168 with MXFP8: 49 us, 5.4 TB/s (a large copy reaches 5.1); 6554 x 2880
-// of an fp32 stream with dropout: 38 us, 5.9 TB/s; 7 rows of 2688 with per-token
-// codes: 4.0 to 4.7 us, latency; gradient of 16384 x 7168: 166 us, 5.65 TB/s, and 5
-// for dweight's last sums; of 333 x 2880: 7.5 and 3.9 us. One row a workgroup without the loads
-// ahead: 55 us the first, 204 the last but one.
+// 4096 x 7168 with MXFP8: 49 us, 5.4 TB/s (a copy of as many bytes reaches 5.4);
+// 6554 x 2880 of an fp32 stream with dropout: 38 us, 5.9 TB/s; 7 rows of 2688 with
+// per-token codes: 4.0 to 4.7 us, latency; gradient of 16384 x 7168: 166 us, 5.65
+// TB/s, and 5 for dweight's last sums; of 333 x 2880: 7.5 and 3.9 us. One row a
+// workgroup without the loads ahead: 55 us the first, 204 the last but one.
 #include <type_traits>
 
 #include "dropout_util.h"
